@@ -1,13 +1,17 @@
 /*
  * sa.h -- C ABI of the GB300 KV-cache attention library (libsa.so).
  *
- * Eight operations, all computed on the GPU on the caller's stream:
+ * Twelve operations, all computed on the GPU on the caller's stream:
  *
  *   validate_indices     index-row validation with a device error word
  *   build_present_kv     present K/V = past ++ current (concat or in-place append)
  *   sparse_attn_decode   selected-token attention (dense or FP8 hybrid cache)
  *   attn_prefill         dense (causal) prefill with softcap, present K/V out
- *   paged_attn_decode    causal decode over a 16-token page table
+ *   paged_attn_decode    causal decode over a page table (element or FP8 pages)
+ *   rotary_embed         rotary positions of queries and keys
+ *   paged_kv_write       new tokens' K/V, rotated and quantised, into their pages
+ *   paged_kv_read        a context read back from its pages into packed rows
+ *   attn_prefill_packed  causal prefill of packed sequences of different lengths
  *   sparse_index_select  ratio-4 index scoring + top-k (produces selected indices)
  *   csa_ratio4_attention compressed sparse attention: window store + records + sink
  *   csa_*_compress       the compression stages that produce the CSA records
@@ -74,6 +78,13 @@ extern "C" {
 #define SA_F16 1
 #define SA_BF16 2
 #define SA_FP8_E4M3_B64 3 /* hybrid record: blocks of [E8M0, 64 x E4M3FN] + bf16 tail */
+/* page format of a quantised pool (pool_format; 0 = pages of plain elements).
+ * A pool is uint8 [num_pages, Hkv, page_tokens * (D + 1)]: per page and KV head
+ * first page_tokens rows of D E4M3FN codes, then one E8M0 byte per row; an
+ * element is code * 2^(byte - 127), and every element of a row whose byte is
+ * 255 is NaN.  D is 64, 128 or 256 and page_tokens a multiple of 16, so that
+ * a page of one head is one contiguous, 16-byte aligned piece. */
+#define SA_FP8_E4M3_PAGE 4
 
 /* ---- index-row status codes (row_status bytes; OR-ed into err_word) --- */
 #define SA_IDX_BELOW_SENTINEL 1  /* a value below -1                          */
@@ -90,6 +101,10 @@ extern "C" {
                                     past the valid records (skipped)             */
 #define SA_ERRBIT_COMPRESS 4096  /* csa_*_compress: a record met a non-finite
                                     value and was stored as zeros                */
+#define SA_ERRBIT_SEQ 8192       /* packed sequences: the starts decrease or leave
+                                    the tensor                                   */
+#define SA_ERRBIT_NONFINITE 16384 /* paged_kv_write: a row to quantise held a NaN
+                                    or an infinity and is stored as NaN          */
 
 /* ---- sa_sparse_params.options bits ------------------------------------- */
 #define SA_OPT_ROW_COPIES 1u     /* dense f16/bf16 caches: fetch each K/V row with
@@ -573,6 +588,11 @@ int attn_prefill(const sa_prefill_params* p, void* stream);
  * SA_ERRBIT_PAGE (err_word nullable) and is never dereferenced.
  * dtype SA_F16 / SA_BF16 / SA_F32; scale 0 means 1/sqrt(D).  Workspace rules
  * as for sparse_attn_decode.
+ * pool_format SA_FP8_E4M3_PAGE: quantised pages (q and y SA_F16 or SA_BF16, D
+ * 64 / 128 / 256, page_tokens a multiple of 16, pools 16-byte aligned, options
+ * 0); k_new / v_new are quantised as paged_kv_write does.  The codes' values
+ * enter the products exactly and the scales in fp32.  E4M3's NaN codes, which
+ * paged_kv_write never stores, read as +-480 here.
  */
 typedef struct {
   const void* q;
@@ -587,7 +607,7 @@ typedef struct {
   uint32_t options;     /* 0, or SA_OPT_ROW_COPIES (pages fetched row by row) */
   int64_t B, Hq, Hkv, D, page_tokens, max_pages, num_pages;
   float scale;
-  float pad2_;
+  int32_t pool_format;  /* 0: elements of dtype, or SA_FP8_E4M3_PAGE */
   uint32_t* err_word;
   void* workspace;
   size_t workspace_bytes;
@@ -595,6 +615,160 @@ typedef struct {
 
 size_t paged_attn_decode_workspace(const sa_paged_params* p);
 int paged_attn_decode(const sa_paged_params* p, void* stream);
+
+/*
+ * Rotary positions -- sa_rope_table fills a table of angles from a
+ * configuration (host only, nothing is launched), which rotary_embed and
+ * paged_kv_write take.  Pair i (of rotary_dim / 2) turns by the angle
+ * position * f_i, with f_i, in 64 bits,
+ *   SA_ROPE_NONE    base^(-2i / rotary_dim)
+ *   SA_ROPE_LINEAR  that / factor
+ *   SA_ROPE_NTK     the same with base * factor^(rotary_dim / (rotary_dim - 2))
+ *   SA_ROPE_RAMP    f (g + (1 - g) / factor), f the plain frequency and
+ *                   g = clamp((r - ramp_low) / (ramp_high - ramp_low), 0, 1) of the
+ *                   pair's turns r = original_len f / (2 pi) over the original
+ *                   context: fast pairs keep their frequency, slow ones take the
+ *                   linear scaling
+ *   SA_ROPE_FREQS   inv_freq[i], given by the caller
+ * and (u, v) becomes mscale * (u cos - v sin, u sin + v cos).  The pair is
+ * dims (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved; dims from
+ * rotary_dim on pass unchanged.  The table keeps f_i as a 64-bit fraction of a
+ * turn, so position * f_i modulo one turn is exact integer arithmetic at any
+ * position (int32 or int64, negative ones too).
+ * rotary_dim: even, 2 .. 256.  mscale 0 means 1.  Returns SA_OK, SA_ERR_NULL,
+ * SA_ERR_SHAPE (a size or a parameter out of its range: base <= 0, factor <= 0,
+ * ramp_high <= ramp_low, original_len <= 0 where it is used, a frequency that
+ * is not finite) or SA_ERR_UNSUPPORTED (an unknown scaling).
+ */
+#define SA_ROPE_NONE 0
+#define SA_ROPE_LINEAR 1
+#define SA_ROPE_NTK 2
+#define SA_ROPE_RAMP 3
+#define SA_ROPE_FREQS 4
+#define SA_ROPE_MAX_PAIRS 128
+typedef struct {
+  int32_t rotary_dim, interleaved, scaling;
+  float mscale;
+  double base, factor, original_len, ramp_low, ramp_high;
+  const double* inv_freq; /* SA_ROPE_FREQS: host [rotary_dim / 2] */
+} sa_rope_config;
+typedef struct {
+  int32_t rotary_dim, interleaved;
+  float mscale;
+  int32_t reserved_; /* 0 */
+  uint64_t turns[SA_ROPE_MAX_PAIRS]; /* f_i / (2 pi) * 2^64 modulo 2^64 */
+} sa_rope;
+int sa_rope_table(const sa_rope_config* c, sa_rope* out);
+
+/*
+ * rotary_embed -- rotary positions of q [B, S, Hq, D] and, when k != NULL,
+ * k [B, S, Hk, D], in one launch.  Tensors are given by their batch, token and
+ * head strides in elements (the D elements of a head are contiguous), so
+ * packed [T, H, D] tensors (B = 1), head-major [B, H, S, D] tensors and views
+ * into a fused projection all serve.  positions: device int32 or int64, token
+ * s of batch b at positions[b * pos_stride + s] (pos_stride 0: one row of S
+ * positions for every batch).  q_out / k_out may be the input itself (same
+ * pointer and strides); any other overlap is SA_ERR_OVERLAP.  dtype SA_F32,
+ * SA_F16 or SA_BF16; angles are reduced exactly, cos and sin and the rotation
+ * are fp32, rounded once.  S 0 is a call that does nothing.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const void* positions;
+  const sa_rope* rope; /* host */
+  int32_t dtype;
+  int32_t pos_is_i64;
+  int64_t B, S, Hq, Hk, D;
+  int64_t pos_stride;
+  int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3];
+} sa_rotary_params;
+int rotary_embed(const sa_rotary_params* p, void* stream);
+
+/*
+ * paged_kv_write / paged_kv_read -- packed rows of K and V to and from pages.
+ *
+ * k / v [T, Hkv, D] in dtype (SA_F32, SA_F16, SA_BF16), given by their token
+ * and head strides in elements.  Sequence b owns rows seq_start[b] ..
+ * seq_start[b + 1] - 1 (device int32 [B + 1], non-decreasing; rows behind the
+ * last sequence belong to nobody).  Pages as for paged_attn_decode.
+ *
+ * paged_kv_write: the n_b rows of sequence b are the last n_b tokens of its
+ * ctx_len[b]: row seq_start[b] + i is written at token ctx_len[b] - n_b + i.
+ * seq_start NULL means one row per sequence (T == B).  With rope != NULL, K is
+ * rotated at that token's position first, in fp32.  Pages of plain elements
+ * take dtype's own elements (an exact copy, or the rotated row rounded once);
+ * SA_FP8_E4M3_PAGE rows are quantised from the fp32 row: the exponent is the
+ * smallest e with max|row| / 2^e <= 448 (0 for a row of zeros, at least -127),
+ * the codes the nearest-even E4M3FN of x / 2^e.  A row that holds a NaN or an
+ * infinity is stored with scale byte 255 (reads as NaN) and sets
+ * SA_ERRBIT_NONFINITE.  Nothing else in the pools is touched.
+ *
+ * paged_kv_read: rows seq_start[b] + i receive token i of sequence b (its first
+ * n_b tokens); rope must be NULL.  The values are exact products rounded once
+ * to dtype.  Rows behind the last sequence stay as they are.
+ *
+ * A table entry outside [0, num_pages), a token outside [0, ctx_len[b]) or a
+ * ctx_len outside [0, max_pages * page_tokens] sets SA_ERRBIT_PAGE, starts that
+ * decrease or leave [0, T] set SA_ERRBIT_SEQ (err_word nullable); such rows are
+ * skipped, and no access leaves the tensors.  Two rows written to one slot (a
+ * page shared by two sequences) leave either row's bytes there.
+ * pool_format 0 (pages [num_pages, Hkv, page_tokens, D] of dtype) serves any D
+ * up to 1024; the rope then needs rotary_dim <= D.  No workspace.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  void* k_pool;
+  void* v_pool;
+  const int32_t* block_table; /* [B, max_pages] */
+  const int32_t* ctx_len;     /* [B] */
+  const int32_t* seq_start;   /* [B + 1] */
+  const sa_rope* rope;        /* host, nullable */
+  uint32_t* err_word;
+  int32_t dtype;
+  int32_t pool_format;
+  int64_t T, B, Hkv, D, page_tokens, max_pages, num_pages;
+  int64_t k_strides[2], v_strides[2]; /* token, head */
+} sa_kv_pages_params;
+int paged_kv_write(const sa_kv_pages_params* p, void* stream);
+int paged_kv_read(const sa_kv_pages_params* p, void* stream);
+
+/*
+ * attn_prefill_packed -- attn_prefill's attention over packed sequences of
+ * different lengths: q / y [Tq, Hq, D], k / v [Tk, Hkv, D] (GQA), given by
+ * their token and head strides in elements.  Sequence b has the query rows
+ * q_start[b] .. q_start[b + 1] - 1 and the key rows k_start[b] .. (device int32
+ * [B + 1], non-decreasing; k_start NULL: q_start).  With nq queries and nk
+ * keys, query i sees keys j <= i + nk - nq when causal (the ends are aligned:
+ * a chunk of a prompt sees the context before it), every key otherwise; a
+ * query that sees no key gives 0.  softcap as in attn_prefill, scale 0 means
+ * 1/sqrt(D).  Rows of y behind the last sequence stay as they are; rows of q,
+ * k and v outside the sequences may hold anything.
+ * dtype SA_F16 / SA_BF16 with D 64 or 128, a positive scale, Hq / Hkv <= 128
+ * and 16-byte aligned pointers and strides run on the tcgen05 tensor cores;
+ * other shapes (SA_F32, D a multiple of 4 up to 256) take a kernel on the fp32
+ * pipes.  Malformed starts set SA_ERRBIT_SEQ (err_word nullable), leave y
+ * unspecified and read or write nothing outside the tensors.  No workspace.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* y;
+  const int32_t* q_start;
+  const int32_t* k_start;
+  uint32_t* err_word;
+  int32_t dtype;
+  int32_t causal;
+  int64_t B, Tq, Tk, Hq, Hkv, D;
+  int64_t q_strides[2], k_strides[2], v_strides[2], y_strides[2]; /* token, head */
+  float scale;
+  float softcap;
+} sa_packed_params;
+int attn_prefill_packed(const sa_packed_params* p, void* stream);
 
 #ifdef __cplusplus
 }

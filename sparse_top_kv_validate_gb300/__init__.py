@@ -10,10 +10,11 @@ Entry points (same names as the C ABI):
     validate_indices, build_present_kv, sparse_attn_decode, attn_prefill,
     paged_attn_decode, sparse_index_select, csa_ratio4_attention,
     csa_ratio128_compress, csa_ratio4_main_compress, csa_ratio4_index_compress,
-    csa_pool_weight
+    csa_pool_weight, rotary_embed, paged_kv_write, paged_kv_read, attn_prefill_packed
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 import threading
@@ -35,6 +36,9 @@ __all__ = [
     "CsaParams", "csa_ratio4_attention", "csa_ratio4_attention_workspace", "ERRBIT_RECORD",
     "CompressParams", "csa_ratio128_compress", "csa_ratio4_main_compress",
     "csa_ratio4_index_compress", "csa_pool_weight", "ERRBIT_COMPRESS",
+    "RopeTable", "rope_table", "RotaryParams", "rotary_embed", "KvPagesParams", "paged_kv_write",
+    "paged_kv_read", "new_fp8_pool", "PackedParams", "attn_prefill_packed", "FP8_E4M3_PAGE",
+    "ERRBIT_SEQ", "ERRBIT_NONFINITE",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -51,6 +55,8 @@ SEL_TIE, SEL_NONFINITE = 1, 2
 ERRBIT_SEL_TIE, ERRBIT_SEL_NONFINITE = 512, 1024
 ERRBIT_RECORD = 2048
 ERRBIT_COMPRESS = 4096
+FP8_E4M3_PAGE = 4
+ERRBIT_SEQ, ERRBIT_NONFINITE = 8192, 16384
 
 _p = C.c_void_p
 _i64 = C.c_int64
@@ -93,7 +99,7 @@ class PagedParams(C.Structure):
         ("dtype", _i32), ("options", C.c_uint32),
         ("B", _i64), ("Hq", _i64), ("Hkv", _i64), ("D", _i64), ("page_tokens", _i64),
         ("max_pages", _i64), ("num_pages", _i64),
-        ("scale", C.c_float), ("pad2_", C.c_float),
+        ("scale", C.c_float), ("pool_format", _i32),
         ("err_word", _p), ("workspace", _p), ("workspace_bytes", C.c_size_t),
     ]
 
@@ -127,6 +133,50 @@ class CompressParams(C.Structure):
         ("logical", _p), ("err_word", _p),
         ("B", _i64), ("S", _i64), ("D", _i64), ("n_rope", _i64), ("rows", _i64),
         ("record_stride", _i64), ("total", _i64), ("reserved_", _i64),
+    ]
+
+
+class RopeTable(C.Structure):
+    """Angles of the rotary pairs (``sa_rope``), made by ``rope_table``."""
+    _fields_ = [("rotary_dim", _i32), ("interleaved", _i32), ("mscale", C.c_float),
+                ("reserved_", _i32), ("turns", C.c_uint64 * 128)]
+
+
+class _RopeConfig(C.Structure):
+    _fields_ = [("rotary_dim", _i32), ("interleaved", _i32), ("scaling", _i32),
+                ("mscale", C.c_float), ("base", C.c_double), ("factor", C.c_double),
+                ("original_len", C.c_double), ("ramp_low", C.c_double),
+                ("ramp_high", C.c_double), ("inv_freq", _p)]
+
+
+class RotaryParams(C.Structure):
+    _fields_ = [
+        ("q", _p), ("k", _p), ("q_out", _p), ("k_out", _p), ("positions", _p), ("rope", _p),
+        ("dtype", _i32), ("pos_is_i64", _i32),
+        ("B", _i64), ("S", _i64), ("Hq", _i64), ("Hk", _i64), ("D", _i64), ("pos_stride", _i64),
+        ("q_strides", _i64 * 3), ("k_strides", _i64 * 3), ("q_out_strides", _i64 * 3),
+        ("k_out_strides", _i64 * 3),
+    ]
+
+
+class KvPagesParams(C.Structure):
+    _fields_ = [
+        ("k", _p), ("v", _p), ("k_pool", _p), ("v_pool", _p), ("block_table", _p),
+        ("ctx_len", _p), ("seq_start", _p), ("rope", _p), ("err_word", _p),
+        ("dtype", _i32), ("pool_format", _i32),
+        ("T", _i64), ("B", _i64), ("Hkv", _i64), ("D", _i64), ("page_tokens", _i64),
+        ("max_pages", _i64), ("num_pages", _i64), ("k_strides", _i64 * 2),
+        ("v_strides", _i64 * 2),
+    ]
+
+
+class PackedParams(C.Structure):
+    _fields_ = [
+        ("q", _p), ("k", _p), ("v", _p), ("y", _p), ("q_start", _p), ("k_start", _p),
+        ("err_word", _p), ("dtype", _i32), ("causal", _i32),
+        ("B", _i64), ("Tq", _i64), ("Tk", _i64), ("Hq", _i64), ("Hkv", _i64), ("D", _i64),
+        ("q_strides", _i64 * 2), ("k_strides", _i64 * 2), ("v_strides", _i64 * 2),
+        ("y_strides", _i64 * 2), ("scale", C.c_float), ("softcap", C.c_float),
     ]
 
 
@@ -199,6 +249,14 @@ def load():
         L.paged_attn_decode_workspace.argtypes = [C.POINTER(PagedParams)]
         L.paged_attn_decode.restype = C.c_int
         L.paged_attn_decode.argtypes = [C.POINTER(PagedParams), _p]
+        L.sa_rope_table.restype = C.c_int
+        L.sa_rope_table.argtypes = [C.POINTER(_RopeConfig), C.POINTER(RopeTable)]
+        for name, params in (("rotary_embed", RotaryParams), ("paged_kv_write", KvPagesParams),
+                             ("paged_kv_read", KvPagesParams),
+                             ("attn_prefill_packed", PackedParams)):
+            fn = getattr(L, name)
+            fn.restype = C.c_int
+            fn.argtypes = [C.POINTER(params), _p]
         _lib = L
         return _lib
 
@@ -493,8 +551,12 @@ def _paged_params(q, k_pool, v_pool, block_table, ctx_len, y, k_new, v_new, scal
     p.k_new, p.v_new = _ptr(k_new), _ptr(v_new)
     p.block_table, p.ctx_len, p.y = block_table.data_ptr(), ctx_len.data_ptr(), _ptr(y)
     p.dtype = _dt(q)
+    if k_pool.dtype == torch.uint8:
+        p.pool_format, page_tokens = FP8_E4M3_PAGE, _fp8_page_tokens(k_pool, v_pool, D)
+    else:
+        page_tokens = k_pool.shape[2]
     p.B, p.Hq, p.Hkv, p.D = B, Hq, k_pool.shape[1], D
-    p.page_tokens, p.max_pages, p.num_pages = k_pool.shape[2], block_table.shape[1], k_pool.shape[0]
+    p.page_tokens, p.max_pages, p.num_pages = page_tokens, block_table.shape[1], k_pool.shape[0]
     p.scale = float(scale)
     p.err_word = _ptr(err_word)
     p.options = int(options)
@@ -510,9 +572,11 @@ def paged_attn_decode(q, k_pool, v_pool, block_table, ctx_len, *, k_new=None, v_
                       scale=0.0, err_word=None, y=None, workspace=None, stream=None,
                       options=0):
     """Paged causal decode: ``q [B,Hq,1,D]`` (or ``[B,Hq,D]``), pools
-    ``[num_pages,Hkv,page_tokens,D]``, ``block_table int32 [B,max_pages]``,
-    ``ctx_len int32 [B]``; optional ``k_new/v_new [B,Hkv,D]`` written at token
-    ``ctx_len-1`` first.  Returns ``y`` shaped like ``q``."""
+    ``[num_pages,Hkv,page_tokens,D]`` of q's dtype, or FP8 pools (uint8
+    ``[num_pages,Hkv,page_tokens*(D+1)]``, see ``new_fp8_pool``; q float16 or
+    bfloat16), ``block_table int32 [B,max_pages]``, ``ctx_len int32 [B]``;
+    optional ``k_new/v_new [B,Hkv,D]`` written (quantised for FP8 pools) at
+    token ``ctx_len-1`` first.  Returns ``y`` shaped like ``q``."""
     L = load()
     for n, t in (("q", q), ("k_pool", k_pool), ("v_pool", v_pool), ("block_table", block_table),
                  ("ctx_len", ctx_len), ("k_new", k_new), ("v_new", v_new),
@@ -520,6 +584,9 @@ def paged_attn_decode(q, k_pool, v_pool, block_table, ctx_len, *, k_new=None, v_
         _dev(t, n)
     if block_table.dtype != torch.int32 or ctx_len.dtype != torch.int32:
         raise TypeError("block_table and ctx_len must be int32")
+    if k_pool.dtype == torch.uint8:
+        return _paged_fp8_decode(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, scale,
+                                 err_word, y, workspace, stream, options)
     if y is None:
         y = torch.empty_like(q)
     p = _paged_params(q, k_pool, v_pool, block_table, ctx_len, y, k_new, v_new, scale, err_word,
@@ -528,6 +595,31 @@ def paged_attn_decode(q, k_pool, v_pool, block_table, ctx_len, *, k_new=None, v_
     ws, nb = _workspace(need, q.device, workspace)
     p.workspace, p.workspace_bytes = _ptr(ws), nb
     _check("paged_attn_decode", L.paged_attn_decode(C.byref(p), _stream(stream)))
+    return y
+
+
+def _paged_fp8_decode(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, scale, err_word,
+                      y, workspace, stream, options):
+    B, Hkv, D = q.shape[0], k_pool.shape[1], q.shape[-1]
+    if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[2] != 1):
+        raise ValueError("q must be [B, Hq, 1, D] or [B, Hq, D]")
+    _same_device(q, k_pool=k_pool, v_pool=v_pool, block_table=block_table, ctx_len=ctx_len,
+                 k_new=k_new, v_new=v_new, err_word=err_word, y=y)
+    _paged_shapes(B, block_table, ctx_len)
+    for n, t in (("k_new", k_new), ("v_new", v_new)):
+        if t is not None and (t.dtype != q.dtype or t.numel() != B * Hkv * D):
+            raise ValueError(f"{n} must be [B, Hkv, D] of q's dtype")
+    if y is not None and (_dev(y, "y").dtype != q.dtype or y.shape != q.shape):
+        raise ValueError("y must be shaped and typed like q")
+    with _launching(q.device, stream) as s:
+        if y is None:
+            y = torch.empty_like(q)
+        p = _paged_params(q, k_pool, v_pool, block_table, ctx_len, y, k_new, v_new, scale,
+                          err_word, options)
+        need = int(L.paged_attn_decode_workspace(C.byref(p)))
+        ws, nb = _stream_workspace(need, q.device, s, workspace)
+        p.workspace, p.workspace_bytes = _ptr(ws), nb
+        _check("paged_attn_decode", L.paged_attn_decode(C.byref(p), s))
     return y
 
 
@@ -752,3 +844,334 @@ def csa_pool_weight(t, *, w=None, stream=None):
     _check("csa_pool_weight", load().csa_pool_weight(t.data_ptr(), w.data_ptr(), t.numel(),
                                                       _stream(stream)))
     return w
+
+
+# ---- the serving step around a paged cache --------------------------------------------------
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+class _launching:
+    """The tensors' device made current and the launching stream: ``stream``,
+    or the device's current one.  Tensors allocated inside belong to it."""
+
+    __slots__ = ("device", "stream", "guard", "on")
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        same = self.device.index is None or self.device.index == torch.cuda.current_device()
+        self.guard = _NO_GUARD if same else torch.cuda.device(self.device)
+        self.guard.__enter__()
+        if self.stream is None:
+            self.on = _NO_GUARD
+            return torch.cuda.current_stream().cuda_stream
+        self.on = torch.cuda.stream(self.stream)
+        self.on.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        self.on.__exit__(*exc)
+        self.guard.__exit__(*exc)
+        return False
+
+
+def _stream_workspace(nbytes, device, stream, workspace):
+    """Scratch for one call on ``stream`` (a handle): the given tensor, else one
+    kept per (device, stream), so that calls that may overlap never share it.
+    Under graph capture it comes from the graph's own memory instead: a kept
+    tensor could be replaced while the graph still names it, or be shared with
+    another graph that replays at the same time."""
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        return workspace, workspace.numel() * workspace.element_size()
+    if nbytes == 0:
+        return None, 0
+    if torch.cuda.is_current_stream_capturing():
+        return new_workspace(nbytes, device), nbytes
+    key = ("launch", device.index, stream)
+    buf = _ws_cache.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = new_workspace(max(nbytes, 1 << 20), device)
+        _ws_cache[key] = buf
+    return buf, buf.numel()
+
+
+def _rows(t, name, dtype=None, dims=3):
+    """A CUDA tensor whose last axis is contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} axes")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    return t
+
+
+def _same_device(first, **others):
+    for n, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{n} is on {t.device}, not on {first.device}")
+
+
+def _int32(t, name, numel=None):
+    _dev(t, name)
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} entries")
+    return t
+
+
+def _paged_shapes(B, block_table, ctx_len):
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    if ctx_len.numel() != B:
+        raise ValueError("ctx_len must be [B]")
+
+
+def _fp8_page_tokens(k_pool, v_pool, D):
+    """Tokens of a page of the FP8 pools (uint8 [num_pages, Hkv, page_tokens * (D + 1)])."""
+    if k_pool.dim() != 3 or v_pool.shape != k_pool.shape or v_pool.dtype != torch.uint8:
+        raise ValueError("FP8 pools are two uint8 tensors [num_pages, Hkv, page_tokens * (D + 1)]")
+    if k_pool.shape[2] % (D + 1):
+        raise ValueError(f"the pools' pages do not hold rows of {D} codes and a scale")
+    return k_pool.shape[2] // (D + 1)
+
+
+def new_fp8_pool(num_pages: int, Hkv: int, page_tokens: int, D: int, device="cuda") -> torch.Tensor:
+    """A zeroed FP8 page pool, uint8 ``[num_pages, Hkv, page_tokens * (D + 1)]``: per page and
+    head ``page_tokens`` rows of D E4M3 codes, then their E8M0 scale bytes."""
+    return torch.zeros((num_pages, Hkv, page_tokens * (D + 1)), dtype=torch.uint8, device=device)
+
+
+_SCALING = {"none": 0, "linear": 1, "ntk": 2, "ramp": 3}
+
+
+def rope_table(rotary_dim, *, base=10000.0, interleaved=False, scaling="none", factor=1.0,
+               original_len=0, ramp=(1.0, 32.0), mscale=1.0, inv_freq=None) -> RopeTable:
+    """The angles of ``rotary_dim // 2`` rotary pairs, computed once in 64 bits on the host.
+
+    Pair i turns by ``position * f_i``, ``f_i = base ** (-2i / rotary_dim)``, scaled for long
+    contexts: ``"linear"`` (f / factor), ``"ntk"`` (a larger base) or ``"ramp"`` (pairs with more
+    than ``ramp[1]`` turns over ``original_len`` tokens keep f, those with fewer than ``ramp[0]``
+    take f / factor, a linear mix between); or ``inv_freq`` gives the f_i.  ``mscale`` multiplies
+    the rotated dims.  ``interleaved`` pairs dims (2i, 2i + 1), otherwise (i, i + rotary_dim / 2)."""
+    c = _RopeConfig()
+    c.rotary_dim, c.interleaved, c.mscale = int(rotary_dim), int(bool(interleaved)), float(mscale)
+    if inv_freq is not None:
+        freqs = [float(f) for f in inv_freq]
+        if len(freqs) != c.rotary_dim // 2:
+            raise ValueError("inv_freq must have rotary_dim / 2 entries")
+        keep = (C.c_double * len(freqs))(*freqs)
+        c.scaling, c.inv_freq = 4, C.cast(keep, _p)
+    else:
+        if scaling not in _SCALING:
+            raise ValueError(f"scaling must be one of {sorted(_SCALING)}")
+        c.scaling = _SCALING[scaling]
+    c.base, c.factor, c.original_len = float(base), float(factor), float(original_len)
+    c.ramp_low, c.ramp_high = float(ramp[0]), float(ramp[1])
+    out = RopeTable()
+    _check("rope_table", load().sa_rope_table(C.byref(c), C.byref(out)))
+    return out
+
+
+def _rope_arg(rope):
+    if rope is None:
+        return None
+    if not isinstance(rope, RopeTable):
+        raise TypeError("rope must come from rope_table()")
+    return C.addressof(rope)
+
+
+def rotary_embed(q, k, positions, rope, *, q_out=None, k_out=None, stream=None):
+    """Rotary positions of ``q`` and ``k`` (or ``k`` None) in one launch.
+
+    Packed tensors ``[T, H, D]`` with ``positions`` int32/int64 ``[T]``, or head-major ones
+    ``[B, H, S, D]`` with positions ``[S]`` (every batch) or ``[B, S]``; only the last axis has to
+    be contiguous, so views into a fused projection are fine.  ``rope`` comes from
+    ``rope_table``.  ``q_out`` / ``k_out`` may be the inputs themselves.  Returns
+    ``(q_out, k_out)``."""
+    L = load()
+    dims = 4 if isinstance(q, torch.Tensor) and q.dim() == 4 else 3
+    _rows(q, "q", dims=dims)
+    p = RotaryParams()
+    p.dtype = _dt(q)
+    if k is not None:
+        _rows(k, "k", q.dtype, dims)
+    _dev(positions, "positions")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be int32 or int64")
+    if dims == 3:
+        (p.S, p.Hq, p.D), p.B = q.shape, 1
+        batch, axes = (), (0, 1)
+        if positions.shape != (q.shape[0],):
+            raise ValueError("positions must be [T]")
+    else:
+        p.B, p.Hq, p.S, p.D = q.shape
+        batch, axes = (q.shape[0],), (0, 2, 1)
+        if positions.shape != (q.shape[2],) and positions.shape != (q.shape[0], q.shape[2]):
+            raise ValueError("positions must be [S] or [B, S]")
+        p.pos_stride = q.shape[2] if positions.dim() == 2 else 0
+    if k is not None:
+        same = k.shape[0] == q.shape[0] and k.shape[-1] == q.shape[-1] and \
+            (dims == 3 or k.shape[2] == q.shape[2])
+        if not same:
+            raise ValueError("q and k must have the same tokens and head size")
+        p.Hk = k.shape[1]
+    _same_device(q, k=k, positions=positions, q_out=q_out, k_out=k_out)
+    for n, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if o is not None and (t is None or _rows(o, n, q.dtype, dims).shape != t.shape):
+            raise ValueError(f"{n} must be shaped like its input")
+    with _launching(q.device, stream) as s:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        if q.numel() == 0:
+            return q_out, k_out
+        p.rope = _rope_arg(rope)
+        p.positions, p.pos_is_i64 = positions.data_ptr(), int(positions.dtype == torch.int64)
+        for x, n in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out")):
+            if x is not None:
+                setattr(p, n, x.data_ptr())
+                st = x.stride()
+                getattr(p, n + "_strides")[:] = ([0] if not batch else []) + [st[i] for i in axes]
+        _check("rotary_embed", L.rotary_embed(C.byref(p), s))
+    return q_out, k_out
+
+
+def _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, err_word):
+    _rows(k, "k")
+    _rows(v, "v", k.dtype)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    for n, t in (("k_pool", k_pool), ("v_pool", v_pool), ("err_word", err_word)):
+        _dev(t, n)
+    _int32(block_table, "block_table")
+    _int32(ctx_len, "ctx_len")
+    B = ctx_len.numel()
+    _paged_shapes(B, block_table, ctx_len)
+    if seq_start is not None:
+        _int32(seq_start, "seq_start", B + 1)
+    _same_device(k, v=v, k_pool=k_pool, v_pool=v_pool, block_table=block_table, ctx_len=ctx_len,
+                 seq_start=seq_start, err_word=err_word)
+    p = KvPagesParams()
+    p.T, p.Hkv, p.D = k.shape
+    p.dtype = _dt(k)
+    if k_pool.dtype == torch.uint8:
+        p.pool_format = FP8_E4M3_PAGE
+        p.page_tokens = _fp8_page_tokens(k_pool, v_pool, k.shape[2])
+    else:
+        if k_pool.dim() != 4 or k_pool.dtype != k.dtype or v_pool.dtype != k.dtype or \
+                v_pool.shape != k_pool.shape or k_pool.shape[3] != k.shape[2]:
+            raise ValueError("pools must be [num_pages, Hkv, page_tokens, D] of the rows' dtype, "
+                             "or FP8 pools")
+        p.page_tokens = k_pool.shape[2]
+    if k_pool.shape[1] != k.shape[1]:
+        raise ValueError("the pools and the rows have different head counts")
+    p.k, p.v, p.k_pool, p.v_pool = k.data_ptr(), v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr()
+    p.block_table, p.ctx_len = block_table.data_ptr(), ctx_len.data_ptr()
+    p.seq_start, p.err_word = _ptr(seq_start), _ptr(err_word)
+    p.B, p.max_pages, p.num_pages = B, block_table.shape[1], k_pool.shape[0]
+    p.k_strides[:] = k.stride()[:2]
+    p.v_strides[:] = v.stride()[:2]
+    return p
+
+
+def paged_kv_write(k, v, k_pool, v_pool, block_table, ctx_len, seq_start=None, *, rope=None,
+                   err_word=None, stream=None):
+    """Write new tokens' K and V into their pages, K rotated first when ``rope`` (from
+    ``rope_table``) is given, both quantised when the pools are FP8 (``new_fp8_pool``).
+
+    ``k/v [T, Hkv, D]`` packed rows (only the last axis contiguous): sequence b owns rows
+    ``seq_start[b] .. seq_start[b+1]`` (int32 ``[B+1]``; None: one row each), the last tokens of
+    its ``ctx_len[b]`` (int32 ``[B]``, the new tokens counted)."""
+    L = load()
+    p = _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, err_word)
+    if seq_start is None and k.shape[0] != ctx_len.numel():
+        raise ValueError("without seq_start every sequence has one row")
+    if k.numel() == 0:
+        return
+    p.rope = _rope_arg(rope)
+    with _launching(k.device, stream) as s:
+        _check("paged_kv_write", L.paged_kv_write(C.byref(p), s))
+
+
+def paged_kv_read(k_pool, v_pool, block_table, ctx_len, seq_start, k=None, v=None, *, total=None,
+                  head_dim=None, dtype=torch.bfloat16, err_word=None, stream=None):
+    """Read contexts back from their pages into packed rows ``k/v [T, Hkv, D]``: row
+    ``seq_start[b] + i`` receives token i of sequence b (dequantised from FP8 pools and rounded
+    once).  ``k`` and ``v`` are given, or allocated as ``[total, Hkv, head_dim]`` of ``dtype``
+    (zeros, so that rows of no sequence are defined).  Returns ``(k, v)``."""
+    L = load()
+    _dev(k_pool, "k_pool")
+    if (k is None) != (v is None):
+        raise ValueError("give both k and v, or neither")
+    with _launching(k_pool.device, stream) as s:
+        if k is None:
+            if total is None or head_dim is None:
+                raise ValueError("give k and v, or total and head_dim")
+            shape = (int(total), k_pool.shape[1], int(head_dim))
+            k = torch.zeros(shape, dtype=dtype, device=k_pool.device)
+            v = torch.zeros(shape, dtype=dtype, device=k_pool.device)
+        if seq_start is None:
+            raise ValueError("seq_start is required")
+        p = _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, err_word)
+        if k.numel() == 0:
+            return k, v
+        _check("paged_kv_read", L.paged_kv_read(C.byref(p), s))
+    return k, v
+
+
+def attn_prefill_packed(q, k, v, q_start, k_start=None, *, causal=True, scale=0.0, softcap=0.0,
+                        y=None, err_word=None, stream=None):
+    """Prefill attention over packed sequences of different lengths: ``q [Tq, Hq, D]``,
+    ``k/v [Tk, Hkv, D]`` (only the last axis contiguous), sequence b's query rows at
+    ``q_start[b] .. q_start[b+1]`` and its key rows at ``k_start[b] ..`` (int32 ``[B+1]``;
+    ``k_start`` None: ``q_start``).  With more keys than queries the queries are the last tokens
+    of the context (causal: query i sees keys ``<= i + nk - nq``); a query that sees no key gives
+    0.  Rows behind the last sequence are not written.  Returns ``y [Tq, Hq, D]``."""
+    L = load()
+    _rows(q, "q")
+    _rows(k, "k", q.dtype)
+    _rows(v, "v", q.dtype)
+    if v.shape != k.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("k and v must have the same shape, and q's head size")
+    _int32(q_start, "q_start")
+    B = q_start.numel() - 1
+    if k_start is not None:
+        _int32(k_start, "k_start", B + 1)
+    elif k.shape[0] != q.shape[0]:
+        raise ValueError("k_start is required when q and k have different rows")
+    _dev(err_word, "err_word")
+    _same_device(q, k=k, v=v, q_start=q_start, k_start=k_start, err_word=err_word, y=y)
+    if y is not None and _rows(y, "y", q.dtype).shape != q.shape:
+        raise ValueError("y must be shaped like q")
+    with _launching(q.device, stream) as s:
+        if y is None:
+            y = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if q.numel() == 0:
+            return y
+        if k.numel() == 0:  # no keys anywhere: an empty tensor has no address to give
+            k = v = torch.empty((1,) + tuple(k.shape[1:]), dtype=q.dtype, device=q.device)
+            k_rows = 0
+        else:
+            k_rows = k.shape[0]
+        p = PackedParams()
+        p.q, p.k, p.v, p.y = q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr()
+        p.q_start, p.k_start, p.err_word = q_start.data_ptr(), _ptr(k_start), _ptr(err_word)
+        p.dtype, p.causal = _dt(q), int(bool(causal))
+        p.B, p.Tk = B, k_rows
+        p.Tq, p.Hq, p.D = q.shape
+        p.Hkv = k.shape[1]
+        p.scale, p.softcap = float(scale), float(softcap)
+        p.q_strides[:] = q.stride()[:2]
+        p.k_strides[:] = k.stride()[:2]
+        p.v_strides[:] = v.stride()[:2]
+        p.y_strides[:] = y.stride()[:2]
+        _check("attn_prefill_packed", L.attn_prefill_packed(C.byref(p), s))
+    return y

@@ -13,6 +13,7 @@
 
 #include "../../include/sa.h"
 #include "kernels.h"
+#include "serving.h"
 
 namespace {
 
@@ -408,6 +409,11 @@ int sparse_plan(const sa_sparse_params* p, Plan& pl) {
 }
 
 }  // namespace
+
+namespace sa {
+void* kernel_event_before() { return t_ev_before; }
+void* kernel_event_after() { return t_ev_after; }
+}  // namespace sa
 
 extern "C" {
 
@@ -820,6 +826,9 @@ int attn_prefill(const sa_prefill_params* p, void* stream) {
 
 // ---- paged decode ------------------------------------------------------------------
 
+// FP8 pages: every CTA keeps the sequences' tile prefix in shared memory.
+constexpr int64_t kFp8PagesMaxBatch = 8192;
+
 static int check_paged(const sa_paged_params* p, int query = 0) {
   if (!p || !p->q || !p->k_pool || !p->v_pool || !p->block_table || !p->ctx_len ||
       (!p->y && !query))
@@ -829,12 +838,25 @@ static int check_paged(const sa_paged_params* p, int query = 0) {
     return SA_ERR_SHAPE;
   if (p->Hq % p->Hkv != 0) return SA_ERR_SHAPE;
   if (dtype_bytes(p->dtype) == 0) return SA_ERR_DTYPE;
+  const bool fp8 = p->pool_format == SA_FP8_E4M3_PAGE;
+  if (p->pool_format != 0 && !fp8) return SA_ERR_DTYPE;
   if (p->options & ~SA_OPT_ROW_COPIES) return SA_ERR_UNSUPPORTED;
+  if (fp8) {
+    if (p->dtype == SA_F32) return SA_ERR_DTYPE;
+    if (!(p->D == 64 || p->D == 128 || p->D == 256) || p->page_tokens % 16 != 0 ||
+        p->options != 0 || p->B > kFp8PagesMaxBatch)
+      return SA_ERR_UNSUPPORTED;
+    if ((p->k_new == nullptr) != (p->v_new == nullptr)) return SA_ERR_NULL;
+    if (!aligned16(p->k_pool) || !aligned16(p->v_pool) ||
+        reinterpret_cast<uintptr_t>(p->y) % 4)
+      return SA_ERR_ALIGN;
+  }
   if (p->num_pages * p->Hkv * p->page_tokens >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;
   if (!std::isfinite(p->scale)) return SA_ERR_SHAPE;
   const size_t es = dtype_bytes(p->dtype);
   const size_t yb = static_cast<size_t>(p->B * p->Hq * p->D) * es;
-  const size_t pool = static_cast<size_t>(p->num_pages * p->Hkv * p->page_tokens * p->D) * es;
+  const size_t pool = fp8 ? static_cast<size_t>(p->num_pages * p->Hkv * p->page_tokens * (p->D + 1))
+                          : static_cast<size_t>(p->num_pages * p->Hkv * p->page_tokens * p->D) * es;
   if (overlaps(p->y, yb, p->q, yb) || overlaps(p->y, yb, p->k_pool, pool) ||
       overlaps(p->y, yb, p->v_pool, pool) || overlaps(p->k_pool, pool, p->v_pool, pool))
     return SA_ERR_OVERLAP;
@@ -867,9 +889,85 @@ static void paged_args(const sa_paged_params* p, sa::GatherArgs& g) {
   g.scale_log2 = scale * 1.4426950408889634f;
 }
 
+// FP8 pages: the head groups that a warp serves, as the "KV heads" of the work
+// units (a pool head's group of more heads than a warp can hold is cut evenly),
+// and the workspace.  False when the request has too many tiles.
+static bool plan_fp8_pages(const sa_paged_params* p, Plan& pl) {
+  sa::GatherArgs& g = pl.g;
+  const int64_t group = p->Hq / p->Hkv, most = sa::fp8_pages_max_heads(static_cast<int>(p->D));
+  int64_t parts = 1;
+  while (group % parts != 0 || group / parts > most) ++parts;
+  g.Hkv = p->Hkv * parts;
+  g.g = g.hpu = group / parts;
+  g.n_groups = g.I = g.Hkv;
+  g.units = g.B * g.Hkv;
+  const int64_t context = p->max_pages * p->page_tokens;
+  if (context >= (int64_t(1) << 31) || g.units * ((context + 15) / 16) >= (int64_t(1) << 31))
+    return false;
+  const int sms = device_shape().sms;
+  const int64_t warps = sa::fp8_pages_grid_warps(static_cast<int>(p->D), g.hpu, sms);
+  size_t off = 0;
+  pl.off_meta = off;
+  off += align_up(sizeof(int64_t) + static_cast<size_t>(g.B + 1) * sizeof(int32_t));
+  const size_t partials = static_cast<size_t>(warps) * 2 * g.hpu;
+  pl.off_part_o = off;
+  off += align_up(partials * g.D * sizeof(float));
+  pl.off_part_ml = off;
+  off += align_up(partials * 2 * sizeof(float));
+  pl.bytes = off;
+  return true;
+}
+
+static int paged_fp8_decode(const sa_paged_params* p, cudaStream_t st) {
+  Plan pl;
+  paged_args(p, pl.g);
+  if (!plan_fp8_pages(p, pl)) return SA_ERR_UNSUPPORTED;
+  const int rc = check_workspace(pl, p->workspace, p->workspace_bytes);
+  if (rc != SA_OK) return rc;
+  if (p->k_new) {
+    sa::KvPagesArgs w;
+    memset(&w, 0, sizeof(w));
+    w.x[0] = const_cast<void*>(p->k_new);
+    w.x[1] = const_cast<void*>(p->v_new);
+    w.pool[0] = p->k_pool;
+    w.pool[1] = p->v_pool;
+    for (int i = 0; i < 2; ++i) {
+      w.xs[i][0] = p->Hkv * p->D;
+      w.xs[i][1] = p->D;
+    }
+    w.block_table = p->block_table;
+    w.ctx_len = p->ctx_len;
+    w.err_word = p->err_word;
+    w.fp8 = 1;
+    w.aligned = aligned16(p->k_new) && aligned16(p->v_new);
+    w.T = w.B = static_cast<int>(p->B);
+    w.Hkv = static_cast<int>(p->Hkv);
+    w.D = static_cast<int>(p->D);
+    w.page_tokens = p->page_tokens;
+    w.max_pages = p->max_pages;
+    w.num_pages = p->num_pages;
+    if (sa::launch_kv_write(w, p->dtype, st) != 0) return SA_ERR_LAUNCH;
+  }
+  sa::GatherArgs& g = pl.g;
+  char* ws = static_cast<char*>(p->workspace);
+  g.meta = reinterpret_cast<int64_t*>(ws + pl.off_meta);
+  g.pref_out = reinterpret_cast<int32_t*>(ws + pl.off_meta + sizeof(int64_t));
+  g.part_o = reinterpret_cast<float*>(ws + pl.off_part_o);
+  g.part_ml = reinterpret_cast<float*>(ws + pl.off_part_ml);
+  sa::mark_event(t_ev_before, st);
+  const int lrc = sa::launch_fp8_pages(g, p->Hkv, p->dtype, device_shape().sms, st);
+  sa::mark_event(t_ev_after, st);
+  if (lrc != 0 || sa::launch_stream_combine(g, p->dtype, st) != 0) return SA_ERR_LAUNCH;
+  return SA_OK;
+}
+
 size_t paged_attn_decode_workspace(const sa_paged_params* p) {
   if (check_paged(p, 1) != SA_OK) return 0;
   Plan pl;
+  if (p->pool_format == SA_FP8_E4M3_PAGE) {
+    paged_args(p, pl.g);
+    return plan_fp8_pages(p, pl) ? pl.bytes : 0;
+  }
   paged_args(p, pl.g);
   if (plan_gather(pl, p->dtype) != SA_OK) return 0;
   return pl.bytes;
@@ -879,6 +977,7 @@ int paged_attn_decode(const sa_paged_params* p, void* stream) {
   int rc = check_paged(p);
   if (rc != SA_OK) return rc;
   cudaStream_t st = as_stream(stream);
+  if (p->pool_format == SA_FP8_E4M3_PAGE) return paged_fp8_decode(p, st);
   Plan pl;
   paged_args(p, pl.g);
   rc = plan_gather(pl, p->dtype);

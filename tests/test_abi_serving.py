@@ -1,0 +1,154 @@
+"""CPU-only checks of the serving-step entry points: struct layouts, and the
+host-side refusals (fake addresses; every request below is refused before
+anything is launched)."""
+import ctypes as C
+
+import pytest
+
+import sparse_top_kv_validate_gb300 as sa
+from test_abi import _c_layout, host_lib, lib  # noqa: F401  (fixtures)
+
+
+@pytest.mark.parametrize("cname,py", [("sa_rope", sa.RopeTable), ("sa_rope_config", sa._RopeConfig),
+                                      ("sa_rotary_params", sa.RotaryParams),
+                                      ("sa_kv_pages_params", sa.KvPagesParams),
+                                      ("sa_packed_params", sa.PackedParams),
+                                      ("sa_paged_params", sa.PagedParams)])
+def test_struct_layout_matches_header(cname, py):
+    fields = [f for f, _ in py._fields_]
+    size, offs = _c_layout(cname, fields)
+    assert C.sizeof(py) == size
+    assert [getattr(py, f).offset for f in fields] == offs
+
+
+def _rope(R=64):
+    return sa.rope_table(R)
+
+
+def _set(p, **kw):
+    for k, v in kw.items():
+        if isinstance(v, (list, tuple)):
+            getattr(p, k)[:] = v
+        else:
+            setattr(p, k, v)
+    return p
+
+
+def _rotary(keep):
+    p = sa.RotaryParams()
+    keep.append(_rope())
+    return _set(p, q=0x100000, k=0x200000, q_out=0x300000, k_out=0x400000, positions=0x500000,
+                rope=C.addressof(keep[-1]), dtype=sa.BF16, B=1, S=10, Hq=8, Hk=2, D=128,
+                q_strides=[0, 1024, 128], k_strides=[0, 256, 128], q_out_strides=[0, 1024, 128],
+                k_out_strides=[0, 256, 128])
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=None), -1), (dict(positions=None), -1), (dict(rope=None), -1), (dict(k_out=None), -1),
+    (dict(dtype=9), -3), (dict(B=0), -2), (dict(Hq=0), -2), (dict(S=-1), -2), (dict(D=0), -2),
+    (dict(D=32), -2),                                    # rotary_dim 64 beyond the head
+    (dict(q_strides=[0, -1024, 128]), -2),
+    (dict(q_out_strides=[0, 0, 128]), -2),               # rows on top of one another
+    (dict(q_out_strides=[0, 1024, 64]), -2),
+    (dict(q=0x100001), -4), (dict(positions=0x500002), -4),
+    (dict(q_out=0x100000 + 256), -6), (dict(k_out=0x100000), -6), (dict(k_out=0x300000), -6),
+    (dict(positions=0x300000), -6),
+    (dict(S=1 << 31), -7), (dict(D=512, q_strides=[0, 4096, 512], k_strides=[0, 1024, 512],
+                                 q_out_strides=[0, 4096, 512], k_out_strides=[0, 1024, 512]), -7)])
+def test_rotary_refusals(host_lib, change, status):      # noqa: F811
+    keep = []
+    assert host_lib.rotary_embed(C.byref(_set(_rotary(keep), **change)), None) == status
+
+
+def test_rotary_takes_interleaved_views_in_place_and_empty_calls(host_lib):  # noqa: F811
+    keep = []
+    # q and k are heads of one buffer, rotated in place: no overlap is found, and S = 0
+    # launches nothing
+    p = _set(_rotary(keep), S=0, k=0x100000 + 8 * 256, q_out=0x100000, k_out=0x100000 + 8 * 256,
+             q_strides=[0, 1536, 128], k_strides=[0, 1536, 128], q_out_strides=[0, 1536, 128],
+             k_out_strides=[0, 1536, 128])
+    assert host_lib.rotary_embed(C.byref(p), None) == 0
+    # the same views one head further into each other
+    p = _set(p, S=10, k=0x100000 + 7 * 256, k_out=0x100000 + 7 * 256)
+    assert host_lib.rotary_embed(C.byref(p), None) == -6
+
+
+def _pages():
+    p = sa.KvPagesParams()
+    return _set(p, k=0x100000, v=0x200000, k_pool=0x10000000, v_pool=0x20000000, block_table=0x300000,
+                ctx_len=0x400000, seq_start=0x500000, dtype=sa.BF16, pool_format=sa.FP8_E4M3_PAGE, T=20,
+                B=2, Hkv=2, D=128, page_tokens=16, max_pages=4, num_pages=8, k_strides=[256, 128],
+                v_strides=[256, 128])
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(k=None), -1), (dict(v_pool=None), -1), (dict(ctx_len=None), -1), (dict(block_table=None), -1),
+    (dict(dtype=3), -3), (dict(pool_format=2), -3), (dict(B=0), -2), (dict(T=-1), -2), (dict(page_tokens=0), -2),
+    (dict(seq_start=None), -2), (dict(k_strides=[-256, 128]), -2),
+    (dict(D=96), -7), (dict(page_tokens=8), -7), (dict(max_pages=1 << 28), -7), (dict(pool_format=0, D=2000), -7),
+    (dict(k_pool=0x10000008), -4), (dict(k=0x100001), -4),
+    (dict(v_pool=0x10000000 + 4096), -6), (dict(k=0x10000000), -6)])
+def test_page_write_and_read_refusals(host_lib, change, status):  # noqa: F811
+    for fn in (host_lib.paged_kv_write, host_lib.paged_kv_read):
+        assert fn(C.byref(_set(_pages(), **change)), None) == status
+
+
+def test_page_read_refuses_a_rotation_and_one_output_for_both(host_lib):  # noqa: F811
+    rope = _rope()
+    p = _set(_pages(), rope=C.addressof(rope))
+    assert host_lib.paged_kv_read(C.byref(p), None) == -7
+    p = _set(_pages(), v=0x100000)
+    assert host_lib.paged_kv_read(C.byref(p), None) == -6
+    rope.reserved_ = 1
+    p = _set(_pages(), rope=C.addressof(rope))
+    assert host_lib.paged_kv_write(C.byref(p), None) == -2
+    p = _set(_pages(), rope=C.addressof(_rope(256)))
+    assert host_lib.paged_kv_write(C.byref(p), None) == -2
+
+
+def _fp8_decode():
+    p = sa.PagedParams()
+    return _set(p, q=0x100000, y=0x200000, k_pool=0x10000000, v_pool=0x20000000, block_table=0x300000,
+                ctx_len=0x400000, dtype=sa.F16, pool_format=sa.FP8_E4M3_PAGE, B=2, Hq=8, Hkv=2, D=128,
+                page_tokens=16, max_pages=4, num_pages=8)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=sa.F32), -3), (dict(pool_format=7), -3), (dict(D=96), -7), (dict(page_tokens=24), -7),
+    (dict(options=sa.OPT_ROW_COPIES), -7), (dict(B=8193), -7), (dict(k_new=0x700000), -1),
+    (dict(k_pool=0x10000004), -4), (dict(y=0x200002), -4), (dict(y=0x20000000 + 64), -6),
+    (dict(max_pages=1 << 27), -7), (dict(Hq=7), -2)])
+def test_fp8_page_decode_refusals(host_lib, change, status):  # noqa: F811
+    assert host_lib.paged_attn_decode(C.byref(_set(_fp8_decode(), **change)), None) == status
+
+
+def test_fp8_page_decode_needs_its_workspace(host_lib):  # noqa: F811
+    p = _fp8_decode()
+    need = host_lib.paged_attn_decode_workspace(C.byref(p))
+    assert need > 0
+    assert host_lib.paged_attn_decode(C.byref(p), None) == -5
+    _set(p, workspace=0x40000000, workspace_bytes=need - 1)
+    assert host_lib.paged_attn_decode(C.byref(p), None) == -5
+    _set(p, workspace=0x40000010, workspace_bytes=need)
+    assert host_lib.paged_attn_decode(C.byref(p), None) == -4
+
+
+def _packed():
+    p = sa.PackedParams()
+    return _set(p, q=0x1000000, k=0x2000000, v=0x3000000, y=0x4000000, q_start=0x500000, k_start=0x600000,
+                dtype=sa.BF16, causal=1, B=2, Tq=20, Tk=30, Hq=8, Hkv=2, D=128, q_strides=[1024, 128],
+                k_strides=[256, 128], v_strides=[256, 128], y_strides=[1024, 128])
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=None), -1), (dict(y=None), -1), (dict(q_start=None), -1), (dict(dtype=8), -3), (dict(B=0), -2),
+    (dict(Hq=9), -2), (dict(Tq=-1), -2), (dict(k_start=None), -2), (dict(softcap=-1.0), -2),
+    (dict(scale=float("inf")), -2), (dict(y_strides=[0, 128]), -2), (dict(k_strides=[-256, 128]), -2),
+    (dict(D=258), -7), (dict(D=66), -7), (dict(Tq=1 << 30), -7), (dict(q=0x1000001), -4), (dict(y=0x1000000), -6),
+    (dict(y=0x2000000 + 512), -6)])
+def test_packed_prefill_refusals(host_lib, change, status):  # noqa: F811
+    assert host_lib.attn_prefill_packed(C.byref(_set(_packed(), **change)), None) == status
+
+
+def test_packed_prefill_without_queries_launches_nothing(host_lib):  # noqa: F811
+    assert host_lib.attn_prefill_packed(C.byref(_set(_packed(), Tq=0)), None) == 0

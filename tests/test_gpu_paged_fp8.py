@@ -1,0 +1,261 @@
+"""GPU parity of paged_attn_decode over FP8 pages against 64-bit attention over the
+pages' own values.
+
+Tolerance: the codes and q enter the products exactly; an fp32 sum of D products is
+off by at most D 2^-22 of the sum of magnitudes (a step of 2^-23 per addition, twice
+for truncation), so a score by e_s = D 2^-22 max sum|q||k| scale, and with its
+scaling and exp2 (2^-21 of up to 2^7 log2 units) a probability by 2 (e_s + 2^-14) of
+itself; the probability times the value's scale is held to 2^-16; the sum and the
+division add 2^-18.  An output is off by the total times sum p |v|, plus half a step."""
+import math
+
+import pytest
+import torch
+
+from oracle import serving as orc
+from test_gpu_paged_kv import DT, Layout
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def fill(lay, Hkv, D, seed, spread=3):
+    """Pools of random codes (NaN codes left out) and scale bytes."""
+    g = torch.Generator().manual_seed(seed)
+    pools = []
+    for _ in range(2):
+        p = torch.randint(0, 256, (lay.pages, Hkv, lay.pt * (D + 1)), generator=g, dtype=torch.uint8)
+        c = p[..., :lay.pt * D]
+        c[(c & 127) == 127] = 64
+        p[..., lay.pt * D:] = torch.randint(119 - spread, 119 + spread, (lay.pages, Hkv, lay.pt), generator=g).to(torch.uint8)
+        pools.append(p)
+    return pools
+
+
+def values(lay, pool, b, h, D):
+    out = torch.empty(lay.ctx[b], D, dtype=torch.float64)
+    for pi in range(-(-lay.ctx[b] // lay.pt)):
+        page = int(lay.table[b, pi])
+        codes = pool[page, h, :lay.pt * D].view(lay.pt, D)
+        x = orc.dequantise_rows(codes, pool[page, h, lay.pt * D:])
+        n = min(lay.pt, lay.ctx[b] - pi * lay.pt)
+        out[pi * lay.pt:pi * lay.pt + n] = x[:n]
+    return out
+
+
+def check(y, q, lay, pools, scale=None, seqs=None):
+    y = y.cpu()
+    B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
+    Hkv = pools[0].shape[1]
+    g = Hq // Hkv
+    scale = scale or 1 / math.sqrt(D)
+    fi = torch.finfo(y.dtype)
+    for b in range(B) if seqs is None else seqs:
+        for h in range(Hkv):
+            qq = q[b].reshape(Hq, D)[h * g:(h + 1) * g].double().cpu()
+            want, mag, most = orc.attend(qq, values(lay, pools[0], b, h, D), values(lay, pools[1], b, h, D), scale)
+            got = y[b].reshape(Hq, D)[h * g:(h + 1) * g].double()
+            rel = 2 * (D * 2.0 ** -22 * most + 2.0 ** -14) + 2.0 ** -16 + 2.0 ** -18
+            tol = rel * mag + (want.abs() + rel * mag) * fi.eps / 2 + fi.smallest_normal * fi.eps
+            assert torch.isfinite(got).all()
+            off = float(((got - want).abs() - tol).max())
+            assert off <= 0, f"seq {b} head {h}: {off:.3e} over the bound"
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("ctx,pt,Hkv,g,D", [
+    ([1], 16, 1, 1, 128), ([16], 16, 2, 4, 128), ([17, 1, 300, 15], 16, 2, 4, 128), ([33, 500], 32, 3, 8, 64),
+    ([1000, 3, 64, 65], 64, 1, 16, 64), ([700, 90], 16, 2, 16, 128), ([257, 31], 16, 2, 6, 256), ([129], 48, 1, 32, 128),
+    ([400, 2], 16, 1, 17, 256), ([5000, 1, 2, 3], 16, 8, 4, 128), ([90] * 33, 16, 1, 2, 64)])
+def test_matches_64_bits(cuda_lib, dt, ctx, pt, Hkv, g, D):
+    lay = Layout(ctx, ctx, pt, seed=D + len(ctx))
+    pools = fill(lay, Hkv, D, 1)
+    q = torch.randn(len(ctx), Hkv * g, 1, D, generator=torch.Generator().manual_seed(2)).to(DT[dt])
+    table, ctx_t, _ = lay.gpu()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = cuda_lib.paged_attn_decode(q.to(DEV), pools[0].to(DEV), pools[1].to(DEV), table, ctx_t, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0 and y.shape == q.shape
+    check(y, q, lay, pools)
+    y3 = cuda_lib.paged_attn_decode(q[:, :, 0].contiguous().to(DEV), pools[0].to(DEV), pools[1].to(DEV), table, ctx_t)
+    assert torch.equal(y3, y[:, :, 0])                     # and the same again, bit for bit
+
+
+def test_a_long_context_split_over_the_machine(cuda_lib):
+    lay = Layout([70000, 5, 20000], [1, 1, 1], 16, seed=3)
+    pools = fill(lay, 2, 128, 4)
+    q = torch.randn(3, 8, 1, 128, generator=torch.Generator().manual_seed(5)).bfloat16()
+    table, ctx_t, _ = lay.gpu()
+    y = cuda_lib.paged_attn_decode(q.to(DEV), pools[0].to(DEV), pools[1].to(DEV), table, ctx_t, scale=0.05)
+    check(y, q, lay, pools, scale=0.05)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_every_code_and_far_scales(cuda_lib, dt):
+    """All 254 finite codes (subnormal ones among them) as K and as V; scales from 2^-60 to
+    2^40 between the tokens of one sequence."""
+    D, n = 128, 64
+    lay = Layout([n], [n], 16)
+    codes = torch.tensor([c for c in range(256) if c & 127 != 127], dtype=torch.uint8)
+    pools = []
+    for s in range(2):
+        rows = codes[(torch.arange(n * D) * (7 if s else 1)) % 254].view(n, D)
+        e = torch.tensor([127 - 60, 127, 127 + (40 if s else 0), 120], dtype=torch.uint8)[torch.arange(n) % 4]
+        p = torch.zeros(lay.pages, 1, 16 * (D + 1), dtype=torch.uint8)
+        for i in range(n):
+            page, slot = lay.place(0, i)
+            orc.write_row(p, page, 0, slot, 16, D, rows[i], e[i])
+        pools.append(p)
+    table, ctx_t, _ = lay.gpu()
+    if dt == "f16":                                        # the output has to hold the result
+        for i in range(n):
+            page, slot = lay.place(0, i)
+            b = pools[1][page, 0, 16 * D + slot]
+            pools[1][page, 0, 16 * D + slot] = min(int(b), 120)
+    for size in (1.0, 2.0 ** -13, 100.0):
+        q = (torch.randn(1, 4, 1, D, generator=torch.Generator().manual_seed(1)) * size / 64).to(DT[dt])
+        y = cuda_lib.paged_attn_decode(q.to(DEV), pools[0].to(DEV), pools[1].to(DEV), table, ctx_t, scale=2.0 ** -7 / size)
+        check(y, q, lay, pools, scale=2.0 ** -7 / size)
+
+
+def test_what_lies_behind_the_context_never_counts(cuda_lib):
+    """NaN codes and NaN scales in the slots past the context, in its page and in others."""
+    lay = Layout([37, 16, 1], [1] * 3, 32)
+    pools = fill(lay, 2, 128, 7)
+    clean = [p.clone() for p in pools]
+    for p in pools:
+        used = torch.zeros(lay.pages, 32, dtype=torch.bool)
+        for b, c in enumerate(lay.ctx):
+            for i in range(c):
+                used[lay.place(b, i)] = True
+        for page in range(lay.pages):
+            for slot in range(32):
+                if not used[page, slot]:
+                    p[page, :, slot * 128:(slot + 1) * 128] = 0xFF
+                    p[page, :, 32 * 128 + slot] = 255
+    q = torch.randn(3, 8, 1, 128, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    table, ctx_t, _ = lay.gpu()
+    a = cuda_lib.paged_attn_decode(q, pools[0].to(DEV), pools[1].to(DEV), table, ctx_t)
+    b = cuda_lib.paged_attn_decode(q, clean[0].to(DEV), clean[1].to(DEV), table, ctx_t)
+    assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+
+
+def test_nan_rows_and_nan_queries_come_out_as_nan(cuda_lib):
+    lay = Layout([9000, 50], [1, 1], 16)
+    table, ctx_t, _ = lay.gpu()
+    q = torch.randn(2, 4, 1, 64, generator=torch.Generator().manual_seed(1)).half().to(DEV)
+    for which in (0, 1):
+        pools = fill(lay, 1, 64, 7)
+        page, slot = lay.place(0, 4000)
+        pools[which][page, 0, 16 * 64 + slot] = 255
+        y = cuda_lib.paged_attn_decode(q, pools[0].to(DEV), pools[1].to(DEV), table, ctx_t)
+        assert torch.isnan(y[0]).all() and torch.isfinite(y[1]).all()
+    q[0, 2] = float("nan")
+    pools = fill(lay, 1, 64, 7)
+    y = cuda_lib.paged_attn_decode(q, pools[0].to(DEV), pools[1].to(DEV), table, ctx_t)
+    assert torch.isnan(y[0, 2]).all() and torch.isfinite(y[0, [0, 1, 3]]).all() and torch.isfinite(y[1]).all()
+
+
+def test_new_token_is_quantised_into_its_page_first(cuda_lib):
+    sa = cuda_lib
+    lay = Layout([33, 16, 1, 700], [1] * 4, 16)
+    pools = fill(lay, 2, 128, 3)
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn(4, 8, 1, 128, generator=g).bfloat16().to(DEV)
+    kn, vn = (torch.randn(4, 2, 128, generator=g).bfloat16().to(DEV) for _ in range(2))
+    table, ctx_t, _ = lay.gpu()
+    a, b = [p.to(DEV) for p in pools], [p.to(DEV) for p in pools]
+    y = sa.paged_attn_decode(q, *a, table, ctx_t, k_new=kn, v_new=vn)
+    sa.paged_kv_write(kn, vn, *b, table, ctx_t)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert torch.equal(y, sa.paged_attn_decode(q, *b, table, ctx_t))
+    check(y, q, lay, [p.cpu() for p in b])
+
+
+def test_bad_contexts_and_table_entries(cuda_lib):
+    sa = cuda_lib
+    lay = Layout([40, 40, 40], [1] * 3, 16)
+    pools = fill(lay, 2, 64, 3)
+    q = torch.randn(3, 4, 1, 64, generator=torch.Generator().manual_seed(1)).half().to(DEV)
+    table, ctx_t, _ = lay.gpu()
+    for what in ("table", "long", "none"):
+        t, c = table.clone(), ctx_t.clone()
+        if what == "table":
+            t[1, 0] = -3
+        else:
+            c[1] = 10 ** 6 if what == "long" else 0
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        y = sa.paged_attn_decode(q, *[p.to(DEV) for p in pools], t, c, err_word=err)
+        assert int(err) == sa.ERRBIT_PAGE
+        assert torch.isfinite(y.float()).all()
+        # the other sequences are right; not bit for bit what they were: the tiles that one
+        # sequence no longer has move where the others' contexts are cut, and so the order of
+        # their sums, which the bound of check() allows for
+        check(y, q, lay, pools, seqs=(0, 2))
+        if what != "table":
+            assert not y[1].any()                          # no context: zeros
+
+
+def test_two_streams_and_two_graphs_at_once(cuda_lib):
+    """Calls in flight together have scratch of their own: kept per stream, and a graph's own."""
+    sa = cuda_lib
+    lay = Layout([20000, 3000], [1, 1], 16, seed=8)
+    pools = [p.to(DEV) for p in fill(lay, 2, 128, 5)]
+    table, ctx_t, _ = lay.gpu()
+    qs = [torch.randn(2, 8, 1, 128, generator=torch.Generator().manual_seed(i)).bfloat16().to(DEV) for i in range(2)]
+    want = [sa.paged_attn_decode(q, *pools, table, ctx_t) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(sa.paged_attn_decode(qs[i], *pools, table, ctx_t, stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(sa.paged_attn_decode(qs[i], *pools, table, ctx_t))
+        graphs.append(g)
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(outs[i], want[i]) for i in range(2))
+
+
+def test_a_workspace_of_the_callers(cuda_lib):
+    sa = cuda_lib
+    lay = Layout([20000], [1], 16)
+    pools = [p.to(DEV) for p in fill(lay, 1, 64, 5)]
+    table, ctx_t, _ = lay.gpu()
+    q = torch.randn(1, 2, 1, 64).half().to(DEV)
+    need = sa.paged_attn_decode_workspace(q, *pools, table, ctx_t)
+    ws = sa.new_workspace(need, DEV).fill_(0xFF)
+    y = sa.paged_attn_decode(q, *pools, table, ctx_t, workspace=ws)
+    assert torch.equal(y, sa.paged_attn_decode(q, *pools, table, ctx_t))
+    with pytest.raises(sa.SAError):
+        sa.paged_attn_decode(q, *pools, table, ctx_t, workspace=sa.new_workspace(need - 1, DEV))
+
+
+def test_refusals(cuda_lib):
+    sa = cuda_lib
+    lay = Layout([40], [1], 16)
+    table, ctx_t, _ = lay.gpu()
+    pools = [sa.new_fp8_pool(lay.pages, 2, 16, 128) for _ in range(2)]
+    q = torch.zeros(1, 8, 1, 128, dtype=torch.float16, device=DEV)
+    for kw in (dict(q=q.float()), dict(options=sa.OPT_ROW_COPIES)):
+        with pytest.raises(sa.SAError):
+            sa.paged_attn_decode(**dict(dict(q=q, k_pool=pools[0], v_pool=pools[1], block_table=table, ctx_len=ctx_t), **kw))
+    kn = torch.zeros(1, 2, 128, dtype=torch.float16, device=DEV)
+    for kw in (dict(q=q[..., :64].contiguous()), dict(v_pool=pools[1][:-1]), dict(k_new=kn.float(), v_new=kn.float()),
+               dict(k_new=kn[..., :64].contiguous(), v_new=kn), dict(y=q.float()), dict(q=q.expand(1, 8, 2, 128).contiguous()),
+               dict(ctx_len=ctx_t.expand(2).contiguous())):
+        with pytest.raises(ValueError):
+            sa.paged_attn_decode(**dict(dict(q=q, k_pool=pools[0], v_pool=pools[1], block_table=table, ctx_len=ctx_t), **kw))
+    with pytest.raises(sa.SAError):
+        sa.paged_attn_decode(q, *pools, table, ctx_t, k_new=kn)
+    with pytest.raises(sa.SAError):
+        sa.paged_attn_decode(q, pools[0], pools[0], table, ctx_t)
