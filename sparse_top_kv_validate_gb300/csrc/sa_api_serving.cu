@@ -349,7 +349,11 @@ int attn_prefill_packed(const sa_packed_params* p, void* stream) {
   a.scale = p->scale != 0.f ? p->scale : 1.0f / sqrtf(static_cast<float>(p->D));
   a.softcap = p->softcap;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool vec = q.vec16() && k.vec16() && v.vec16() && y.vec16();
+  bool vec = true;  // 16-byte rows whose strides a tensor map can hold
+  for (const Strided* t : all) {
+    vec = vec && t->vec16();
+    for (int i = 0; i < 2; ++i) vec = vec && (t->n[i] <= 1 || t->st[i] > 0);
+  }
   sa::mark_event(sa::kernel_event_before(), st);
   const int rc = vec && sa::packed_tc_supported(a) ? sa::launch_packed_tc(a, st) : sa::launch_packed_simt(a, st);
   sa::mark_event(sa::kernel_event_after(), st);
