@@ -8,31 +8,43 @@
 // short ones.
 //
 // GB300 design (one persistent CTA per SM; warps 0-3 service, 4-11 softmax):
-//  * A query tile is 128 rows: 128 / g tokens times the g query heads of one
-//    KV head, so that a short sequence fills its tiles and the heads share
-//    every K/V tile.  A work item is a pair of neighbouring tiles, the two
-//    "sides": each has its own scores, probabilities and outputs in tensor
-//    memory (S0 S1 O0 O1, 128 columns each at D 128), its own MMA lane and its
-//    own softmax warpgroup of 128 threads, one row per thread.  While one side's
-//    softmax runs, the tensor cores work for the other; a row's maximum and sum
-//    never leave its thread.
-//  * P (16 bits) overwrites the first half of its own scores.  An MMA lane
-//    issues PV(j) and then S(j + 1) into the same columns: the tensor cores take
-//    one thread's MMAs in order.
-//  * Warp 0 loads Q (box: 64 dims x g heads x 128 / g tokens) and the K and V
-//    tiles through a ring of slots; warps 1 and 3 are the MMA lanes; warp 2
-//    passes every V tile on: where keys end inside a tile it zeroes the rows
-//    behind them (0 times another sequence's NaN is NaN), and where some of a
-//    tile's keys are hidden from some rows it looks for values that are not
-//    finite: these are zeroed too, and the rows that do see them add them in
-//    the epilogue.
+//  * A work item is a query tile of 128 rows: 128 / g tokens times the g query
+//    heads of one KV head, so that a short sequence fills its tiles and the
+//    heads share every K/V tile.
+//  * Tensor memory holds three score buffers and O.  Key tile t of the CTA (the
+//    count runs on across its items) goes to buffer t % 3 and to softmax
+//    warpgroup t % 2, whose threads own a row each.  A tile's way (scores,
+//    softmax, PV, buffer free) takes about four times as long as its MMAs: three
+//    tiles on the way at once, two of them in softmax, keep the tensor cores
+//    about half busy.  Measured, 4 x 4,096 tokens, 32 / 8 heads of 128, causal,
+//    bf16: 463 us, 1,189 TFLOP/s.  Other orders tried: two row tiles per item
+//    that share K and V, a score buffer and a warpgroup each, 500 us; the same
+//    with two MMA lanes that interleave, so that both tiles' softmax runs at the
+//    same time, 625 us; with two warpgroups per row tile, half the columns
+//    each, 646 us.
+//  * A thread reads its 128 scores from tensor memory twice, in a loop over
+//    chunks of 32 columns.  Kept in registers they spill, and local memory
+//    shares its path with the MMAs' shared-memory operands; unrolled, the
+//    roles' loops no longer fit the instruction cache together (both measured:
+//    575 us).
+//  * The two threads of a row agree on its offset tile by tile: a thread posts
+//    the offset after its tile (the old one unless the tile's maximum exceeds it
+//    by more than 2^8), the other one's next tile starts from it.  The raise
+//    rescales O in tensor memory, after the previous PV.  With a softcap up to
+//    67 the logits are bounded, the offset is 0 and nothing is posted.
+//  * Warp 0 loads Q (box: 64 dims x g heads x 128 / g tokens; two buffers) and the
+//    K and V tiles through two rings; warp 1's lane issues S = Q K^T and warp 3's
+//    O += P V (P over the first half of its scores), so that a barrier wait or a
+//    commit of one leaves the other's MMAs running.
+//  * Warp 2 passes every V tile on: where keys end inside a tile it zeroes the
+//    rows behind them (0 times another sequence's NaN is NaN), and where some of
+//    a tile's keys are hidden from some rows it looks for values that are not
+//    finite: these are zeroed too, and the rows that do see them add them in the
+//    epilogue.
 //  * Items go to CTAs in a snake order of falling cost.  The lengths are on
 //    the device, so every CTA works out the order itself: the rank of an item
 //    among all has a closed form per sequence (an item's number of key tiles
 //    grows along its sequence), and a CTA keeps only its own items.
-//  * Without a softcap, or with a large one, the row's offset is a maximum that
-//    is raised only by more than 2^8 (O is then rescaled in tensor memory);
-//    with a softcap up to 67 the logits are bounded and the offset is 0.
 //  * Every mbarrier wait is bounded; a stalled pipeline sets
 //    SA_ERRBIT_TIMEOUT, stops every role, and still frees the tensor memory.
 #include <cuda.h>
@@ -51,7 +63,9 @@ namespace sa {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 384;            // 4 service warps, 2 softmax warpgroups
+constexpr int kSBufs = 3;                // score buffers in tensor memory
+constexpr int kLead = 2;                 // K tiles loaded ahead of the V tiles
 constexpr int kTile = 128;               // rows of a query tile; keys of a K/V tile
 constexpr int kSlabBytes = kTile * 128;  // 128 rows x 64 sixteen-bit columns
 constexpr float kRescaleLog2 = 8.0f;     // lazy-maximum slack (factor 256)
@@ -65,19 +79,28 @@ template <int D>
 struct Geo {
   static constexpr int kSlabs = D / 64;
   static constexpr int kTileBytes = kSlabs * kSlabBytes;   // 16 or 32 KB
-  static constexpr int kStages = D == 128 ? 4 : 8;         // ring slots: K tiles even, V tiles odd
-  static constexpr int kOffQ = 0;                          // two sides
-  static constexpr int kOffRing = 2 * kTileBytes;
-  static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
-  // barriers: per side q_full, q_empty, s_full, p_full, o_full, done; per slot
-  // kv_full, kv_empty, v_ready (V slots)
-  static constexpr int kBarQFull = 0, kBarQEmpty = 2, kBarS = 4, kBarP = 6, kBarO = 8, kBarDone = 10,
-                       kBarKvFull = 12, kBarKvEmpty = kBarKvFull + kStages,
-                       kBarV = kBarKvEmpty + kStages, kNumBars = kBarV + kStages;
+  static constexpr int kStages = D == 128 ? 2 : 4;         // slots of the K ring, and of the V ring
+  static constexpr int kOffQ = 0;                          // two buffers
+  static constexpr int kOffK = 2 * kTileBytes;
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kOffBar = kOffV + kStages * kTileBytes;
+  // barriers: per Q buffer q_full, q_empty; per ring slot k_full, k_empty, v_full,
+  // v_ready (past warp 2), v_empty; per score buffer s_full, p_full, pv_done; o_full,
+  // o_read; per warpgroup and turn posted (offsets), sums; per MMA lane done.  (A
+  // warpgroup may be one post ahead of the other's wait, never two.)
+  static constexpr int kBarQFull = 0, kBarQEmpty = 2, kBarKFull = 4, kBarKEmpty = kBarKFull + kStages,
+                       kBarVFull = kBarKEmpty + kStages, kBarVReady = kBarVFull + kStages,
+                       kBarVEmpty = kBarVReady + kStages, kBarS = kBarVEmpty + kStages,
+                       kBarP = kBarS + kSBufs, kBarPv = kBarP + kSBufs, kBarO = kBarPv + kSBufs,
+                       kBarORead = kBarO + 1, kBarPost = kBarORead + 1, kBarSum = kBarPost + 4,
+                       kBarDone = kBarSum + 4, kNumBars = kBarDone + 2;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffFlags = kOffTmemSlot + 4;       // abort, hidden values found
-  static constexpr int kOffSeq = (kOffFlags + 8 + 15) / 16 * 16;  // int4 [B]; int [B + 1]; uint2 [items]
-  static constexpr uint32_t kColS = 0, kColO = 2 * kTile;  // + side * 128, + side * D
+  // float [2 warpgroups][2 turns][128] posted offsets; [2 turns][2 warpgroups][2][128] offsets
+  // and sums at the end of an item
+  static constexpr int kOffXch = (kOffFlags + 8 + 15) / 16 * 16;
+  static constexpr int kOffSeq = kOffXch + 12 * kTile * 4;  // int4 [B]; int [B + 1]; uint2 [items]
+  static constexpr uint32_t kColS = 0, kColO = kSBufs * kTile;
   static constexpr uint32_t kTmemCols = 512;
 };
 
@@ -110,24 +133,23 @@ __device__ __forceinline__ int tiles_of(int causal, int nq, int nk, int last) {
   return lim < 0 ? 1 : lim / kTile + 1;
 }
 
-// Pairs of a sequence with at least x key tiles.
-__device__ __forceinline__ int pairs_with(const Params& p, int nq, int nk, int x) {
-  const int step = 2 * p.tpt, pairs = (nq + step - 1) / step;
-  if (x <= 1) return pairs;
-  const int thr = (x - 1) * kTile;      // the pair's last key must reach thr
+// Query tiles of a sequence with at least x key tiles.
+__device__ __forceinline__ int tiles_with(const Params& p, int nq, int nk, int x) {
+  const int tiles = (nq + p.tpt - 1) / p.tpt;
+  if (x <= 1) return tiles;
+  const int thr = (x - 1) * kTile;      // the tile's last key must reach thr
   if (nk - 1 < thr) return 0;
-  if (!p.causal) return pairs;
+  if (!p.causal) return tiles;
   const int need = thr - (nk - nq);     // and so its last token
-  if (need <= 0) return pairs;
+  if (need <= 0) return tiles;
   if (nq - 1 < need) return 0;
-  return pairs - need / step;           // pairs from the one that holds token `need` on
+  return tiles - need / p.tpt;          // tiles from the one that holds token `need` on
 }
 
 struct Item {
   int q0, nq, k0, nk, kvh;
-  int tok;      // first token of side 0
-  int ns[2];    // key tiles of each side (0: the side has no rows)
-  int n;        // of both
+  int tok;      // first token
+  int n;        // key tiles
   int seen;     // the last key that every row of the item sees
 };
 
@@ -140,7 +162,7 @@ __device__ __forceinline__ int item_index(int k, int G) {
 
 struct Work {
   const int4* seq;      // first query row, queries, first key row, keys
-  const uint2* list;    // this CTA's items: sequence << 16 | KV head, pair
+  const uint2* list;    // this CTA's items: sequence << 16 | KV head, query tile
   int n_items, G, cap;
 
   __device__ __forceinline__ bool get(int k, const Params& p, Item& it) const {
@@ -152,12 +174,8 @@ struct Work {
     it.k0 = s.z;
     it.nk = s.w;
     it.kvh = e.x & 0xffff;
-    it.tok = static_cast<int>(e.y) * 2 * p.tpt;
-    it.ns[0] = tiles_of(p.causal, it.nq, it.nk, min(it.tok + p.tpt, it.nq) - 1);
-    it.ns[1] = it.tok + p.tpt < it.nq
-                   ? tiles_of(p.causal, it.nq, it.nk, min(it.tok + 2 * p.tpt, it.nq) - 1)
-                   : 0;
-    it.n = max(it.ns[0], it.ns[1]);
+    it.tok = static_cast<int>(e.y) * p.tpt;
+    it.n = tiles_of(p.causal, it.nq, it.nk, min(it.tok + p.tpt, it.nq) - 1);
     it.seen = last_key(p.causal, it.nq, it.nk, it.tok);
     return true;
   }
@@ -170,7 +188,7 @@ __device__ __forceinline__ Work lay_out_work(const Params& p, uint8_t* area) {
   int* pref = reinterpret_cast<int*>(seq + p.B);
   uint2* list = reinterpret_cast<uint2*>(pref + ((p.B + 2) & ~1));
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
-  const int step = 2 * p.tpt;
+  const int step = p.tpt;
   bool bad = false;
   for (int b = tid; b < p.B; b += kThreads) {
     const Span q = span_of(p.q_start, b, p.Tq), k = span_of(p.k_start, b, p.Tk);
@@ -196,30 +214,30 @@ __device__ __forceinline__ Work lay_out_work(const Params& p, uint8_t* area) {
     if (lane == 0) pref[p.B] = carry;
   }
   __syncthreads();
-  const int pairs = pref[p.B];
+  const int tiles = pref[p.B];
   const int G = static_cast<int>(gridDim.x);
-  Work w{seq, list, pairs * p.Hkv, G, p.cap_items};
-  for (int i = tid; i < pairs; i += kThreads) {
+  Work w{seq, list, tiles * p.Hkv, G, p.cap_items};
+  for (int i = tid; i < tiles; i += kThreads) {
     int lo = 0, hi = p.B;  // the last sequence with pref <= i
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (pref[mid] <= i) lo = mid;
       else hi = mid;
     }
-    const int b = lo, pr = i - pref[b];
+    const int b = lo, qt = i - pref[b];
     const int4 s = seq[b];
-    const int n = tiles_of(p.causal, s.y, s.w, min((pr + 1) * step, s.y) - 1);
+    const int n = tiles_of(p.causal, s.y, s.w, min((qt + 1) * step, s.y) - 1);
     // items with more key tiles, then those with as many of earlier sequences
     // and of this one
-    int rank = pr - (pref[b + 1] - pref[b] - pairs_with(p, s.y, s.w, n));
+    int rank = qt - (pref[b + 1] - pref[b] - tiles_with(p, s.y, s.w, n));
     for (int o = 0; o < p.B; ++o) {
       const int4 t = seq[o];
-      rank += o < b ? pairs_with(p, t.y, t.w, n) : pairs_with(p, t.y, t.w, n + 1);
+      rank += o < b ? tiles_with(p, t.y, t.w, n) : tiles_with(p, t.y, t.w, n + 1);
     }
     for (int h = 0; h < p.Hkv; ++h) {
       const int x = rank * p.Hkv + h, k = x / G, r = x - k * G;
       if (((k & 1) ? G - 1 - r : r) == static_cast<int>(blockIdx.x) && k < p.cap_items)
-        list[k] = make_uint2(static_cast<uint32_t>(b) << 16 | static_cast<uint32_t>(h), static_cast<uint32_t>(pr));
+        list[k] = make_uint2(static_cast<uint32_t>(b) << 16 | static_cast<uint32_t>(h), static_cast<uint32_t>(qt));
     }
   }
   __syncthreads();
@@ -237,47 +255,42 @@ __device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUt
   tc05::prefetch_tmap(tk);
   tc05::prefetch_tmap(tv);
   const uint32_t q_bytes = static_cast<uint32_t>(G::kSlabs * p.g * p.tpt * 128);
-  uint32_t kv_cnt = 0, q_cnt[2] = {0, 0};
-  bool stop = false;
+  uint32_t k_cnt = 0, v_cnt = 0, q_cnt = 0;
   Item it;
-  for (int k = 0; !stop && work.get(k, p, it); ++k) {
-    for (int side = 0; side < 2 && !stop; ++side) {
-      if (it.ns[side] == 0) continue;
-      // the side's Q is free once the last S MMA of its previous item has completed
-      if (q_cnt[side] > 0 &&
-          !wait_or_abort(&bars[G::kBarQEmpty + side], (q_cnt[side] - 1) & 1, abort_flag, p.err_word)) {
-        stop = true;
-        break;
-      }
-      mbar_arrive_expect_tx(&bars[G::kBarQFull + side], q_bytes);
+  auto load_tile = [&](const CUtensorMap* map, int off, int full, int empty, uint32_t& cnt, int t) {
+    const uint32_t slot = cnt % G::kStages, use = cnt / G::kStages;
+    if (use > 0 && !wait_or_abort(&bars[empty + slot], (use - 1) & 1, abort_flag, p.err_word)) return false;
+    mbar_arrive_expect_tx(&bars[full + slot], G::kTileBytes);
 #pragma unroll
-      for (int s = 0; s < G::kSlabs; ++s)
-        tc05::tma_load3(sm + G::kOffQ + side * G::kTileBytes + s * kSlabBytes, tq, s * 64, it.kvh * p.g,
-                        it.q0 + it.tok + side * p.tpt, &bars[G::kBarQFull + side]);
-      ++q_cnt[side];
-    }
-    for (int e = 0; e < 2 * it.n && !stop; ++e) {  // K_0, V_0, K_1, V_1, ...
-      const uint32_t slot = kv_cnt % G::kStages, use = kv_cnt / G::kStages;
-      if (use > 0 && !wait_or_abort(&bars[G::kBarKvEmpty + slot], (use - 1) & 1, abort_flag, p.err_word)) {
-        stop = true;
-        break;
-      }
-      mbar_arrive_expect_tx(&bars[G::kBarKvFull + slot], G::kTileBytes);
+    for (int s = 0; s < G::kSlabs; ++s)
+      tc05::tma_load3(sm + off + slot * G::kTileBytes + s * kSlabBytes, map, s * 64, it.kvh, it.k0 + t * kTile,
+                      &bars[full + slot]);
+    ++cnt;
+    return true;
+  };
+  bool ok = true;
+  for (int k = 0; ok && work.get(k, p, it); ++k) {
+    // the buffer is free once the item before the last has stored its rows through it
+    const uint32_t qb = q_cnt & 1;
+    if (q_cnt >= 2 && !wait_or_abort(&bars[G::kBarQEmpty + qb], ((q_cnt >> 1) - 1) & 1, abort_flag, p.err_word)) break;
+    mbar_arrive_expect_tx(&bars[G::kBarQFull + qb], q_bytes);
 #pragma unroll
-      for (int s = 0; s < G::kSlabs; ++s)
-        tc05::tma_load3(sm + G::kOffRing + slot * G::kTileBytes + s * kSlabBytes, (e & 1) ? tv : tk, s * 64,
-                        it.kvh, it.k0 + (e >> 1) * kTile, &bars[G::kBarKvFull + slot]);
-      ++kv_cnt;
+    for (int s = 0; s < G::kSlabs; ++s)
+      tc05::tma_load3(sm + G::kOffQ + qb * G::kTileBytes + s * kSlabBytes, tq, s * 64, it.kvh * p.g, it.q0 + it.tok,
+                      &bars[G::kBarQFull + qb]);
+    ++q_cnt;
+    for (int j = -kLead; ok && j < it.n; ++j) {  // K_0, K_1, then K_(j + 2), V_j
+      if (j + kLead < it.n) ok = load_tile(tk, G::kOffK, G::kBarKFull, G::kBarKEmpty, k_cnt, j + kLead);
+      if (ok && j >= 0) ok = load_tile(tv, G::kOffV, G::kBarVFull, G::kBarVEmpty, v_cnt, j);
     }
   }
   if (*abort_flag) {
     // Let every copy already issued land before the CTA can exit.
-    for (int side = 0; side < 2; ++side)
-      if (q_cnt[side] > 0) mbar_wait(&bars[G::kBarQFull + side], (q_cnt[side] - 1) & 1);
+    for (uint32_t b = 0; b < 2; ++b)
+      if (q_cnt > b) mbar_wait(&bars[G::kBarQFull + b], ((q_cnt - b + 1) / 2 - 1) & 1);
     for (uint32_t s = 0; s < G::kStages; ++s) {
-      if (kv_cnt <= s) break;
-      const uint32_t issued = (kv_cnt - s + G::kStages - 1) / G::kStages;
-      mbar_wait(&bars[G::kBarKvFull + s], (issued - 1) & 1);
+      if (k_cnt > s) mbar_wait(&bars[G::kBarKFull + s], ((k_cnt - s + G::kStages - 1) / G::kStages - 1) & 1);
+      if (v_cnt > s) mbar_wait(&bars[G::kBarVFull + s], ((v_cnt - s + G::kStages - 1) / G::kStages - 1) & 1);
     }
   }
 }
@@ -305,16 +318,16 @@ __device__ void v_gate(const Params& p, const Work& work, uint8_t* sm, uint64_t*
                        volatile int* abort_flag, volatile int* found) {
   using G = Geo<D>;
   const int lane = static_cast<int>(threadIdx.x & 31);
-  uint32_t kv_cnt = 0;
+  uint32_t cnt = 0;
   Item it;
   for (int k = 0; work.get(k, p, it); ++k) {
-    for (int j = 0; j < it.n; ++j, kv_cnt += 2) {
-      const uint32_t idx = kv_cnt + 1, slot = idx % G::kStages;
-      if (!wait_or_abort_warp(&bars[G::kBarKvFull + slot], (idx / G::kStages) & 1, abort_flag, p.err_word))
+    for (int j = 0; j < it.n; ++j, ++cnt) {
+      const uint32_t slot = cnt % G::kStages;
+      if (!wait_or_abort_warp(&bars[G::kBarVFull + slot], (cnt / G::kStages) & 1, abort_flag, p.err_word))
         return;
       const int first = j * kTile;
       if (first + kTile - 1 > it.seen) {  // (rows behind the last key are past `seen` too)
-        uint8_t* tile = sm + G::kOffRing + slot * G::kTileBytes;
+        uint8_t* tile = sm + G::kOffV + slot * G::kTileBytes;
         const int end = min(max(it.nk - first, 0), kTile);      // rows behind: nobody's keys
         for (int e = lane; e < (kTile - end) * 8 * G::kSlabs; e += 32) {
           const int r = end + e / (8 * G::kSlabs), c = e % (8 * G::kSlabs);
@@ -344,105 +357,89 @@ __device__ void v_gate(const Params& p, const Work& work, uint8_t* sm, uint64_t*
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[G::kBarV + slot]);
+      if (lane == 0) mbar_arrive(&bars[G::kBarVReady + slot]);
     }
   }
 }
 
-// ---- role: MMA issuer of one side (one lane) ------------------------------------------------
+// ---- role: MMA issuers (one lane each) ----------------------------------------------------------
 
+// S(t) = Q . K^T into score buffer t % 3, once the buffer's previous P has been
+// read by its PV.
 template <int D, bool kBf16>
-__device__ void mma_lane(int side, const Params& p, const Work& work, uint8_t* sm, uint64_t* bars,
-                         uint32_t tmem, volatile int* abort_flag) {
+__device__ void score_lane(const Params& p, const Work& work, uint8_t* sm, uint64_t* bars, uint32_t tmem,
+                           volatile int* abort_flag) {
   using G = Geo<D>;
   constexpr uint32_t id_s = tc05::idesc_f16(kTile, kTile, kBf16, false, false);
-  constexpr uint32_t id_o = tc05::idesc_f16(kTile, D, kBf16, false, true);
-  const uint64_t dQ = tc05::sw128_desc(smem_u32(sm + G::kOffQ + side * G::kTileBytes), 16, 1024);
-  const uint64_t dK = tc05::sw128_desc(smem_u32(sm + G::kOffRing), 16, 1024);
-  const uint64_t dV = tc05::sw128_desc(smem_u32(sm + G::kOffRing), kSlabBytes, 1024);
-  const uint32_t tS = tmem + G::kColS + side * kTile, tO = tmem + G::kColO + side * D;
-
-  auto issue_s = [&](uint32_t slot) {  // S = Q . K^T
-    const uint64_t b0 = dK + ((slot * G::kTileBytes) >> 4);
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      const uint32_t off = ((kk / 4) * kSlabBytes + (kk % 4) * 32) >> 4;
-      tc05::mma_ss(tS, dQ + off, b0 + off, id_s, kk > 0 ? 1u : 0u);
-    }
-  };
-  auto issue_pv = [&](uint32_t slot, bool acc) {  // O (+)= P . V
-    const uint64_t v0 = dV + ((slot * G::kTileBytes) >> 4);
-#pragma unroll
-    for (int kk = 0; kk < kTile / 16; ++kk)
-      tc05::mma_ts(tO, tS + kk * 8, v0 + ((kk * 2048) >> 4), id_o, (acc || kk > 0) ? 1u : 0u);
-  };
-
-  uint32_t kv_cnt = 0, q_cnt = 0, p_cnt = 0;
-  bool stop = false;
+  const uint64_t dQ = tc05::sw128_desc(smem_u32(sm + G::kOffQ), 16, 1024);
+  const uint64_t dK = tc05::sw128_desc(smem_u32(sm + G::kOffK), 16, 1024);
+  uint32_t t = 0, q_cnt = 0, buf = 0, buf_use = 0;
   Item it;
-  for (int k = 0; !stop && work.get(k, p, it); ++k) {
-    const int n = it.ns[side];
-    const uint32_t base = kv_cnt;
-    kv_cnt += 2 * it.n;
-    auto wait_k = [&](int j) {
-      const uint32_t i = base + 2 * j;
-      return wait_or_abort(&bars[G::kBarKvFull + i % G::kStages], (i / G::kStages) & 1, abort_flag, p.err_word);
-    };
-    auto wait_v = [&](int j) {
-      const uint32_t i = base + 2 * j + 1;
-      return wait_or_abort(&bars[G::kBarV + i % G::kStages], (i / G::kStages) & 1, abort_flag, p.err_word);
-    };
-    auto score = [&](int j) {
-      if (!wait_k(j)) return false;
-      const uint32_t slot = (base + 2 * j) % G::kStages;
+  bool ok = true;
+  for (int k = 0; ok && work.get(k, p, it); ++k, ++q_cnt) {
+    ok = wait_or_abort(&bars[G::kBarQFull + (q_cnt & 1)], (q_cnt >> 1) & 1, abort_flag, p.err_word);
+    for (int j = 0; ok && j < it.n; ++j, ++t) {
+      const uint32_t slot = t % G::kStages;
+      ok = (buf_use == 0 || wait_or_abort(&bars[G::kBarPv + buf], (buf_use - 1) & 1, abort_flag, p.err_word)) &&
+           wait_or_abort(&bars[G::kBarKFull + slot], (t / G::kStages) & 1, abort_flag, p.err_word);
+      if (!ok) break;
       tc05::fence_after_sync();
-      issue_s(slot);
-      tc05::commit(&bars[G::kBarS + side]);
-      tc05::commit(&bars[G::kBarKvEmpty + slot]);
-      if (j == n - 1) tc05::commit(&bars[G::kBarQEmpty + side]);
-      return true;
-    };
-    if (n > 0) {
-      if (!wait_or_abort(&bars[G::kBarQFull + side], q_cnt & 1, abort_flag, p.err_word) || !score(0)) break;
-      ++q_cnt;
-    }
-    for (int j = 0; j < n; ++j) {
-      if (!wait_v(j) || !wait_or_abort(&bars[G::kBarP + side], p_cnt & 1, abort_flag, p.err_word)) {
-        stop = true;
-        break;
+      const uint64_t a0 = dQ + (((q_cnt & 1) * G::kTileBytes) >> 4), b0 = dK + ((slot * G::kTileBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * kSlabBytes + (kk % 4) * 32) >> 4;
+        tc05::mma_ss(tmem + G::kColS + buf * kTile, a0 + off, b0 + off, id_s, kk > 0 ? 1u : 0u);
       }
-      ++p_cnt;
-      const uint32_t slot = (base + 2 * j + 1) % G::kStages;
-      tc05::fence_after_sync();
-      issue_pv(slot, j > 0);
-      tc05::commit(&bars[G::kBarKvEmpty + slot]);
-      if (j == n - 1) tc05::commit(&bars[G::kBarO + side]);
-      if (j + 1 < n && !score(j + 1)) {
-        stop = true;
-        break;
+      tc05::commit(&bars[G::kBarS + buf]);
+      tc05::commit(&bars[G::kBarKEmpty + slot]);
+      if (++buf == kSBufs) {
+        buf = 0;
+        ++buf_use;
       }
-    }
-    // tiles that only the other side reads
-    for (int j = n; j < it.n && !stop; ++j) {
-      if (!wait_k(j)) {
-        stop = true;
-        break;
-      }
-      mbar_arrive(&bars[G::kBarKvEmpty + (base + 2 * j) % G::kStages]);
-      if (!wait_v(j)) {
-        stop = true;
-        break;
-      }
-      mbar_arrive(&bars[G::kBarKvEmpty + (base + 2 * j + 1) % G::kStages]);
     }
   }
   // Every MMA this lane issued completes before the tensor memory is released.
-  uint64_t* done = &bars[G::kBarDone + side];
-  tc05::commit(done);
-  mbar_wait(done, 0);
+  tc05::commit(&bars[G::kBarDone]);
+  mbar_wait(&bars[G::kBarDone], 0);
 }
 
-// ---- role: softmax (one warpgroup per side, one row per thread) ------------------------------
+// O (+)= P(t) . V; the first PV of an item waits until the previous O has been read.
+template <int D, bool kBf16>
+__device__ void value_lane(const Params& p, const Work& work, uint8_t* sm, uint64_t* bars, uint32_t tmem,
+                           volatile int* abort_flag) {
+  using G = Geo<D>;
+  constexpr uint32_t id_o = tc05::idesc_f16(kTile, D, kBf16, false, true);
+  const uint64_t dV = tc05::sw128_desc(smem_u32(sm + G::kOffV), kSlabBytes, 1024);
+  uint32_t t = 0, buf = 0, buf_use = 0;
+  Item it;
+  bool ok = true;
+  for (int k = 0; ok && work.get(k, p, it); ++k) {
+    if (k > 0) ok = wait_or_abort(&bars[G::kBarORead], (k - 1) & 1, abort_flag, p.err_word);
+    for (int j = 0; ok && j < it.n; ++j, ++t) {
+      const uint32_t slot = t % G::kStages;
+      ok = wait_or_abort(&bars[G::kBarVReady + slot], (t / G::kStages) & 1, abort_flag, p.err_word) &&
+           wait_or_abort(&bars[G::kBarP + buf], buf_use & 1, abort_flag, p.err_word);
+      if (!ok) break;
+      tc05::fence_after_sync();
+      const uint64_t v0 = dV + ((slot * G::kTileBytes) >> 4);
+      const uint32_t tP = tmem + G::kColS + buf * kTile;
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        tc05::mma_ts(tmem + G::kColO, tP + kk * 8, v0 + ((kk * 2048) >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+      tc05::commit(&bars[G::kBarPv + buf]);
+      tc05::commit(&bars[G::kBarVEmpty + slot]);
+      if (j == it.n - 1) tc05::commit(&bars[G::kBarO]);
+      if (++buf == kSBufs) {
+        buf = 0;
+        ++buf_use;
+      }
+    }
+  }
+  tc05::commit(&bars[G::kBarDone + 1]);
+  mbar_wait(&bars[G::kBarDone + 1], 0);
+}
+
+// ---- role: softmax (tile t belongs to warpgroup t % 2, a row to a thread) -----------------------
 
 // kCols columns of this thread's O row *= alpha, in tensor memory (warp-collective).
 template <int kCols>
@@ -498,29 +495,27 @@ __device__ __forceinline__ float scale_chunk(uint32_t (&r)[32], float k1) {
   return fmaxf(ax[0], ax[1]);
 }
 
-// Maximum of the chunk's columns <= rel.
+// Maximum of the chunk; kMask: its columns above rel become -inf first.
 template <bool kMask>
-__device__ __forceinline__ float max_chunk(const uint32_t (&r)[32], int rel, float m) {
+__device__ __forceinline__ float max_chunk(uint32_t (&r)[32], int rel, float m) {
   float mx[2] = {m, SA_NEG_INF};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    float a = __uint_as_float(r[2 * i]), b = __uint_as_float(r[2 * i + 1]);
     if (kMask) {
-      if (2 * i > rel) a = SA_NEG_INF;
-      if (2 * i + 1 > rel) b = SA_NEG_INF;
+      if (2 * i > rel) r[2 * i] = __float_as_uint(SA_NEG_INF);
+      if (2 * i + 1 > rel) r[2 * i + 1] = __float_as_uint(SA_NEG_INF);
     }
-    mx[i & 1] = max3(mx[i & 1], a, b);
+    mx[i & 1] = max3(mx[i & 1], __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
   }
   return fmaxf(mx[0], mx[1]);
 }
 
-// p = 2^(logit(x) - m) of 32 columns, masked ones 0, written to tensor memory at
-// tP as 16 columns of 16-bit pairs and added to the two partial sums.
+// p = 2^(logit(x) - m) of 32 columns, masked ones 0, as 16 packed pairs; added to
+// the two partial sums.
 template <int kMode, bool kMask, typename T>
-__device__ __forceinline__ void exp_chunk(const uint32_t (&r)[32], uint32_t tP, float c2, float neg_m,
+__device__ __forceinline__ void exp_chunk(const uint32_t (&r)[32], uint32_t (&pk)[16], float c2, float neg_m,
                                           const float (&tq)[kTanhTerms], int rel, uint64_t (&ls)[2]) {
   const uint64_t c2x2 = f2_pack(c2, c2), nm2 = f2_pack(neg_m, neg_m);
-  uint32_t pk[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float x0 = __uint_as_float(r[2 * i]), x1 = __uint_as_float(r[2 * i + 1]);
@@ -549,136 +544,231 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&r)[32], uint32_t tP, 
     ls[i & 1] = f2_add(ls[i & 1], f2_pack(a, b));
     pk[i] = pack2<T>(a, b);
   }
-  tc05::tmem_st16(tP, pk);
 }
 
 enum Variant { kVarPlain = 0, kVarCapMax = 1, kVarCapFixed = 2 };
 
+// What a thread keeps of an item until its epilogue: the item, and the offset and
+// sum of the row over the warpgroup's own tiles.
+struct Finished {
+  int k;
+  uint32_t last;  // the item's last tile
+  float m, l;
+};
+
 template <int D, typename T, int kVariant>
-__device__ void softmax_rows(const Params& p, const Work& work, uint64_t* bars, uint32_t tmem,
+__device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uint64_t* bars, uint32_t tmem,
                              volatile int* abort_flag, volatile int* found) {
   using G = Geo<D>;
   constexpr bool kCap = kVariant != kVarPlain, kFixed = kVariant == kVarCapFixed;
+  constexpr int kOCols = D / 2;  // O columns that this warpgroup stores
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const int side = (warp - 4) >> 2;
+  const int wg = (warp - 4) >> 2;
   const int row = ((warp & 3) << 5) | lane;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  const uint32_t tS = tmem + lanes + G::kColS + side * kTile, tO = tmem + lanes + G::kColO + side * D;
-  const int rt = row / p.g, rh = row - rt * p.g;  // token of the tile, head of the group
+  const uint32_t tS0 = tmem + lanes + G::kColS, tO = tmem + lanes + G::kColO;
+  volatile float* xch = reinterpret_cast<volatile float*>(sm + G::kOffXch) + row;
+  const int rt = row / p.g;  // token of the tile that this row belongs to
   const float c2 = p.c_log2, k1 = p.k1;
   float tq[kTanhTerms];
 #pragma unroll
-  for (int k = 0; k < kTanhTerms; ++k) tq[k] = p.tq[k];
-  uint32_t s_cnt = 0, o_cnt = 0;
+  for (int i = 0; i < kTanhTerms; ++i) tq[i] = p.tq[i];
+  // The other warpgroup's post after its tile u (every one is waited for, in order).
+  auto posted = [&](uint32_t u) {
+    return wait_or_abort_warp(&bars[G::kBarPost + 2 * (wg ^ 1) + ((u >> 1) & 1)], (u >> 2) & 1, abort_flag, p.err_word);
+  };
+
+  int k = 0;             // current item
+  uint32_t t = 0;        // tiles before it
   Item it;
-  for (int k = 0; work.get(k, p, it); ++k) {
-    const int n = it.ns[side];
-    if (n == 0) continue;
-    const int tok = it.tok + side * p.tpt + rt;
-    const bool live = rt < p.tpt && tok < it.nq;
-    const int lim = live ? last_key(p.causal, it.nq, it.nk, tok) : -1;  // last visible key
-    float m = SA_NEG_INF;
-    uint64_t ls[2] = {0, 0};
-    for (int j = 0; j < n; ++j) {
-      if (!wait_or_abort_warp(&bars[G::kBarS + side], s_cnt & 1, abort_flag, p.err_word)) return;
-      ++s_cnt;
+  bool more = work.get(k, p, it);
+  int j = wg;            // this warpgroup's next tile of it
+  float m = SA_NEG_INF;  // this row's offset after the tiles so far
+  uint64_t ls[2] = {0, 0};
+  Finished done{0, 0, 0.f, 0.f};
+  bool pending = false;  // an item whose epilogue waits until after the next tile
+  while (more || pending) {
+    if (more && j < it.n) {
+      const uint32_t u = t + j, buf = u % kSBufs;
+      const uint32_t tS = tS0 + buf * kTile;
+      if (!wait_or_abort_warp(&bars[G::kBarS + buf], (u / kSBufs) & 1, abort_flag, p.err_word)) return;
       tc05::fence_after_sync();
+      uint32_t r[2][32];
+      tc05::tmem_ld32(tS, r[0]);
+      const int tok = it.tok + rt;
+      const int lim = rt < p.tpt && tok < it.nq ? last_key(p.causal, it.nq, it.nk, tok) : -1;  // last visible key
       const int rel = lim - j * kTile;  // columns above rel are masked
       const bool masked = __any_sync(0xffffffffu, rel < kTile - 1);
-      uint32_t r[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tc05::tmem_ld32(tS + c * 32, r[c]);
-      tc05::tmem_ld_wait();
-      int mode = kPlain;
-      if (kCap) {
-        float ax = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ax = fmaxf(ax, scale_chunk(r[c], k1));
-        mode = __any_sync(0xffffffffu, ax > kTanhPolyBound) ? kFar : kPoly;
+      if (!kFixed && j > 0) {
+        // the offset after the previous tile, the other warpgroup's
+        if (!posted(u - 1)) return;
+        const float o = xch[(2 * (wg ^ 1) + (((u - 1) >> 1) & 1)) * kTile];
+        if (__any_sync(0xffffffffu, o != m)) {
+          const float f = m == o ? 1.0f : ex2(m - o);  // (0 from no offset at all)
+          ls[0] = f2_mul(ls[0], f2_pack(f, f));
+          ls[1] = f2_mul(ls[1], f2_pack(f, f));
+          m = o;
+        }
       }
-      float alpha = 1.0f;
-      bool any_raise = false;
+      float ax = 0.f, mx = SA_NEG_INF;
+      auto look = [&](uint32_t (&x)[32], int c) {
+        if (kCap) ax = fmaxf(ax, scale_chunk(x, k1));
+        if (!kFixed) mx = masked ? max_chunk<true>(x, rel - 32 * c, mx) : max_chunk<false>(x, 0, mx);
+      };
+#pragma unroll 1
+      for (int c = 0; c < 4; c += 2) {  // the next chunk (at last the first again) is on its way meanwhile
+        tc05::tmem_ld_wait();
+        tc05::tmem_ld32(tS + 32 * (c + 1), r[1]);
+        look(r[0], c);
+        tc05::tmem_ld_wait();
+        tc05::tmem_ld32(tS + 32 * ((c + 2) & 3), r[0]);
+        look(r[1], c + 1);
+      }
+      int mode = kPlain;
+      if (kCap) mode = __any_sync(0xffffffffu, ax > kTanhPolyBound) ? kFar : kPoly;
       if (!kFixed) {
-        float mx = SA_NEG_INF;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          mx = masked ? max_chunk<true>(r[c], rel - 32 * c, mx) : max_chunk<false>(r[c], 0, mx);
         float mt = SA_NEG_INF;
         if (mx != SA_NEG_INF)
           mt = mode == kPlain ? mx * c2 : mode == kPoly ? poly_logit(mx, tq) : tanh_far(mx) * c2;
-        const bool raise = mt > m + kRescaleLog2 || (m == SA_NEG_INF && mt > m);
-        any_raise = __any_sync(0xffffffffu, raise);
-        if (raise) {
-          alpha = ex2(m - mt);
-          m = mt;
-          ls[0] = f2_mul(ls[0], f2_pack(alpha, alpha));
-          ls[1] = f2_mul(ls[1], f2_pack(alpha, alpha));
+        const bool up = mt > m + kRescaleLog2 || (m == SA_NEG_INF && mt > m);
+        xch[(2 * wg + ((u >> 1) & 1)) * kTile] = up ? mt : m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[G::kBarPost + 2 * wg + ((u >> 1) & 1)]);
+        if (__any_sync(0xffffffffu, up)) {
+          float alpha = 1.0f;
+          if (up) {
+            alpha = ex2(m - mt);
+            m = mt;
+            ls[0] = f2_mul(ls[0], f2_pack(alpha, alpha));
+            ls[1] = f2_mul(ls[1], f2_pack(alpha, alpha));
+          }
+          if (j > 0) {
+            // O follows once PV(u - 1) has completed.  (S(u - 1) was issued after
+            // PV(u - 4) completed, so no other phase of that barrier is outstanding.)
+            const uint32_t pb = (u - 1) % kSBufs;
+            if (!wait_or_abort_warp(&bars[G::kBarPv + pb], ((u - 1) / kSBufs) & 1, abort_flag, p.err_word)) return;
+            tc05::fence_after_sync();
+            rescale_o<D>(tO, alpha);
+          }
         }
       }
       const float neg_m = (kFixed || m == SA_NEG_INF) ? 0.0f : -m;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t tP = tS + c * 16;
+      auto exps = [&](uint32_t (&x)[32], int c) {
         const int rc = rel - 32 * c;
-        if (!kCap) {
-          if (masked) exp_chunk<kPlain, true, T>(r[c], tP, c2, neg_m, tq, rc, ls);
-          else exp_chunk<kPlain, false, T>(r[c], tP, c2, neg_m, tq, rc, ls);
-        } else if (mode == kPoly) {
-          if (masked) exp_chunk<kPoly, true, T>(r[c], tP, c2, neg_m, tq, rc, ls);
-          else exp_chunk<kPoly, false, T>(r[c], tP, c2, neg_m, tq, rc, ls);
-        } else {
-          exp_chunk<kFar, true, T>(r[c], tP, c2, neg_m, tq, masked ? rc : kTile, ls);
-        }
+        uint32_t pk[16];
+        if (kCap) scale_chunk(x, k1);
+        if (!kCap && masked) exp_chunk<kPlain, true, T>(x, pk, c2, neg_m, tq, rc, ls);
+        else if (!kCap) exp_chunk<kPlain, false, T>(x, pk, c2, neg_m, tq, 0, ls);
+        else if (mode == kFar) exp_chunk<kFar, true, T>(x, pk, c2, neg_m, tq, masked ? rc : kTile, ls);
+        else if (masked) exp_chunk<kPoly, true, T>(x, pk, c2, neg_m, tq, rc, ls);
+        else exp_chunk<kPoly, false, T>(x, pk, c2, neg_m, tq, rc, ls);
+        tc05::tmem_st16(tS + c * 16, pk);
+      };
+#pragma unroll 1
+      for (int c = 0; c < 4; c += 2) {
+        tc05::tmem_ld_wait();
+        tc05::tmem_ld32(tS + 32 * (c + 1), r[1]);
+        exps(r[0], c);
+        tc05::tmem_ld_wait();
+        if (c == 0) tc05::tmem_ld32(tS + 64, r[0]);
+        exps(r[1], c + 1);
       }
-      // PV(j - 1) was issued before S(j) by the same lane, so it has completed
-      // with it: O may follow the new maximum
-      if (!kFixed && any_raise && j > 0) rescale_o<D>(tO, alpha);
       tc05::tmem_st_wait();
       tc05::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[G::kBarP + side]);
+      if (lane == 0) mbar_arrive(&bars[G::kBarP + buf]);
+      j += 2;
     }
 
-    // epilogue: O / l of this row
-    float l;
-    {
+    // The end of an item: its last tile is L's; the other warpgroup, which also
+    // has the next item's first tile, takes that one before the epilogue, so that
+    // the tensor cores find work when O has been read.
+    bool epilogue = pending;
+    pending = false;
+    if (more && j >= it.n && !epilogue) {
       float a, b;
       f2_unpack(f2_add(ls[0], ls[1]), a, b);
-      l = a + b;
+      done = Finished{k, t + it.n - 1, m, a + b};
+      volatile float* mine = xch + (4 + 4 * (k & 1) + 2 * wg) * kTile;
+      mine[0] = m;
+      mine[kTile] = a + b;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[G::kBarSum + 2 * wg + (k & 1)]);
+      const bool owner = (done.last & 1) == static_cast<uint32_t>(wg);
+      t += it.n;
+      more = work.get(++k, p, it);
+      j = static_cast<int>((t ^ wg) & 1);
+      m = SA_NEG_INF;
+      ls[0] = ls[1] = 0;
+      epilogue = owner || !more;
+      pending = !epilogue;
     }
-    if (!wait_or_abort_warp(&bars[G::kBarO + side], o_cnt & 1, abort_flag, p.err_word)) return;
-    ++o_cnt;
+    if (!epilogue) continue;
+
+    // ---- O / l of the rows, half of the columns per warpgroup
+    Item e;
+    work.get(done.k, p, e);
+    const uint32_t turn = done.k & 1;
+    const int tok = e.tok + rt;
+    const int lim = rt < p.tpt && tok < e.nq ? last_key(p.causal, e.nq, e.nk, tok) : -1;
+    if (!wait_or_abort_warp(&bars[G::kBarSum + 2 * (wg ^ 1) + turn], (done.k >> 1) & 1, abort_flag, p.err_word) ||
+        (!kFixed && (done.last & 1) != static_cast<uint32_t>(wg) && !posted(done.last)) ||
+        !wait_or_abort_warp(&bars[G::kBarO], turn, abort_flag, p.err_word))
+      return;
     tc05::fence_after_sync();
+    float l = done.l;
+    {
+      volatile float* others = xch + (4 + 4 * turn + 2 * (wg ^ 1)) * kTile;
+      const float mo = others[0], lo = others[kTile];
+      // O carries the last tile's offset
+      const float mf = (done.last & 1) == static_cast<uint32_t>(wg) ? done.m : mo;
+      l = (kFixed || done.m == mf ? l : l * ex2(done.m - mf)) + (kFixed || mo == mf ? lo : lo * ex2(mo - mf));
+    }
     const float inv_l = l != 0.0f ? 1.0f / l : 0.0f;  // no key: 0; a NaN sum stays NaN
-    T* yrow = static_cast<T*>(p.y) + (it.q0 + tok) * p.ys0 + (it.kvh * p.g + rh) * p.ys1;
+    // The rows leave through the item's Q tile (its last S has completed): 16-byte
+    // pieces, the piece number XORed with the row, so that neither side meets a
+    // bank conflict and a store covers whole lines of 4 (or 8) rows.
+    constexpr int kPieces = kOCols / 8;
+    uint4* stage = reinterpret_cast<uint4*>(sm + G::kOffQ + turn * G::kTileBytes) + (wg * 4 + (warp & 3)) * 32 * kPieces;
     const bool add = *found != 0;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
+#pragma unroll 1
+    for (int c = 0; c < kOCols / 16; ++c) {
       uint32_t o[16];
-      tc05::tmem_ld16(tO + c * 16, o);
+      tc05::tmem_ld16(tO + wg * kOCols + c * 16, o);
       tc05::tmem_ld_wait();
-      if (add && live) {
+      if (add) {
         // values that are not finite were zeroed in the tiles that hide keys from
         // some rows; this row adds those of the keys it sees (rare: read again)
-        const T* v = static_cast<const T*>(p.v) + it.kvh * p.vs1 + c * 16;
-        for (int key = max(it.seen + 1, 0); key <= lim; ++key)
+        const T* v = static_cast<const T*>(p.v) + e.kvh * p.vs1 + wg * kOCols + c * 16;
+        for (int key = max(e.seen + 1, 0); key <= lim; ++key)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float x = to_f32<T>(v[(it.k0 + key) * p.vs0 + i]);
+            const float x = to_f32<T>(v[(e.k0 + key) * p.vs0 + i]);
             if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
           }
       }
-      if (live) {
-        uint32_t pk[8];
+      uint32_t pk[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          pk[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
-        uint4* dst = reinterpret_cast<uint4*>(yrow + c * 16);
-        dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-      }
+      for (int i = 0; i < 8; ++i)
+        pk[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
+      stage[lane * kPieces + ((2 * c) ^ (lane & (kPieces - 1)))] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      stage[lane * kPieces + ((2 * c + 1) ^ (lane & (kPieces - 1)))] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
     }
-    tc05::fence_before_sync();  // these reads of O precede the next item's first P
+    tc05::fence_before_sync();  // these reads precede the next item's first PV
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[G::kBarORead]);
+    T* y = static_cast<T*>(p.y) + e.kvh * p.g * p.ys1 + wg * kOCols + (lane % kPieces) * 8;
+#pragma unroll 1
+    for (int i = 0; i < kPieces; ++i) {
+      const int rl = i * (32 / kPieces) + lane / kPieces;  // row of this warp's 32
+      const int rr = (warp & 3) * 32 + rl, r_t = rr / p.g, r_h = rr - r_t * p.g;
+      const uint4 v = stage[rl * kPieces + ((lane % kPieces) ^ (rl & (kPieces - 1)))];
+      if (r_t < p.tpt && e.tok + r_t < e.nq)
+        *reinterpret_cast<uint4*>(y + (e.q0 + e.tok + r_t) * p.ys0 + r_h * p.ys1) = v;
+    }
+    fence_proxy_async_smem();  // these reads precede the buffer's next load
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[G::kBarQEmpty + turn]);
   }
 }
 
@@ -702,17 +792,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[G::kBarQFull + i], 1);
-      mbar_init(&bars[G::kBarQEmpty + i], 1);
-      mbar_init(&bars[G::kBarS + i], 1);
-      mbar_init(&bars[G::kBarP + i], 4);   // the side's softmax warps
-      mbar_init(&bars[G::kBarO + i], 1);
+      mbar_init(&bars[G::kBarQEmpty + i], 8);  // every softmax warp
       mbar_init(&bars[G::kBarDone + i], 1);
     }
-    for (int s = 0; s < G::kStages; ++s) {
-      mbar_init(&bars[G::kBarKvFull + s], 1);
-      mbar_init(&bars[G::kBarKvEmpty + s], 2);  // both MMA lanes
-      mbar_init(&bars[G::kBarV + s], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars[G::kBarPost + i], 4);  // the warps of a warpgroup
+      mbar_init(&bars[G::kBarSum + i], 4);
     }
+    for (int s = 0; s < G::kStages; ++s) {
+      mbar_init(&bars[G::kBarKFull + s], 1);
+      mbar_init(&bars[G::kBarKEmpty + s], 1);
+      mbar_init(&bars[G::kBarVFull + s], 1);
+      mbar_init(&bars[G::kBarVReady + s], 1);
+      mbar_init(&bars[G::kBarVEmpty + s], 1);
+    }
+    for (int i = 0; i < kSBufs; ++i) {
+      mbar_init(&bars[G::kBarS + i], 1);
+      mbar_init(&bars[G::kBarP + i], 4);
+      mbar_init(&bars[G::kBarPv + i], 1);
+    }
+    mbar_init(&bars[G::kBarO], 1);
+    mbar_init(&bars[G::kBarORead], 8);  // every softmax warp
     *abort_flag = 0;
     *found = 0;
     fence_mbar_init();
@@ -737,13 +837,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) producer<D>(&tq, &tk, &tv, p, work, sm, bars, abort_flag);
   } else if (warp == 1) {
-    if (lane == 0) mma_lane<D, kBf16>(0, p, work, sm, bars, tmem, abort_flag);
+    if (lane == 0) score_lane<D, kBf16>(p, work, sm, bars, tmem, abort_flag);
   } else if (warp == 2) {
     v_gate<D, T>(p, work, sm, bars, abort_flag, found);
   } else if (warp == 3) {
-    if (lane == 0) mma_lane<D, kBf16>(1, p, work, sm, bars, tmem, abort_flag);
+    if (lane == 0) value_lane<D, kBf16>(p, work, sm, bars, tmem, abort_flag);
   } else {
-    softmax_rows<D, T, kVariant>(p, work, bars, tmem, abort_flag, found);
+    softmax_rows<D, T, kVariant>(p, work, sm, bars, tmem, abort_flag, found);
   }
   __syncwarp();
   tc05::fence_before_sync();
@@ -835,7 +935,7 @@ int64_t smem_bytes(int64_t seqs, int64_t items) {
 
 // Items of one launch over `seqs` sequences, at most.
 int64_t items_bound(const PackedArgs& a, int64_t seqs) {
-  const int64_t g = a.Hq / a.Hkv, step = 2 * (kTile / g);
+  const int64_t g = a.Hq / a.Hkv, step = kTile / g;
   return (a.Tq / step + seqs) * a.Hkv;
 }
 
