@@ -7,16 +7,17 @@
 //
 // The work is laid out as in the stream kernel (k_stream.cu): every (sequence,
 // KV head)'s context cut into 16-token tiles laid end to end, one contiguous
-// range of tiles per warp of a persistent grid, whatever the contexts; a unit
-// split across warps leaves partials for stream_combine_kernel.
+// range of tiles per warp of a persistent grid, whatever the contexts.
 //
-//  * A tile's K and V codes go from DRAM straight to registers, 16 bytes per
-//    lane and load: with keys as M of S^T = K Q^T and dims as M of
-//    O^T = V^T P^T, the 16 codes a lane loads are exactly values of its own
-//    MMA fragments once the contraction index (for S) and the output dims (for
-//    O) are numbered to fit.  So no shared memory, barrier or ldmatrix is
-//    needed; the next tile's loads are issued as soon as a register is free
-//    and stay in flight during the arithmetic.
+//  * Each warp has a ring of tiles that TMA fills (16 rows of codes of K and of
+//    V in the 128-byte swizzle, 64-byte for D 64, and their 16 scale bytes each).
+//    With keys as M of S^T = K Q^T and dims as M of O^T = V^T P^T, the 16 codes
+//    that a lane reads with one shared-memory load are values of its own MMA
+//    fragments once the contraction index (for S) and the output dims (for O)
+//    are numbered to fit, so no ldmatrix and no exchange is needed; the swizzle
+//    keeps those loads free of bank conflicts.  (Codes straight from DRAM to
+//    registers, the next tile's loads under this tile's arithmetic, reached
+//    2.75 TB/s: too few bytes in flight.)
 //  * K: e4m3 -> f16 is exact (one conversion per pair), and q enters as f16
 //    after a power of two per head brings its largest element to [2^14, 2^15),
 //    so bf16 and f16 queries lose nothing that fp32 sums would keep (an
@@ -29,39 +30,41 @@
 //    probability's rounding stays far below the output's.
 //  * The running maximum is raised only when a score exceeds it by 2^8 (one
 //    vote per tile instead of a reduction and a rescale).
+//  * A unit split across warps is merged in shared memory by its CTA; only one
+//    split across CTAs leaves partials, one per CTA, for stream_combine_kernel.
+//    (With a partial per warp the merge of a 131,072-token context, 282 partials
+//    per unit, took longer than the attention.)
 #include "gather_common.cuh"
 #include "serving.h"
+#include "tc05.cuh"
 
 namespace sa {
 
 namespace {
 
-constexpr int kCtaWarps = 4;
 constexpr float kRaiseLog2 = 8.0f;
 
 template <int D, int NT>
 struct FGeo {
-  // CTAs per SM that the registers allow
-  static constexpr int kCtas = D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? (NT == 1 ? 4 : 2) : 2;
-  static constexpr int kKs = D / 16;      // contraction steps of S, 16-dim tiles of O
-  static constexpr int kKv = D / 64;      // 16-byte pieces of a K row per lane
-  static constexpr int kVw = D / 32;      // 4-byte words of a V row per lane
+  // warps per CTA (one CTA per SM) that the registers and the rings allow
+  static constexpr int kWarps = D == 64 ? 16 : (D == 128 && NT == 1) ? 12 : 8;
+  static constexpr int kStages = D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? (NT == 1 ? 3 : 4) : 2;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kKs = D / 16;       // contraction steps of S, 16-dim tiles of O
+  static constexpr int kSlabs = D == 256 ? 2 : 1;          // TMA boxes of a K or V tile
+  static constexpr int kBoxCols = D == 64 ? 64 : 128;
+  static constexpr int kTileBytes = 16 * D;                // K, and V
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kHeads = 8 * NT;
+  // per CTA: rings | partials | stage scales | barriers | merge lists | tile prefix
+  static constexpr int kPartFloats = kHeads * (D + 2);     // o, then m and l per head
+  static constexpr int kOffPart = kWarps * kStages * kStageBytes;
+  static constexpr int kOffScale = kOffPart + kWarps * kPartFloats * 4;
+  static constexpr int kOffBar = kOffScale + kWarps * kStages * 32;
+  static constexpr int kOffList = kOffBar + kWarps * kStages * 8;
+  static constexpr int kOffPref = kOffList + (2 * kWarps + 2) * 16;
+  static_assert(kStages * kStageBytes >= kPartFloats * 4, "the last partial reuses the ring");
 };
-
-__device__ __forceinline__ uint4 ld_stream16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 ld_stream8(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p));
-  return v;
-}
 
 // Two E4M3 codes (low 16 bits) -> two f16, exact.
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
@@ -82,10 +85,10 @@ __device__ __forceinline__ uint32_t times_2p120(uint32_t v) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
+// 2^(byte - 127); NaN for 255.
 __device__ __forceinline__ float e8m0_f32(uint32_t byte) {
-  return byte == 0     ? 0x1p-127f
-         : byte == 255 ? __int_as_float(0x7fffffff)
-                       : __uint_as_float(byte << 23);
+  const uint32_t odd = ((byte + 1) & 255u) < 2u ? 0x400000u : 0u;  // 0: 2^-127, subnormal; 255: NaN
+  return __uint_as_float((byte << 23) | odd);
 }
 
 // (tile indices stay below 2^31, checked on the host)
@@ -114,25 +117,31 @@ __device__ __forceinline__ Unit unit_at(const GatherArgs& a, const int32_t* pref
   return r;
 }
 
-// One tile's codes and scale bytes in registers (raw), as loaded ahead.
-template <int D>
-struct KTile {
-  uint4 x[2][D / 64];     // rows gid and gid + 8
-  uint32_t s[2];          // their scale bytes
-};
-template <int D>
-struct VTile {
-  uint32_t x[4][D / 32];  // tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9: this lane's dims
-  uint32_t s[2];          // scale bytes of tokens gid and gid + 8
+// A unit's partial result in shared memory: where, whose, and what of it it covers.
+struct Part {
+  int32_t unit_off, unit_tu;   // first tile and tiles of the unit
+  int32_t head0;               // b * Hq + first query head
+  int32_t where;               // float offset of o from the shared-memory base (-1: none)
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kCtaWarps * 32, FGeo<D, NT>::kCtas)
-    fp8_pages_kernel(GatherArgs a, int64_t pool_heads, int64_t min_range) {
+__global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
+    fp8_pages_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                     const GatherArgs a, int64_t pool_heads, int64_t min_range) {
   using G = FGeo<D, NT>;
-  extern __shared__ int32_t pref[];  // [B + 1]
+  constexpr int NW = G::kWarps, S = G::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  int32_t* pref = reinterpret_cast<int32_t*>(sm + G::kOffPref);  // [B + 1]
+  Part* parts = reinterpret_cast<Part*>(sm + G::kOffList);       // [2 * NW]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gid = lane >> 2, tig = lane & 3;
+  const int hpu = static_cast<int>(a.hpu);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + G::kOffBar) + warp * S;
+  if (lane < S) mbar_init(&full[lane], 1);
+  if (lane < 2) parts[2 * warp + lane].where = -1;
+  fence_mbar_init();
   pdl_launch_dependents();  // the combine kernel may start launching (it waits for this grid)
 
   // ---- tile space (every CTA computes it) ----------------------------------------------
@@ -160,303 +169,434 @@ __global__ void __launch_bounds__(kCtaWarps * 32, FGeo<D, NT>::kCtas)
   }
   __syncthreads();
   const int64_t total = a.Hkv * static_cast<int64_t>(pref[a.B]);
-  const int64_t gw_total = static_cast<int64_t>(gridDim.x) * kCtaWarps;
+  const int64_t gw_total = static_cast<int64_t>(gridDim.x) * NW;
   int64_t R = (total + gw_total - 1) / gw_total;
   if (R < min_range) R = min_range;
   if (blockIdx.x == 0) {
+    // the combine kernel sees the CTAs as its "warps"
     for (int64_t b = threadIdx.x; b <= a.B; b += blockDim.x) a.pref_out[b] = pref[b];
-    if (threadIdx.x == 0) a.meta[0] = R;
+    if (threadIdx.x == 0) a.meta[0] = R * NW;
     // sequences without tiles still need a (zero) output
     for (int64_t e = threadIdx.x; e < a.B * a.Hq * D; e += blockDim.x) {
       const int64_t b = e / (a.Hq * D);
       if (pref[b + 1] == pref[b]) static_cast<T*>(a.y)[e] = from_f32<T>(0.f);
     }
   }
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kCtaWarps + warp;
-  if (gw * R >= total) return;
-  const int32_t t_begin = static_cast<int32_t>(gw * R);
-  const int32_t t_end = static_cast<int32_t>(min(gw * R + R, total));
+  const int64_t c_begin = static_cast<int64_t>(blockIdx.x) * NW * R;
+  if (c_begin >= total) return;  // the whole CTA
+  const int32_t c_end = static_cast<int32_t>(min(c_begin + NW * R, total));
+  const int32_t t_begin = static_cast<int32_t>(min(c_begin + warp * R, total));
+  const int32_t t_end = static_cast<int32_t>(min(c_begin + (warp + 1) * R, total));
 
-  const int pt = static_cast<int>(a.page_tokens);
-  const int64_t page_bytes = a.page_tokens * (D + 1);
-  const uint32_t sub = static_cast<uint32_t>(a.Hkv / pool_heads);
-  const uint8_t* kp = static_cast<const uint8_t*>(a.k);
-  const uint8_t* vp = static_cast<const uint8_t*>(a.v);
+  if (t_begin < t_end) {
+    uint8_t* ring = sm + warp * S * G::kStageBytes;
+    uint8_t* scales = sm + G::kOffScale + warp * S * 32;
+    const uint32_t ring_s = smem_u32(ring), scales_s = smem_u32(scales);
+    const uint32_t pt = static_cast<uint32_t>(a.page_tokens);
+    const int64_t page_bytes = a.page_tokens * (D + 1);
+    const uint32_t sub = static_cast<uint32_t>(a.Hkv / pool_heads);
+    const uint8_t* kp = static_cast<const uint8_t*>(a.k);
+    const uint8_t* vp = static_cast<const uint8_t*>(a.v);
 
-  // Byte offset of tile t's page (of its head), and its first slot; negative
-  // when the table entry is bad.
-  auto page_of = [&](const Unit& un, int32_t t, int& slot) -> int64_t {
-    const uint32_t tok = static_cast<uint32_t>(t - un.off) * 16u;
-    const uint32_t pi = tok / static_cast<uint32_t>(pt);
-    slot = static_cast<int>(tok - pi * static_cast<uint32_t>(pt));
-    const int32_t page = __ldg(a.block_table + un.b * a.max_pages + pi);
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0 && a.err_word) atomicOr(a.err_word, SA_ERRBIT_PAGE);
-      return -1;
-    }
-    return (page * pool_heads + static_cast<uint32_t>(un.grp) / sub) * page_bytes;
-  };
-  auto load_k = [&](int64_t off, int slot, KTile<D>& k) {
-    const uint8_t* row = kp + off + (slot + gid) * D + 16 * tig;
+    // The issue side: a tile's table entry is loaded a step before its copies.
+    struct Ahead {
+      int32_t page, slot, head;
+    };
+    Unit nxt = unit_at(a, pref, t_begin);
+    auto look = [&](int32_t t) {
+      if (t >= nxt.off + nxt.tu) nxt = unit_at(a, pref, t);
+      const uint32_t tok = static_cast<uint32_t>(t - nxt.off) * 16u, pi = tok / pt;
+      Ahead h;
+      h.slot = static_cast<int32_t>(tok - pi * pt);
+      h.head = static_cast<int32_t>(static_cast<uint32_t>(nxt.grp) / sub);
+      h.page = __ldg(a.block_table + nxt.b * a.max_pages + pi);
+      return h;
+    };
+    uint32_t good = 0;  // bit per stage: its page exists
+    auto issue = [&](int stage, const Ahead& h) {
+      const bool ok = h.page >= 0 && h.page < a.num_pages;
+      good = ok ? good | (1u << stage) : good & ~(1u << stage);
+      fence_proxy_async_smem();  // this warp's reads of the stage precede the refill
+      __syncwarp();
+      if (lane == 0) {
+        uint64_t* bar = &full[stage];
+        if (ok) {
+          const int64_t ph = h.page * pool_heads + h.head;
+          uint8_t* dst = ring + stage * G::kStageBytes;
+          mbar_arrive_expect_tx(bar, G::kStageBytes + 32);
 #pragma unroll
-    for (int i = 0; i < G::kKv; ++i) {
-      k.x[0][i] = ld_stream16(row + 64 * i);
-      k.x[1][i] = ld_stream16(row + 8 * D + 64 * i);
-    }
-    const uint8_t* sc = kp + off + pt * D + slot + gid;
-    k.s[0] = __ldg(sc);
-    k.s[1] = __ldg(sc + 8);
-  };
-  auto load_v = [&](int64_t off, int slot, VTile<D>& v) {
-    const uint8_t* row = vp + off + (slot + 2 * tig) * D;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t* r = row + ((i & 1) + (i >> 1) * 8) * D;
-      if (D == 64) {
-        const uint2 w = ld_stream8(r + 8 * gid);
-        v.x[i][0] = w.x;
-        v.x[i][1] = w.y;
-      } else {
-#pragma unroll
-        for (int p = 0; p < D / 128; ++p) {
-          const uint4 w = ld_stream16(r + 128 * p + 16 * gid);
-          v.x[i][4 * p] = w.x;
-          v.x[i][4 * p + 1] = w.y;
-          v.x[i][4 * p + 2] = w.z;
-          v.x[i][4 * p + 3] = w.w;
-        }
-      }
-    }
-    const uint8_t* sc = vp + off + pt * D + slot + gid;
-    v.s[0] = __ldg(sc);
-    v.s[1] = __ldg(sc + 8);
-  };
-
-  // ---- per-unit state ---------------------------------------------------------------------
-  uint32_t qf[NT][G::kKs][2];
-  float mult[NT][2];                 // per head: scale * log2(e) * the query's power of two
-  float o[G::kKs][NT][4];
-  float m_run[NT][2], l_run[NT][2];  // heads 2 tig, 2 tig + 1; l: this lane's tokens
-  Unit cur = unit_at(a, pref, t_begin);
-  const int32_t first_off = cur.off;
-
-  auto start_unit = [&]() {
-    const T* qp = static_cast<const T*>(a.q);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int hh = nt * 8 + gid;
-      const bool live = hh < a.hpu;
-      const T* qr = qp + (cur.b * a.Hq + cur.grp * a.hpu + (live ? hh : 0)) * D;
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < G::kKv; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(to_f32<T>(qr[64 * i + 16 * tig + e])));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // a power of two that puts amax into [2^14, 2^15); kept inside fp32's exponents
-      int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
-      if (amax == 0.f || !(amax <= 3.0e38f)) ex = 0;
-      ex = max(ex, -126);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-#pragma unroll
-      for (int kk = 0; kk < G::kKs; ++kk) {
-        // contraction step kk covers dims 64 (kk / 4) + 16 tig + 4 (kk % 4) + 0 .. 3 of this lane
-        const T* q4 = qr + 64 * (kk / 4) + 16 * tig + 4 * (kk % 4);
-        const float f0 = live ? to_f32<T>(q4[0]) * down : 0.f, f1 = live ? to_f32<T>(q4[1]) * down : 0.f;
-        const float f2 = live ? to_f32<T>(q4[2]) * down : 0.f, f3 = live ? to_f32<T>(q4[3]) * down : 0.f;
-        qf[nt][kk][0] = pack2<__half>(f0, f1);
-        qf[nt][kk][1] = pack2<__half>(f2, f3);
-      }
-      mult[nt][0] = a.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * tig);
-      mult[nt][1] = a.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * tig + 4);
-      m_run[nt][0] = m_run[nt][1] = SA_NEG_INF;
-      l_run[nt][0] = l_run[nt][1] = 0.f;
-#pragma unroll
-      for (int mt = 0; mt < G::kKs; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
-    }
-  };
-
-  // This lane's dims of O tile mt: 2 of them, consecutive.
-  auto dim_of = [&](int mt) {
-    return D == 64 ? 8 * gid + 2 * mt : (mt / 8) * 128 + 16 * gid + 2 * (mt % 8);
-  };
-
-  auto flush_unit = [&]() {
-    const bool whole = cur.off >= t_begin && cur.off + cur.tu <= t_end;
-    const int64_t pbase = (gw * 2 + ((cur.off == first_off) ? 0 : 1)) * a.hpu;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float l = l_run[nt][j];
-#pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
-        const int hh = nt * 8 + 2 * tig + j;
-        if (hh >= a.hpu) continue;
-        if (whole) {
-          const float inv = (m_run[nt][j] == SA_NEG_INF || l == 0.f) ? 0.f : 1.0f / l;
-          T* yp = static_cast<T*>(a.y) + (cur.b * a.Hq + cur.grp * a.hpu + hh) * D;
-#pragma unroll
-          for (int mt = 0; mt < G::kKs; ++mt)
-            *reinterpret_cast<uint32_t*>(yp + dim_of(mt)) =
-                pack2<T>(o[mt][nt][j] * inv, o[mt][nt][2 + j] * inv);
-        } else {
-          float* po = a.part_o + (pbase + hh) * D;
-#pragma unroll
-          for (int mt = 0; mt < G::kKs; ++mt)
-            *reinterpret_cast<float2*>(po + dim_of(mt)) = make_float2(o[mt][nt][j], o[mt][nt][2 + j]);
-          if (gid == 0) {
-            a.part_ml[2 * (pbase + hh)] = m_run[nt][j];
-            a.part_ml[2 * (pbase + hh) + 1] = l;
+          for (int s = 0; s < G::kSlabs; ++s) {
+            tc05::tma_load3(dst + s * 2048, &tk, s * 128, h.slot, static_cast<int>(ph), bar);
+            tc05::tma_load3(dst + G::kTileBytes + s * 2048, &tv, s * 128, h.slot, static_cast<int>(ph), bar);
           }
+          const int64_t so = ph * page_bytes + a.page_tokens * D + h.slot;
+          bulk_g2s(scales + stage * 32, kp + so, 16, bar);
+          bulk_g2s(scales + stage * 32 + 16, vp + so, 16, bar);
+        } else {
+          if (a.err_word) atomicOr(a.err_word, SA_ERRBIT_PAGE);
+          mbar_arrive(bar);
         }
       }
-  };
-
-  // ---- main loop -----------------------------------------------------------------------------
-  KTile<D> kt;
-  VTile<D> vt;
-  Unit nxt = cur;
-  int slot = 0;
-  int64_t off = page_of(cur, t_begin, slot);
-  if (off >= 0) {
-    load_k(off, slot, kt);
-    load_v(off, slot, vt);
-  }
-  start_unit();
-  for (int32_t t = t_begin; t < t_end; ++t) {
-    if (t >= cur.off + cur.tu) {
-      flush_unit();
-      cur = nxt;
-      start_unit();
+    };
+    Unit cur = nxt;
+    const int32_t first_off = cur.off;
+    {
+      Ahead h[S];
+#pragma unroll
+      for (int q = 0; q < S; ++q)
+        if (t_begin + q < t_end) h[q] = look(t_begin + q);
+#pragma unroll
+      for (int q = 0; q < S; ++q)
+        if (t_begin + q < t_end) issue(q, h[q]);
     }
-    const bool have = off >= 0;
-    // the next tile's place (its table entry is on its way during S)
-    int64_t off_n = -1;
-    int slot_n = 0;
-    const bool more = t + 1 < t_end;
-    if (more) {
-      if (t + 1 >= nxt.off + nxt.tu) nxt = unit_at(a, pref, t + 1);
-      off_n = page_of(nxt, t + 1, slot_n);
-    }
-    const int left = cur.ctx - (t - cur.off) * 16;  // tokens from this tile on
-    const bool lo_ok = have && gid < left, hi_ok = have && gid + 8 < left;
+    Ahead next{-1, 0, 0};
+    if (t_begin + S < t_end) next = look(t_begin + S);
 
-    // S^T = K . Q^T over the codes
-    float s[NT][4];
+    // ---- per-unit state -------------------------------------------------------------------
+    uint32_t qf[NT][G::kKs][2];
+    float mult[NT][2];                 // per head: scale * log2(e) * the query's power of two
+    float o[G::kKs][NT][4];
+    float m_run[NT][2], l_run[NT][2];  // heads 2 tig, 2 tig + 1; l: this lane's tokens
+
+    // Dims of contraction step kk that this lane holds: 4 of them, consecutive.
+    auto q_dim = [&](int kk) {
+      return D == 64 ? 16 * tig + 4 * kk : 128 * (kk / 8) + 32 * tig + 4 * (kk % 8);
+    };
+    auto start_unit = [&]() {
+      const T* qp = static_cast<const T*>(a.q);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        const int hh = nt * 8 + gid;
+        const bool live = hh < hpu;
+        const T* qr = qp + (cur.b * a.Hq + cur.grp * a.hpu + (live ? hh : 0)) * D;
+        float amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+        for (int kk = 0; kk < G::kKs; ++kk) {
+          float f[4];
 #pragma unroll
-    for (int i = 0; i < G::kKv; ++i) {
-      const uint32_t w0[4] = {kt.x[0][i].x, kt.x[0][i].y, kt.x[0][i].z, kt.x[0][i].w};
-      const uint32_t w1[4] = {kt.x[1][i].x, kt.x[1][i].y, kt.x[1][i].z, kt.x[1][i].w};
+          for (int e = 0; e < 4; ++e) {
+            f[e] = to_f32<T>(qr[q_dim(kk) + e]);
+            amax = fmaxf(amax, fabsf(f[e]));
+          }
+          // kept raw in T's own 16 bits until the row's maximum is known
+          qf[nt][kk][0] = pack2<T>(f[0], f[1]);
+          qf[nt][kk][1] = pack2<T>(f[2], f[3]);
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // a power of two that puts amax into [2^14, 2^15); kept inside fp32's exponents
+        int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+        if (amax == 0.f || !(amax <= 3.0e38f)) ex = 0;
+        ex = max(ex, -126);
+        const float down = live ? __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : 0.f;
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t a0 = e4m3x2_f16x2(w0[w]), a2 = e4m3x2_f16x2(w0[w] >> 16);
-        const uint32_t a1 = e4m3x2_f16x2(w1[w]), a3 = e4m3x2_f16x2(w1[w] >> 16);
+        for (int kk = 0; kk < G::kKs; ++kk)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma16816<__half>(s[nt], a0, a1, a2, a3, qf[nt][4 * i + w][0], qf[nt][4 * i + w][1]);
+          for (int e = 0; e < 2; ++e) {
+            const T* x = reinterpret_cast<const T*>(&qf[nt][kk][e]);
+            const float lo = to_f32<T>(x[0]), hi = to_f32<T>(x[1]);
+            qf[nt][kk][e] = live ? pack2<__half>(lo * down, hi * down) : 0u;
+          }
+        mult[nt][0] = a.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * tig);
+        mult[nt][1] = a.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * tig + 4);
+        m_run[nt][0] = m_run[nt][1] = SA_NEG_INF;
+        l_run[nt][0] = l_run[nt][1] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < G::kKs; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
       }
-    }
-    const float ks0 = e8m0_f32(kt.s[0]), ks1 = e8m0_f32(kt.s[1]);
-    if (more && off_n >= 0) load_k(off_n, slot_n, kt);
-
-    // scores in log2 units; probabilities against the running maximum
-    const float vs0 = lo_ok ? e8m0_f32(vt.s[0]) : 0.f, vs1 = hi_ok ? e8m0_f32(vt.s[1]) : 0.f;
-    uint32_t ph[NT][2], pl[NT][2];
+    };
+    // This lane's dims of O tile mt: 2 of them, consecutive.
+    auto dim_of = [&](int mt) {
+      return D == 64 ? 8 * gid + 2 * mt : (mt / 8) * 128 + 16 * gid + 2 * (mt % 8);
+    };
+    // End of a unit's tiles in this warp: y when the whole unit lies in this
+    // warp's range, else a partial in shared memory (the first unit's in the
+    // area for partials, the last one's, at the end, over the ring).
+    auto flush_unit = [&]() {
+      const bool whole = cur.off >= t_begin && cur.off + cur.tu <= t_end;
+      const int second = cur.off != first_off;
+      float* po = second ? reinterpret_cast<float*>(ring)
+                         : reinterpret_cast<float*>(sm + G::kOffPart) + warp * G::kPartFloats;
+      const int32_t head0 = static_cast<int32_t>(cur.b * a.Hq + cur.grp * a.hpu);
+      if (!whole && lane == 0)
+        parts[2 * warp + second] = Part{cur.off, cur.tu, head0, static_cast<int32_t>(po - reinterpret_cast<float*>(sm))};
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = s[nt][e] * ((e < 2) ? ks0 : ks1) * mult[nt][e & 1];
-        s[nt][e] = ((e < 2) ? lo_ok : hi_ok) ? x : SA_NEG_INF;
-      }
-      // (a NaN score raises nothing and makes its row NaN through p)
-      const bool raise = fmaxf(s[nt][0], s[nt][2]) > m_run[nt][0] + kRaiseLog2 ||
-                         fmaxf(s[nt][1], s[nt][3]) > m_run[nt][1] + kRaiseLog2 ||
-                         m_run[nt][0] == SA_NEG_INF || m_run[nt][1] == SA_NEG_INF;
-      if (__any_sync(0xffffffffu, raise)) {
-        float al[2];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          // a row of nothing but NaN scores still gets a finite maximum, so that its
-          // NaN sum is not taken for an empty one
-          const float x0 = s[nt][j], x1 = s[nt][2 + j];
-          float tm = fmaxf(x0 == x0 ? x0 : 0.f, x1 == x1 ? x1 : 0.f);
+          float l = l_run[nt][j];
 #pragma unroll
-          for (int sh = 4; sh < 32; sh <<= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, sh));
-          const float mn = fmaxf(m_run[nt][j], tm);
-          al[j] = mn == SA_NEG_INF ? 1.f : ex2(m_run[nt][j] - mn);
-          m_run[nt][j] = mn;
-          l_run[nt][j] *= al[j];
+          for (int sh = 4; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+          const int hh = nt * 8 + 2 * tig + j;
+          if (hh >= hpu) continue;
+          if (whole) {
+            const float inv = (m_run[nt][j] == SA_NEG_INF || l == 0.f) ? 0.f : 1.0f / l;
+            T* yp = static_cast<T*>(a.y) + static_cast<int64_t>(head0 + hh) * D;
+#pragma unroll
+            for (int mt = 0; mt < G::kKs; ++mt)
+              *reinterpret_cast<uint32_t*>(yp + dim_of(mt)) = pack2<T>(o[mt][nt][j] * inv, o[mt][nt][2 + j] * inv);
+          } else {
+#pragma unroll
+            for (int mt = 0; mt < G::kKs; ++mt)
+              *reinterpret_cast<float2*>(po + hh * D + dim_of(mt)) = make_float2(o[mt][nt][j], o[mt][nt][2 + j]);
+            if (gid == 0) {
+              po[G::kHeads * D + 2 * hh] = m_run[nt][j];
+              po[G::kHeads * D + 2 * hh + 1] = l;
+            }
+          }
         }
+    };
+
+    // ---- main loop -----------------------------------------------------------------------------
+    start_unit();
+    bool timed_out = false;
+    int stage = 0;
+    uint32_t parity = 0;
+#pragma unroll 1
+    for (int32_t t = t_begin; t < t_end; ++t) {
+      if (t >= cur.off + cur.tu) {
+        flush_unit();
+        cur = unit_at(a, pref, t);
+        start_unit();
+      }
+      if (!mbar_wait(&full[stage], parity)) timed_out = true;
+      const bool have = (good >> stage) & 1u;
+      const int left = cur.ctx - (t - cur.off) * 16;  // tokens from this tile on
+      const bool lo_ok = have && gid < left, hi_ok = have && gid + 8 < left;
+      const uint32_t kt = ring_s + stage * G::kStageBytes, vt = kt + G::kTileBytes;
+      const uint32_t sc = scales_s + stage * 32 + gid;
+      auto lds16 = [](uint32_t addr) {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+        return v;
+      };
+      auto lds1 = [](uint32_t addr) {
+        uint32_t v;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+        return v;
+      };
+      const uint32_t kb0 = lds1(sc), kb1 = lds1(sc + 8), vb0 = lds1(sc + 16), vb1 = lds1(sc + 24);
+
+      // S^T = K . Q^T over the codes: rows gid and gid + 8, 16 dims per load
+      float s[NT][4];
 #pragma unroll
-        for (int mt = 0; mt < G::kKs; ++mt) {
-          o[mt][nt][0] *= al[0];
-          o[mt][nt][1] *= al[1];
-          o[mt][nt][2] *= al[0];
-          o[mt][nt][3] *= al[1];
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        uint32_t at;
+        if (D == 64) at = gid * 64 + ((tig ^ ((gid >> 1) & 3)) << 4);
+        else at = (i >> 1) * 2048 + gid * 128 + (((2 * tig + (i & 1)) ^ gid) << 4);
+        const uint4 r0 = lds16(kt + at), r1 = lds16(kt + at + (D == 64 ? 512 : 1024));
+        const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t a0 = e4m3x2_f16x2(w0[w]), a2 = e4m3x2_f16x2(w0[w] >> 16);
+          const uint32_t a1 = e4m3x2_f16x2(w1[w]), a3 = e4m3x2_f16x2(w1[w] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816<__half>(s[nt], a0, a1, a2, a3, qf[nt][4 * i + w][0], qf[nt][4 * i + w][1]);
         }
       }
-      const float mu0 = m_run[nt][0] == SA_NEG_INF ? 0.f : m_run[nt][0];
-      const float mu1 = m_run[nt][1] == SA_NEG_INF ? 0.f : m_run[nt][1];
-      const float p0 = ex2(s[nt][0] - mu0), p1 = ex2(s[nt][1] - mu1);
-      const float p2 = ex2(s[nt][2] - mu0), p3 = ex2(s[nt][3] - mu1);
-      l_run[nt][0] += p0 + p2;
-      l_run[nt][1] += p1 + p3;
-      const float w0 = p0 * vs0, w1 = p1 * vs0, w2 = p2 * vs1, w3 = p3 * vs1;
-      const uint32_t h01 = pack2<__nv_bfloat16>(w0, w1), h23 = pack2<__nv_bfloat16>(w2, w3);
-      ph[nt][0] = movm_t(h01);
-      ph[nt][1] = movm_t(h23);
-      pl[nt][0] = movm_t(pack2<__nv_bfloat16>(w0 - __uint_as_float(h01 << 16),
-                                              w1 - __uint_as_float(h01 & 0xffff0000u)));
-      pl[nt][1] = movm_t(pack2<__nv_bfloat16>(w2 - __uint_as_float(h23 << 16),
-                                              w3 - __uint_as_float(h23 & 0xffff0000u)));
-    }
-
-    // O^T += V^T . P^T
-    if (have) {
+      // V's codes of tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9: this lane's dims
+      uint32_t vx[4][D / 32];
 #pragma unroll
-      for (int w = 0; w < G::kVw; ++w) {
-        // (tokens 2 tig, 2 tig + 1), (2 tig + 8, 2 tig + 9): dims 4w, 4w + 1 | 4w + 2, 4w + 3
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * tig + (i & 1);  // + 8: the same swizzle phase
+        if (D == 64) {
+          const uint32_t at = vt + ((i >> 1) * 8 + r) * 64 + (((gid >> 1) ^ ((r >> 1) & 3)) << 4) + (gid & 1) * 8;
+          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(vx[i][0]), "=r"(vx[i][1]) : "r"(at));
+        } else {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t sel = half ? 0x7632u : 0x5410u;
-          const uint32_t z0 = __byte_perm(vt.x[0][w], vt.x[1][w], sel);
-          const uint32_t z1 = __byte_perm(vt.x[2][w], vt.x[3][w], sel);
-          const uint32_t a0 = times_2p120(high_codes_bf16x2(z0 << 8));
-          const uint32_t a1 = times_2p120(high_codes_bf16x2(z0));
-          const uint32_t a2 = times_2p120(high_codes_bf16x2(z1 << 8));
-          const uint32_t a3 = times_2p120(high_codes_bf16x2(z1));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816<__nv_bfloat16>(o[2 * w + half][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-            mma16816<__nv_bfloat16>(o[2 * w + half][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+          for (int b = 0; b < D / 128; ++b) {
+            const uint4 v = lds16(vt + b * 2048 + ((i >> 1) * 8 + r) * 128 + ((gid ^ r) << 4));
+            vx[i][4 * b] = v.x;
+            vx[i][4 * b + 1] = v.y;
+            vx[i][4 * b + 2] = v.z;
+            vx[i][4 * b + 3] = v.w;
           }
         }
       }
+
+      // scores in log2 units; probabilities against the running maximum
+      const float ks0 = e8m0_f32(kb0), ks1 = e8m0_f32(kb1);
+      const float vs0 = lo_ok ? e8m0_f32(vb0) : 0.f, vs1 = hi_ok ? e8m0_f32(vb1) : 0.f;
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = s[nt][e] * ((e < 2) ? ks0 : ks1) * mult[nt][e & 1];
+          s[nt][e] = ((e < 2) ? lo_ok : hi_ok) ? x : SA_NEG_INF;
+        }
+        // (a NaN score raises nothing and makes its row NaN through p)
+        const bool raise = fmaxf(s[nt][0], s[nt][2]) > m_run[nt][0] + kRaiseLog2 ||
+                           fmaxf(s[nt][1], s[nt][3]) > m_run[nt][1] + kRaiseLog2 ||
+                           m_run[nt][0] == SA_NEG_INF || m_run[nt][1] == SA_NEG_INF;
+        if (__any_sync(0xffffffffu, raise)) {
+          float al[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            // a row of nothing but NaN scores still gets a finite maximum, so that its
+            // NaN sum is not taken for an empty one
+            const float x0 = s[nt][j], x1 = s[nt][2 + j];
+            float tm = fmaxf(x0 == x0 ? x0 : 0.f, x1 == x1 ? x1 : 0.f);
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, sh));
+            const float mn = fmaxf(m_run[nt][j], tm);
+            al[j] = mn == SA_NEG_INF ? 1.f : ex2(m_run[nt][j] - mn);
+            m_run[nt][j] = mn;
+            l_run[nt][j] *= al[j];
+          }
+#pragma unroll
+          for (int mt = 0; mt < G::kKs; ++mt) {
+            o[mt][nt][0] *= al[0];
+            o[mt][nt][1] *= al[1];
+            o[mt][nt][2] *= al[0];
+            o[mt][nt][3] *= al[1];
+          }
+        }
+        const float mu0 = m_run[nt][0] == SA_NEG_INF ? 0.f : m_run[nt][0];
+        const float mu1 = m_run[nt][1] == SA_NEG_INF ? 0.f : m_run[nt][1];
+        const float p0 = ex2(s[nt][0] - mu0), p1 = ex2(s[nt][1] - mu1);
+        const float p2 = ex2(s[nt][2] - mu0), p3 = ex2(s[nt][3] - mu1);
+        l_run[nt][0] += p0 + p2;
+        l_run[nt][1] += p1 + p3;
+        const float w0 = p0 * vs0, w1 = p1 * vs0, w2 = p2 * vs1, w3 = p3 * vs1;
+        const uint32_t h01 = pack2<__nv_bfloat16>(w0, w1), h23 = pack2<__nv_bfloat16>(w2, w3);
+        ph[nt][0] = movm_t(h01);
+        ph[nt][1] = movm_t(h23);
+        pl[nt][0] = movm_t(pack2<__nv_bfloat16>(w0 - __uint_as_float(h01 << 16),
+                                                w1 - __uint_as_float(h01 & 0xffff0000u)));
+        pl[nt][1] = movm_t(pack2<__nv_bfloat16>(w2 - __uint_as_float(h23 << 16),
+                                                w3 - __uint_as_float(h23 & 0xffff0000u)));
+      }
+
+      // the stage is free: its refill, S tiles on
+      if (t + S < t_end) {
+        const Ahead h = next;
+        if (t + S + 1 < t_end) next = look(t + S + 1);
+        issue(stage, h);
+      }
+
+      // O^T += V^T . P^T
+      if (have) {
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          // (tokens 2 tig, 2 tig + 1), (2 tig + 8, 2 tig + 9): dims 4w, 4w + 1 | 4w + 2, 4w + 3
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t sel = half ? 0x7632u : 0x5410u;
+            const uint32_t z0 = __byte_perm(vx[0][w], vx[1][w], sel);
+            const uint32_t z1 = __byte_perm(vx[2][w], vx[3][w], sel);
+            const uint32_t a0 = times_2p120(high_codes_bf16x2(z0 << 8));
+            const uint32_t a1 = times_2p120(high_codes_bf16x2(z0));
+            const uint32_t a2 = times_2p120(high_codes_bf16x2(z1 << 8));
+            const uint32_t a3 = times_2p120(high_codes_bf16x2(z1));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816<__nv_bfloat16>(o[2 * w + half][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+              mma16816<__nv_bfloat16>(o[2 * w + half][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+            }
+          }
+        }
+      }
+      if (++stage == S) {
+        stage = 0;
+        parity ^= 1u;
+      }
     }
-    if (more && off_n >= 0) load_v(off_n, slot_n, vt);
-    off = off_n;
-    slot = slot_n;
+    if (timed_out && lane == 0 && a.err_word) atomicOr(a.err_word, SA_ERRBIT_TIMEOUT);
+    __syncwarp();  // every lane has read the ring before a partial goes over it
+    flush_unit();
   }
-  flush_unit();
+  __syncthreads();
+
+  // ---- merge of the units that this CTA's warps share ----------------------------------------
+  // The partials are in tile order, a unit's next to one another.
+  const float* fsm = reinterpret_cast<const float*>(sm);
+  for (int e = 0; e < 2 * NW;) {
+    const Part p = parts[e];
+    if (p.where < 0) {
+      ++e;
+      continue;
+    }
+    int last = e;
+    for (int f = e; f < 2 * NW; ++f) {
+      if (parts[f].where < 0) continue;
+      if (parts[f].unit_off != p.unit_off) break;
+      last = f;
+    }
+    const bool whole = p.unit_off >= c_begin && p.unit_off + p.unit_tu <= c_end;
+    // slot 0: the CTA's range begins inside the unit (or with it), else 1
+    const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (c_begin >= p.unit_off ? 0 : 1)) * a.hpu;
+    for (int x = threadIdx.x; x < hpu * (D / 4); x += G::kThreads) {
+      const int hh = x / (D / 4), d = (x - hh * (D / 4)) * 4;
+      float M = SA_NEG_INF;
+      for (int f = e; f <= last; ++f)
+        if (parts[f].where >= 0) M = fmaxf(M, fsm[parts[f].where + G::kHeads * D + 2 * hh]);
+      float L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int f = e; f <= last; ++f) {
+        const int w = parts[f].where;
+        if (w < 0) continue;
+        const float m = fsm[w + G::kHeads * D + 2 * hh];
+        if (m == SA_NEG_INF) continue;
+        const float c = ex2(m - M);
+        const float4 v = *reinterpret_cast<const float4*>(fsm + w + hh * D + d);
+        L += fsm[w + G::kHeads * D + 2 * hh + 1] * c;
+        acc.x = fmaf(v.x, c, acc.x);
+        acc.y = fmaf(v.y, c, acc.y);
+        acc.z = fmaf(v.z, c, acc.z);
+        acc.w = fmaf(v.w, c, acc.w);
+      }
+      if (whole) {
+        const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
+        uint32_t* yp = reinterpret_cast<uint32_t*>(static_cast<T*>(a.y) + static_cast<int64_t>(p.head0 + hh) * D + d);
+        yp[0] = pack2<T>(acc.x * inv, acc.y * inv);
+        yp[1] = pack2<T>(acc.z * inv, acc.w * inv);
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (slot + hh) * D + d) = acc;
+        if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * (slot + hh)) = make_float2(M, L);
+      }
+    }
+    e = last + 1;
+  }
+}
+
+// A pool as rows of codes: [pages * heads, page_tokens, D] bytes, the page stride with
+// its scale bytes; boxes of 16 rows.
+template <int D, int NT>
+bool pool_map(CUtensorMap* m, const void* base, const GatherArgs& a, int64_t pool_heads) {
+  using G = FGeo<D, NT>;
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(a.page_tokens),
+                              static_cast<cuuint64_t>(a.num_pages * pool_heads)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(a.page_tokens * (D + 1))};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(G::kBoxCols), 16, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, int D, int NT>
 int launch_t(const GatherArgs& a, int64_t pool_heads, int sms, cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(a.B + 1) * sizeof(int32_t);
-  // Ranges of at least four tiles: below that a warp's set-up and the merge of
-  // its partial cost more than the tiles.
-  fp8_pages_kernel<T, D, NT><<<static_cast<unsigned>(sms * FGeo<D, NT>::kCtas), kCtaWarps * 32, smem,
-                              st>>>(a, pool_heads, 4);
+  using G = FGeo<D, NT>;
+  CUtensorMap tk, tv;
+  if (!pool_map<D, NT>(&tk, a.k, a, pool_heads) || !pool_map<D, NT>(&tv, a.v, a, pool_heads)) return -1;
+  const size_t smem = 1024 + G::kOffPref + static_cast<size_t>(a.B + 1) * sizeof(int32_t);
+  if (cudaFuncSetAttribute(fp8_pages_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return -1;
+  // Ranges of at least two tiles: below that a warp's set-up and the merge of its
+  // partial cost more than the tiles.
+  fp8_pages_kernel<T, D, NT><<<static_cast<unsigned>(sms), G::kThreads, smem, st>>>(tk, tv, a, pool_heads, 2);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
@@ -472,14 +612,6 @@ int launch_d(const GatherArgs& a, int64_t pool_heads, int sms, cudaStream_t st) 
 }  // namespace
 
 int64_t fp8_pages_max_heads(int D) { return D == 256 ? 8 : 16; }
-
-int64_t fp8_pages_grid_warps(int D, int64_t hpu, int sms) {
-  const bool two = hpu > 8;
-  const int ctas = D == 64    ? (two ? FGeo<64, 2>::kCtas : FGeo<64, 1>::kCtas)
-                   : D == 128 ? (two ? FGeo<128, 2>::kCtas : FGeo<128, 1>::kCtas)
-                              : FGeo<256, 1>::kCtas;
-  return static_cast<int64_t>(sms) * ctas * kCtaWarps;
-}
 
 int launch_fp8_pages(const GatherArgs& a, int64_t pool_heads, int dtype, int sms, cudaStream_t st) {
   if (dtype == SA_F16) return launch_d<__half>(a, pool_heads, sms, st);

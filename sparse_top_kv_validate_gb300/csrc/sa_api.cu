@@ -827,7 +827,7 @@ int attn_prefill(const sa_prefill_params* p, void* stream) {
 // ---- paged decode ------------------------------------------------------------------
 
 // FP8 pages: every CTA keeps the sequences' tile prefix in shared memory.
-constexpr int64_t kFp8PagesMaxBatch = 8192;
+constexpr int64_t kFp8PagesMaxBatch = 4096;
 
 static int check_paged(const sa_paged_params* p, int query = 0) {
   if (!p || !p->q || !p->k_pool || !p->v_pool || !p->block_table || !p->ctx_len ||
@@ -902,14 +902,13 @@ static bool plan_fp8_pages(const sa_paged_params* p, Plan& pl) {
   g.n_groups = g.I = g.Hkv;
   g.units = g.B * g.Hkv;
   const int64_t context = p->max_pages * p->page_tokens;
-  if (context >= (int64_t(1) << 31) || g.units * ((context + 15) / 16) >= (int64_t(1) << 31))
+  if (context >= (int64_t(1) << 31) || p->num_pages * p->Hkv >= (int64_t(1) << 31) ||
+      p->B * p->Hq >= (int64_t(1) << 31) || g.units * ((context + 15) / 16) >= (int64_t(1) << 31))
     return false;
-  const int sms = device_shape().sms;
-  const int64_t warps = sa::fp8_pages_grid_warps(static_cast<int>(p->D), g.hpu, sms);
   size_t off = 0;
   pl.off_meta = off;
   off += align_up(sizeof(int64_t) + static_cast<size_t>(g.B + 1) * sizeof(int32_t));
-  const size_t partials = static_cast<size_t>(warps) * 2 * g.hpu;
+  const size_t partials = static_cast<size_t>(device_shape().sms) * 2 * g.hpu;
   pl.off_part_o = off;
   off += align_up(partials * g.D * sizeof(float));
   pl.off_part_ml = off;

@@ -54,9 +54,8 @@ int launch_kv_read(const KvPagesArgs& a, int dtype, cudaStream_t st);
 // ---- decode over FP8 pages ------------------------------------------------------------
 // GatherArgs of the paged source with Hkv the number of query-head groups
 // (KV heads times sub-groups) and g = hpu heads per group; the stream kernel's
-// combine merges the split units.
+// combine merges the units split across its CTAs (one per SM).
 int64_t fp8_pages_max_heads(int D);           // query heads one group can hold
-int64_t fp8_pages_grid_warps(int D, int64_t hpu, int sms);
 int launch_fp8_pages(const GatherArgs& a, int64_t pool_heads, int dtype, int sms,
                      cudaStream_t st);
 
