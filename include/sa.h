@@ -591,8 +591,7 @@ int attn_prefill(const sa_prefill_params* p, void* stream);
  * pool_format SA_FP8_E4M3_PAGE: quantised pages (q and y SA_F16 or SA_BF16, D
  * 64 / 128 / 256, page_tokens a multiple of 16, B <= 4096, pools 16-byte aligned, options
  * 0); k_new / v_new are quantised as paged_kv_write does.  The codes' values
- * enter the products exactly and the scales in fp32.  E4M3's NaN codes, which
- * paged_kv_write never stores, read as +-480 here.
+ * enter the products exactly and the scales in fp32.
  */
 typedef struct {
   const void* q;

@@ -49,6 +49,7 @@ IDX_BELOW_SENTINEL, IDX_AFTER_PADDING, IDX_OUT_OF_RANGE = 1, 2, 4
 IDX_NOT_INCREASING, IDX_DUPLICATE, IDX_ALL_PADDING = 8, 16, 32
 ERRBIT_WRITE_POS, ERRBIT_PAGE, ERRBIT_TIMEOUT = 64, 128, 256
 ERR_SCRATCH_LIMIT = -9
+ERR_WORKSPACE = -5
 NOALLOC_SCRATCH_BYTES = 16 << 20
 OPT_ROW_COPIES, OPT_FP8_WARP_MMA = 1, 2
 SEL_TIE, SEL_NONFINITE = 1, 2
@@ -197,6 +198,8 @@ def lib_path() -> str:
 def load():
     """Load ``libsa.so`` (built by ``__graft_entry__.build()``); raise if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -600,24 +603,33 @@ def paged_attn_decode(q, k_pool, v_pool, block_table, ctx_len, *, k_new=None, v_
 
 def _paged_fp8_decode(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, scale, err_word,
                       y, workspace, stream, options):
-    B, Hkv, D = q.shape[0], k_pool.shape[1], q.shape[-1]
-    if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[2] != 1):
+    shape = q.shape
+    B, D, Hkv = shape[0], shape[-1], k_pool.shape[1]
+    if not (len(shape) == 3 or (len(shape) == 4 and shape[2] == 1)):
         raise ValueError("q must be [B, Hq, 1, D] or [B, Hq, D]")
-    _same_device(q, k_pool=k_pool, v_pool=v_pool, block_table=block_table, ctx_len=ctx_len,
-                 k_new=k_new, v_new=v_new, err_word=err_word, y=y)
+    device = _same_device(q, (k_pool, v_pool, block_table, ctx_len, k_new, v_new, err_word, y))
     _paged_shapes(B, block_table, ctx_len)
     for n, t in (("k_new", k_new), ("v_new", v_new)):
         if t is not None and (t.dtype != q.dtype or t.numel() != B * Hkv * D):
             raise ValueError(f"{n} must be [B, Hkv, D] of q's dtype")
-    if y is not None and (_dev(y, "y").dtype != q.dtype or y.shape != q.shape):
+    if y is not None and (_dev(y, "y").dtype != q.dtype or y.shape != shape):
         raise ValueError("y must be shaped and typed like q")
-    with _launching(q.device, stream) as s:
+    with _launching(device, stream) as s:
         if y is None:
             y = torch.empty_like(q)
         p = _paged_params(q, k_pool, v_pool, block_table, ctx_len, y, k_new, v_new, scale,
                           err_word, options)
-        need = int(L.paged_attn_decode_workspace(C.byref(p)))
-        ws, nb = _stream_workspace(need, q.device, s, workspace)
+        if workspace is None:
+            # the kept scratch is nearly always large enough: ask only when it is not
+            ws = _kept_workspace(device, s)
+            if ws is not None:
+                p.workspace, p.workspace_bytes = ws.data_ptr(), ws.numel()
+                rc = L.paged_attn_decode(C.byref(p), s)
+                if rc != ERR_WORKSPACE:
+                    _check("paged_attn_decode", rc)
+                    return y
+        ws, nb = _stream_workspace(int(L.paged_attn_decode_workspace(C.byref(p))), device, s,
+                                   workspace)
         p.workspace, p.workspace_bytes = _ptr(ws), nb
         _check("paged_attn_decode", L.paged_attn_decode(C.byref(p), s))
     return y
@@ -848,33 +860,38 @@ def csa_pool_weight(t, *, w=None, stream=None):
 
 # ---- the serving step around a paged cache --------------------------------------------------
 
-_NO_GUARD = contextlib.nullcontext()
-
-
 class _launching:
-    """The tensors' device made current and the launching stream: ``stream``,
-    or the device's current one.  Tensors allocated inside belong to it."""
+    """The tensors' device made current and the launching stream's handle:
+    ``stream``'s, or the device's current one's.  Tensors allocated inside belong
+    to that stream."""
 
-    __slots__ = ("device", "stream", "guard", "on")
+    __slots__ = ("device", "stream", "stack")
 
     def __init__(self, device, stream):
-        self.device, self.stream = device, stream
+        self.device, self.stream, self.stack = device, stream, None
 
     def __enter__(self):
-        same = self.device.index is None or self.device.index == torch.cuda.current_device()
-        self.guard = _NO_GUARD if same else torch.cuda.device(self.device)
-        self.guard.__enter__()
-        if self.stream is None:
-            self.on = _NO_GUARD
+        index = self.device.index
+        if self.stream is None and index == torch.cuda.current_device():
             return torch.cuda.current_stream().cuda_stream
-        self.on = torch.cuda.stream(self.stream)
-        self.on.__enter__()
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(self.device))
+        if self.stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        self.stack.enter_context(torch.cuda.stream(self.stream))
         return self.stream.cuda_stream
 
     def __exit__(self, *exc):
-        self.on.__exit__(*exc)
-        self.guard.__exit__(*exc)
+        if self.stack is not None:
+            self.stack.close()
         return False
+
+
+def _kept_workspace(device, stream):
+    """The scratch kept for calls on ``stream`` (a handle), or None: none yet, or a
+    graph is being captured."""
+    ws = _ws_cache.get(("launch", device.index, stream))
+    return None if ws is None or torch.cuda.is_current_stream_capturing() else ws
 
 
 def _stream_workspace(nbytes, device, stream, workspace):
@@ -899,22 +916,25 @@ def _stream_workspace(nbytes, device, stream, workspace):
 
 
 def _rows(t, name, dtype=None, dims=3):
-    """A CUDA tensor whose last axis is contiguous."""
+    """The shape and strides of a CUDA tensor whose last axis is contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != dims:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != dims:
         raise ValueError(f"{name} must have {dims} axes")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    return t
+    return shape, strides
 
 
-def _same_device(first, **others):
-    for n, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{n} is on {t.device}, not on {first.device}")
+def _same_device(first, others):
+    device = first.device
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"a tensor is on {t.device}, not on {device}")
+    return device
 
 
 def _int32(t, name, numel=None):
@@ -997,89 +1017,87 @@ def rotary_embed(q, k, positions, rope, *, q_out=None, k_out=None, stream=None):
     ``(q_out, k_out)``."""
     L = load()
     dims = 4 if isinstance(q, torch.Tensor) and q.dim() == 4 else 3
-    _rows(q, "q", dims=dims)
-    p = RotaryParams()
-    p.dtype = _dt(q)
-    if k is not None:
-        _rows(k, "k", q.dtype, dims)
+    qs, qst = _rows(q, "q", dims=dims)
+    dtype = _dt(q)
     _dev(positions, "positions")
-    if positions.dtype not in (torch.int32, torch.int64):
+    i64 = positions.dtype == torch.int64
+    if not i64 and positions.dtype != torch.int32:
         raise TypeError("positions must be int32 or int64")
+    ps = tuple(positions.shape)
     if dims == 3:
-        (p.S, p.Hq, p.D), p.B = q.shape, 1
-        batch, axes = (), (0, 1)
-        if positions.shape != (q.shape[0],):
+        B, (S, Hq, D) = 1, qs
+        if ps != (S,):
             raise ValueError("positions must be [T]")
     else:
-        p.B, p.Hq, p.S, p.D = q.shape
-        batch, axes = (q.shape[0],), (0, 2, 1)
-        if positions.shape != (q.shape[2],) and positions.shape != (q.shape[0], q.shape[2]):
+        B, Hq, S, D = qs
+        if ps != (S,) and ps != (B, S):
             raise ValueError("positions must be [S] or [B, S]")
-        p.pos_stride = q.shape[2] if positions.dim() == 2 else 0
+    Hk, kst = 0, None
     if k is not None:
-        same = k.shape[0] == q.shape[0] and k.shape[-1] == q.shape[-1] and \
-            (dims == 3 or k.shape[2] == q.shape[2])
-        if not same:
+        ks, kst = _rows(k, "k", q.dtype, dims)
+        if ks[0] != qs[0] or ks[-1] != D or (dims == 4 and ks[2] != S):
             raise ValueError("q and k must have the same tokens and head size")
-        p.Hk = k.shape[1]
-    _same_device(q, k=k, positions=positions, q_out=q_out, k_out=k_out)
+        Hk = ks[1]
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    device = _same_device(q, (k, positions, q_out, k_out))
     for n, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
-        if o is not None and (t is None or _rows(o, n, q.dtype, dims).shape != t.shape):
+        if o is not None and _rows(o, n, q.dtype, dims)[0] != t.shape:
             raise ValueError(f"{n} must be shaped like its input")
-    with _launching(q.device, stream) as s:
+    with _launching(device, stream) as s:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty(qs, dtype=q.dtype, device=device)
         if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        if q.numel() == 0:
+            k_out = torch.empty(ks, dtype=q.dtype, device=device)
+        table = _rope_arg(rope)
+        if S * B * Hq * D == 0:
             return q_out, k_out
-        p.rope = _rope_arg(rope)
-        p.positions, p.pos_is_i64 = positions.data_ptr(), int(positions.dtype == torch.int64)
-        for x, n in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out")):
-            if x is not None:
-                setattr(p, n, x.data_ptr())
-                st = x.stride()
-                getattr(p, n + "_strides")[:] = ([0] if not batch else []) + [st[i] for i in axes]
+
+        def strides(st):  # batch, token, head
+            return (0, st[0], st[1]) if dims == 3 else (st[0], st[2], st[1])
+
+        none = (0, 0, 0)
+        p = RotaryParams(
+            q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), positions.data_ptr(), table,
+            dtype, int(i64), B, S, Hq, Hk, D, S if len(ps) == 2 else 0, strides(qst),
+            strides(kst) if Hk else none, strides(q_out.stride()),
+            strides(k_out.stride()) if Hk else none)
         _check("rotary_embed", L.rotary_embed(C.byref(p), s))
     return q_out, k_out
 
 
-def _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, err_word):
-    _rows(k, "k")
-    _rows(v, "v", k.dtype)
-    if v.shape != k.shape:
+def _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, rope, err_word):
+    """(parameters, device) of a page write or read-back."""
+    shape, kst = _rows(k, "k")
+    vshape, vst = _rows(v, "v", k.dtype)
+    if vshape != shape:
         raise ValueError("k and v must have the same shape")
-    for n, t in (("k_pool", k_pool), ("v_pool", v_pool), ("err_word", err_word)):
-        _dev(t, n)
+    _dev(k_pool, "k_pool")
+    _dev(v_pool, "v_pool")
+    _dev(err_word, "err_word")
     _int32(block_table, "block_table")
     _int32(ctx_len, "ctx_len")
     B = ctx_len.numel()
     _paged_shapes(B, block_table, ctx_len)
     if seq_start is not None:
         _int32(seq_start, "seq_start", B + 1)
-    _same_device(k, v=v, k_pool=k_pool, v_pool=v_pool, block_table=block_table, ctx_len=ctx_len,
-                 seq_start=seq_start, err_word=err_word)
-    p = KvPagesParams()
-    p.T, p.Hkv, p.D = k.shape
-    p.dtype = _dt(k)
+    device = _same_device(k, (v, k_pool, v_pool, block_table, ctx_len, seq_start, err_word))
+    T, Hkv, D = shape
+    pool = k_pool.shape
     if k_pool.dtype == torch.uint8:
-        p.pool_format = FP8_E4M3_PAGE
-        p.page_tokens = _fp8_page_tokens(k_pool, v_pool, k.shape[2])
+        fmt, page_tokens = FP8_E4M3_PAGE, _fp8_page_tokens(k_pool, v_pool, D)
     else:
-        if k_pool.dim() != 4 or k_pool.dtype != k.dtype or v_pool.dtype != k.dtype or \
-                v_pool.shape != k_pool.shape or k_pool.shape[3] != k.shape[2]:
+        if len(pool) != 4 or k_pool.dtype != k.dtype or v_pool.dtype != k.dtype or \
+                v_pool.shape != pool or pool[3] != D:
             raise ValueError("pools must be [num_pages, Hkv, page_tokens, D] of the rows' dtype, "
                              "or FP8 pools")
-        p.page_tokens = k_pool.shape[2]
-    if k_pool.shape[1] != k.shape[1]:
+        fmt, page_tokens = 0, pool[2]
+    if pool[1] != Hkv:
         raise ValueError("the pools and the rows have different head counts")
-    p.k, p.v, p.k_pool, p.v_pool = k.data_ptr(), v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr()
-    p.block_table, p.ctx_len = block_table.data_ptr(), ctx_len.data_ptr()
-    p.seq_start, p.err_word = _ptr(seq_start), _ptr(err_word)
-    p.B, p.max_pages, p.num_pages = B, block_table.shape[1], k_pool.shape[0]
-    p.k_strides[:] = k.stride()[:2]
-    p.v_strides[:] = v.stride()[:2]
-    return p
+    return KvPagesParams(
+        k.data_ptr(), v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
+        ctx_len.data_ptr(), _ptr(seq_start), _rope_arg(rope), _ptr(err_word), _dt(k), fmt, T, B,
+        Hkv, D, page_tokens, block_table.shape[1], pool[0], kst[:2], vst[:2]), device
 
 
 def paged_kv_write(k, v, k_pool, v_pool, block_table, ctx_len, seq_start=None, *, rope=None,
@@ -1091,13 +1109,13 @@ def paged_kv_write(k, v, k_pool, v_pool, block_table, ctx_len, seq_start=None, *
     ``seq_start[b] .. seq_start[b+1]`` (int32 ``[B+1]``; None: one row each), the last tokens of
     its ``ctx_len[b]`` (int32 ``[B]``, the new tokens counted)."""
     L = load()
-    p = _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, err_word)
-    if seq_start is None and k.shape[0] != ctx_len.numel():
+    p, device = _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, rope,
+                                 err_word)
+    if seq_start is None and p.T != p.B:
         raise ValueError("without seq_start every sequence has one row")
-    if k.numel() == 0:
+    if p.T * p.Hkv * p.D == 0:
         return
-    p.rope = _rope_arg(rope)
-    with _launching(k.device, stream) as s:
+    with _launching(device, stream) as s:
         _check("paged_kv_write", L.paged_kv_write(C.byref(p), s))
 
 
@@ -1120,8 +1138,9 @@ def paged_kv_read(k_pool, v_pool, block_table, ctx_len, seq_start, k=None, v=Non
             v = torch.zeros(shape, dtype=dtype, device=k_pool.device)
         if seq_start is None:
             raise ValueError("seq_start is required")
-        p = _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, err_word)
-        if k.numel() == 0:
+        p, _ = _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, None,
+                                err_word)
+        if p.T * p.Hkv * p.D == 0:
             return k, v
         _check("paged_kv_read", L.paged_kv_read(C.byref(p), s))
     return k, v
@@ -1136,42 +1155,34 @@ def attn_prefill_packed(q, k, v, q_start, k_start=None, *, causal=True, scale=0.
     of the context (causal: query i sees keys ``<= i + nk - nq``); a query that sees no key gives
     0.  Rows behind the last sequence are not written.  Returns ``y [Tq, Hq, D]``."""
     L = load()
-    _rows(q, "q")
-    _rows(k, "k", q.dtype)
-    _rows(v, "v", q.dtype)
-    if v.shape != k.shape or k.shape[2] != q.shape[2]:
+    qs, qst = _rows(q, "q")
+    ks, kst = _rows(k, "k", q.dtype)
+    vs, vst = _rows(v, "v", q.dtype)
+    Tq, Hq, D = qs
+    Tk, Hkv, _ = ks
+    if vs != ks or ks[2] != D:
         raise ValueError("k and v must have the same shape, and q's head size")
     _int32(q_start, "q_start")
     B = q_start.numel() - 1
     if k_start is not None:
         _int32(k_start, "k_start", B + 1)
-    elif k.shape[0] != q.shape[0]:
+    elif Tk != Tq:
         raise ValueError("k_start is required when q and k have different rows")
     _dev(err_word, "err_word")
-    _same_device(q, k=k, v=v, q_start=q_start, k_start=k_start, err_word=err_word, y=y)
-    if y is not None and _rows(y, "y", q.dtype).shape != q.shape:
+    device = _same_device(q, (k, v, q_start, k_start, err_word, y))
+    if y is not None and _rows(y, "y", q.dtype)[0] != qs:
         raise ValueError("y must be shaped like q")
-    with _launching(q.device, stream) as s:
+    with _launching(device, stream) as s:
         if y is None:
-            y = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if q.numel() == 0:
+            y = torch.empty(qs, dtype=q.dtype, device=device)
+        if Tq * Hq * D == 0:
             return y
-        if k.numel() == 0:  # no keys anywhere: an empty tensor has no address to give
-            k = v = torch.empty((1,) + tuple(k.shape[1:]), dtype=q.dtype, device=q.device)
-            k_rows = 0
-        else:
-            k_rows = k.shape[0]
-        p = PackedParams()
-        p.q, p.k, p.v, p.y = q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr()
-        p.q_start, p.k_start, p.err_word = q_start.data_ptr(), _ptr(k_start), _ptr(err_word)
-        p.dtype, p.causal = _dt(q), int(bool(causal))
-        p.B, p.Tk = B, k_rows
-        p.Tq, p.Hq, p.D = q.shape
-        p.Hkv = k.shape[1]
-        p.scale, p.softcap = float(scale), float(softcap)
-        p.q_strides[:] = q.stride()[:2]
-        p.k_strides[:] = k.stride()[:2]
-        p.v_strides[:] = v.stride()[:2]
-        p.y_strides[:] = y.stride()[:2]
+        if Tk == 0:  # no keys anywhere: an empty tensor has no address to give
+            k = v = torch.empty((1, Hkv, D), dtype=q.dtype, device=device)
+            kst = vst = k.stride()
+        p = PackedParams(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), q_start.data_ptr(),
+            _ptr(k_start), _ptr(err_word), _dt(q), int(bool(causal)), B, Tq, Tk, Hq, Hkv, D,
+            qst[:2], kst[:2], vst[:2], y.stride()[:2], float(scale), float(softcap))
         _check("attn_prefill_packed", L.attn_prefill_packed(C.byref(p), s))
     return y

@@ -919,14 +919,6 @@ const double* tanh_coefficients() {
   return c;
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
 // Shared memory with `seqs` sequences and `items` places in the item list.
 template <int D>
 int64_t smem_bytes(int64_t seqs, int64_t items) {
@@ -980,8 +972,7 @@ int launch_t(const PackedArgs& a, cudaStream_t st) {
   auto kern = variant == kVarPlain    ? packed_tc05_kernel<D, T, kVarPlain>
               : variant == kVarCapMax ? packed_tc05_kernel<D, T, kVarCapMax>
                                       : packed_tc05_kernel<D, T, kVarCapFixed>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
-    return -1;
+  if (!allow_smem(reinterpret_cast<const void*>(kern))) return -1;
   for (int64_t b0 = 0; b0 < a.B; b0 += kMaxSeqs) {
     const int64_t seqs = a.B - b0 < kMaxSeqs ? a.B - b0 : kMaxSeqs;
     const int64_t items = items_bound(a, seqs);

@@ -23,15 +23,16 @@
 //    so bf16 and f16 queries lose nothing that fp32 sums would keep (an
 //    element 2^-39 below the row's largest is rounded).  The key's scale and
 //    the head's power of two multiply the fp32 score.
-//  * V: codes become bf16 by moving their bits (exponent and mantissa shifted
-//    into place give value * 2^-120; one multiplication by 2^120, exact).  The
-//    value's scale is folded into the probability, p 2^(ev), which bf16's range
-//    always holds; it is split into two bf16 (hi + lo, 16 bits), so that the
-//    probability's rounding stays far below the output's.
+//  * V: the codes become f16 the same way (exact).  The value's scale is folded
+//    into the probability: w = p 2^(ev - E), E a power of two per head that is
+//    raised when w passes 2^12 (O then follows, exactly), so that f16 holds every
+//    weight to 2^-25 of about the largest; it is split into two f16 (hi + lo, 22
+//    bits), so that its rounding stays far below the output's.  (V as bf16, whose
+//    range needs no E, costs 96 more integer instructions of 620 per tile.)
 //  * The running maximum is raised only when a score exceeds it by 2^8 (one
 //    vote per tile instead of a reduction and a rescale).
 //  * A unit split across warps is merged in shared memory by its CTA; only one
-//    split across CTAs leaves partials, one per CTA, for stream_combine_kernel.
+//    split across CTAs leaves partials, one per CTA, for fp8_combine_kernel.
 //    (With a partial per warp the merge of a 131,072-token context, 282 partials
 //    per unit, took longer than the attention.)
 #include "gather_common.cuh"
@@ -43,6 +44,7 @@ namespace sa {
 namespace {
 
 constexpr float kRaiseLog2 = 8.0f;
+constexpr float kWeightMax = 4096.0f;  // of a value weight before its head's E is raised
 
 template <int D, int NT>
 struct FGeo {
@@ -71,18 +73,6 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
   uint32_t h;
   asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
   return h;
-}
-
-// The codes in the high bytes of the two halves of z -> two bf16 of value * 2^-120.
-__device__ __forceinline__ uint32_t high_codes_bf16x2(uint32_t z) {
-  return (z & 0x80008000u) | ((z >> 4) & 0x07F007F0u);
-}
-
-__device__ __forceinline__ uint32_t times_2p120(uint32_t v) {
-  const uint32_t c = 0x7B807B80u;  // bf16 2^120, twice
-  __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                             *reinterpret_cast<const __nv_bfloat162*>(&c));
-  return *reinterpret_cast<uint32_t*>(&r);
 }
 
 // 2^(byte - 127); NaN for 255.
@@ -203,13 +193,28 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
       int32_t page, slot, head;
     };
     Unit nxt = unit_at(a, pref, t_begin);
-    auto look = [&](int32_t t) {
-      if (t >= nxt.off + nxt.tu) nxt = unit_at(a, pref, t);
+    const int32_t* table;             // next entry to look at
+    int32_t n_slot, n_head, n_left;   // slot in its page, head, tiles of the unit to go
+    auto enter = [&](int32_t t) {
       const uint32_t tok = static_cast<uint32_t>(t - nxt.off) * 16u, pi = tok / pt;
-      Ahead h;
-      h.slot = static_cast<int32_t>(tok - pi * pt);
-      h.head = static_cast<int32_t>(static_cast<uint32_t>(nxt.grp) / sub);
-      h.page = __ldg(a.block_table + nxt.b * a.max_pages + pi);
+      n_slot = static_cast<int32_t>(tok - pi * pt);
+      n_head = static_cast<int32_t>(static_cast<uint32_t>(nxt.grp) / sub);
+      n_left = nxt.off + nxt.tu - t;
+      table = a.block_table + nxt.b * a.max_pages + pi;
+    };
+    enter(t_begin);
+    auto look = [&](int32_t t) {
+      if (n_left == 0) {
+        nxt = unit_at(a, pref, t);
+        enter(t);
+      }
+      const Ahead h{__ldg(table), n_slot, n_head};
+      n_slot += 16;
+      if (n_slot == static_cast<int32_t>(pt)) {
+        n_slot = 0;
+        ++table;
+      }
+      --n_left;
       return h;
     };
     uint32_t good = 0;  // bit per stage: its page exists
@@ -257,6 +262,9 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
     float mult[NT][2];                 // per head: scale * log2(e) * the query's power of two
     float o[G::kKs][NT][4];
     float m_run[NT][2], l_run[NT][2];  // heads 2 tig, 2 tig + 1; l: this lane's tokens
+    float down_v[NT][2];               // 2^-E of the value weights (0: none yet)
+    int left = 0;                      // tokens of the unit from this tile on
+    bool fresh = true;                 // a head has no maximum or no E yet
 
     // Dims of contraction step kk that this lane holds: 4 of them, consecutive.
     auto q_dim = [&](int kk) {
@@ -302,11 +310,13 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
         mult[nt][1] = a.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * tig + 4);
         m_run[nt][0] = m_run[nt][1] = SA_NEG_INF;
         l_run[nt][0] = l_run[nt][1] = 0.f;
+        down_v[nt][0] = down_v[nt][1] = 0.f;
 #pragma unroll
         for (int mt = 0; mt < G::kKs; ++mt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
       }
+      fresh = true;
     };
     // This lane's dims of O tile mt: 2 of them, consecutive.
     auto dim_of = [&](int mt) {
@@ -332,8 +342,9 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
           for (int sh = 4; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
           const int hh = nt * 8 + 2 * tig + j;
           if (hh >= hpu) continue;
+          const float up_v = down_v[nt][j] == 0.f ? 1.0f : 1.0f / down_v[nt][j];  // 2^E
           if (whole) {
-            const float inv = (m_run[nt][j] == SA_NEG_INF || l == 0.f) ? 0.f : 1.0f / l;
+            const float inv = (m_run[nt][j] == SA_NEG_INF || l == 0.f) ? 0.f : up_v / l;
             T* yp = static_cast<T*>(a.y) + static_cast<int64_t>(head0 + hh) * D;
 #pragma unroll
             for (int mt = 0; mt < G::kKs; ++mt)
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
           } else {
 #pragma unroll
             for (int mt = 0; mt < G::kKs; ++mt)
-              *reinterpret_cast<float2*>(po + hh * D + dim_of(mt)) = make_float2(o[mt][nt][j], o[mt][nt][2 + j]);
+              *reinterpret_cast<float2*>(po + hh * D + dim_of(mt)) = make_float2(o[mt][nt][j] * up_v, o[mt][nt][2 + j] * up_v);
             if (gid == 0) {
               po[G::kHeads * D + 2 * hh] = m_run[nt][j];
               po[G::kHeads * D + 2 * hh + 1] = l;
@@ -352,19 +363,20 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
 
     // ---- main loop -----------------------------------------------------------------------------
     start_unit();
+    left = cur.ctx - (t_begin - cur.off) * 16;
     bool timed_out = false;
     int stage = 0;
     uint32_t parity = 0;
 #pragma unroll 1
-    for (int32_t t = t_begin; t < t_end; ++t) {
-      if (t >= cur.off + cur.tu) {
+    for (int32_t t = t_begin; t < t_end; ++t, left -= 16) {
+      if (left <= 0) {
         flush_unit();
         cur = unit_at(a, pref, t);
+        left = cur.ctx;
         start_unit();
       }
       if (!mbar_wait(&full[stage], parity)) timed_out = true;
       const bool have = (good >> stage) & 1u;
-      const int left = cur.ctx - (t - cur.off) * 16;  // tokens from this tile on
       const bool lo_ok = have && gid < left, hi_ok = have && gid + 8 < left;
       const uint32_t kt = ring_s + stage * G::kStageBytes, vt = kt + G::kTileBytes;
       const uint32_t sc = scales_s + stage * 32 + gid;
@@ -422,33 +434,48 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
         }
       }
 
-      // scores in log2 units; probabilities against the running maximum
+      if (left < 16) {
+        // slots past the context: their codes may be NaN, and 0 times NaN is NaN
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (2 * tig + (i & 1) + (i >> 1) * 8 >= left)
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) vx[i][w] = 0u;
+      }
+
+      // scores in log2 units less the running maximum; probabilities
       const float ks0 = e8m0_f32(kb0), ks1 = e8m0_f32(kb1);
       const float vs0 = lo_ok ? e8m0_f32(vb0) : 0.f, vs1 = hi_ok ? e8m0_f32(vb1) : 0.f;
-      uint32_t ph[NT][2], pl[NT][2];
+      bool raise = fresh;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = s[nt][e] * ((e < 2) ? ks0 : ks1) * mult[nt][e & 1];
-          s[nt][e] = ((e < 2) ? lo_ok : hi_ok) ? x : SA_NEG_INF;
-        }
+        const float mu0 = m_run[nt][0] == SA_NEG_INF ? 0.f : m_run[nt][0];
+        const float mu1 = m_run[nt][1] == SA_NEG_INF ? 0.f : m_run[nt][1];
+        s[nt][0] = lo_ok ? fmaf(s[nt][0], ks0 * mult[nt][0], -mu0) : SA_NEG_INF;
+        s[nt][1] = lo_ok ? fmaf(s[nt][1], ks0 * mult[nt][1], -mu1) : SA_NEG_INF;
+        s[nt][2] = hi_ok ? fmaf(s[nt][2], ks1 * mult[nt][0], -mu0) : SA_NEG_INF;
+        s[nt][3] = hi_ok ? fmaf(s[nt][3], ks1 * mult[nt][1], -mu1) : SA_NEG_INF;
         // (a NaN score raises nothing and makes its row NaN through p)
-        const bool raise = fmaxf(s[nt][0], s[nt][2]) > m_run[nt][0] + kRaiseLog2 ||
-                           fmaxf(s[nt][1], s[nt][3]) > m_run[nt][1] + kRaiseLog2 ||
-                           m_run[nt][0] == SA_NEG_INF || m_run[nt][1] == SA_NEG_INF;
-        if (__any_sync(0xffffffffu, raise)) {
+        raise = raise || fmaxf(max3(s[nt][0], s[nt][1], s[nt][2]), s[nt][3]) > kRaiseLog2;
+      }
+      if (__any_sync(0xffffffffu, raise) && have) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
           float al[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // a row of nothing but NaN scores still gets a finite maximum, so that its
             // NaN sum is not taken for an empty one
+            const float mu = m_run[nt][j] == SA_NEG_INF ? 0.f : m_run[nt][j];
             const float x0 = s[nt][j], x1 = s[nt][2 + j];
             float tm = fmaxf(x0 == x0 ? x0 : 0.f, x1 == x1 ? x1 : 0.f);
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, sh));
-            const float mn = fmaxf(m_run[nt][j], tm);
+            const float mn = fmaxf(m_run[nt][j], tm + mu);
             al[j] = mn == SA_NEG_INF ? 1.f : ex2(m_run[nt][j] - mn);
+            const float d = mn == SA_NEG_INF ? 0.f : mu - mn;
+            s[nt][j] += d;
+            s[nt][2 + j] += d;
             m_run[nt][j] = mn;
             l_run[nt][j] *= al[j];
           }
@@ -460,20 +487,63 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
             o[mt][nt][3] *= al[1];
           }
         }
-        const float mu0 = m_run[nt][0] == SA_NEG_INF ? 0.f : m_run[nt][0];
-        const float mu1 = m_run[nt][1] == SA_NEG_INF ? 0.f : m_run[nt][1];
-        const float p0 = ex2(s[nt][0] - mu0), p1 = ex2(s[nt][1] - mu1);
-        const float p2 = ex2(s[nt][2] - mu0), p3 = ex2(s[nt][3] - mu1);
+      }
+      float wt[NT][4];  // value weights p 2^(ev)
+      raise = fresh;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float p0 = ex2(s[nt][0]), p1 = ex2(s[nt][1]), p2 = ex2(s[nt][2]), p3 = ex2(s[nt][3]);
         l_run[nt][0] += p0 + p2;
         l_run[nt][1] += p1 + p3;
-        const float w0 = p0 * vs0, w1 = p1 * vs0, w2 = p2 * vs1, w3 = p3 * vs1;
-        const uint32_t h01 = pack2<__nv_bfloat16>(w0, w1), h23 = pack2<__nv_bfloat16>(w2, w3);
-        ph[nt][0] = movm_t(h01);
-        ph[nt][1] = movm_t(h23);
-        pl[nt][0] = movm_t(pack2<__nv_bfloat16>(w0 - __uint_as_float(h01 << 16),
-                                                w1 - __uint_as_float(h01 & 0xffff0000u)));
-        pl[nt][1] = movm_t(pack2<__nv_bfloat16>(w2 - __uint_as_float(h23 << 16),
-                                                w3 - __uint_as_float(h23 & 0xffff0000u)));
+        wt[nt][0] = p0 * vs0;
+        wt[nt][1] = p1 * vs0;
+        wt[nt][2] = p2 * vs1;
+        wt[nt][3] = p3 * vs1;
+        raise = raise || fmaxf(wt[nt][0], wt[nt][2]) * down_v[nt][0] > kWeightMax ||
+                fmaxf(wt[nt][1], wt[nt][3]) * down_v[nt][1] > kWeightMax;
+      }
+      if (__any_sync(0xffffffffu, raise) && have) {
+        fresh = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float al[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float w = fmaxf(wt[nt][j], wt[nt][2 + j]);
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, sh));
+            // 2^-E with E the exponent of the largest weight, never lowered; weights
+            // of nothing (all zero, or infinite) leave it
+            const uint32_t ex = __float_as_uint(w) >> 23;
+            float down = down_v[nt][j];
+            if (ex >= 1 && ex <= 252) {
+              const float want = __uint_as_float((254u - ex) << 23);
+              if (down == 0.f || want < down) down = want;
+            }
+            al[j] = down_v[nt][j] == 0.f ? 1.f : down * (1.0f / down_v[nt][j]);
+            down_v[nt][j] = down;
+            if (m_run[nt][j] == SA_NEG_INF || down == 0.f) fresh = true;
+          }
+#pragma unroll
+          for (int mt = 0; mt < G::kKs; ++mt) {
+            o[mt][nt][0] *= al[0];
+            o[mt][nt][1] *= al[1];
+            o[mt][nt][2] *= al[0];
+            o[mt][nt][3] *= al[1];
+          }
+        }
+      }
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float w0 = wt[nt][0] * down_v[nt][0], w1 = wt[nt][1] * down_v[nt][1];
+        const float w2 = wt[nt][2] * down_v[nt][0], w3 = wt[nt][3] * down_v[nt][1];
+        const __half2 h01 = __floats2half2_rn(w0, w1), h23 = __floats2half2_rn(w2, w3);
+        const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
+        ph[nt][0] = movm_t(*reinterpret_cast<const uint32_t*>(&h01));
+        ph[nt][1] = movm_t(*reinterpret_cast<const uint32_t*>(&h23));
+        pl[nt][0] = movm_t(pack2<__half>(w0 - f01.x, w1 - f01.y));
+        pl[nt][1] = movm_t(pack2<__half>(w2 - f23.x, w3 - f23.y));
       }
 
       // the stage is free: its refill, S tiles on
@@ -490,17 +560,15 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
           // (tokens 2 tig, 2 tig + 1), (2 tig + 8, 2 tig + 9): dims 4w, 4w + 1 | 4w + 2, 4w + 3
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const uint32_t sel = half ? 0x7632u : 0x5410u;
+            const uint32_t sel = half ? 0x7362u : 0x5140u;
             const uint32_t z0 = __byte_perm(vx[0][w], vx[1][w], sel);
             const uint32_t z1 = __byte_perm(vx[2][w], vx[3][w], sel);
-            const uint32_t a0 = times_2p120(high_codes_bf16x2(z0 << 8));
-            const uint32_t a1 = times_2p120(high_codes_bf16x2(z0));
-            const uint32_t a2 = times_2p120(high_codes_bf16x2(z1 << 8));
-            const uint32_t a3 = times_2p120(high_codes_bf16x2(z1));
+            const uint32_t a0 = e4m3x2_f16x2(z0), a1 = e4m3x2_f16x2(z0 >> 16);
+            const uint32_t a2 = e4m3x2_f16x2(z1), a3 = e4m3x2_f16x2(z1 >> 16);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma16816<__nv_bfloat16>(o[2 * w + half][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-              mma16816<__nv_bfloat16>(o[2 * w + half][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+              mma16816<__half>(o[2 * w + half][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+              mma16816<__half>(o[2 * w + half][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
             }
           }
         }
@@ -568,6 +636,68 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
   }
 }
 
+// Merge of the units split across CTAs: y = sum_w o_w 2^(m_w - M) / sum_w l_w 2^(m_w - M)
+// over the CTAs w that share the unit, in order.  A thread takes four dims of one
+// head, so that a unit's partials are read by as many threads as it has, eight at a
+// time: the loads' latency is all that this takes (a block per unit, 25 us for the 18
+// partials of a 65,536-token context, was bound by walking over them).
+template <typename T>
+__global__ void __launch_bounds__(128) fp8_combine_kernel(const GatherArgs a) {
+  pdl_wait();  // the attention kernel's partials and tile space
+  const int D4 = static_cast<int>(a.D) / 4;
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+  const int64_t row = x / D4;  // (unit, head of the group)
+  const int d = static_cast<int>(x - row * D4) * 4;
+  const int64_t u = row / a.hpu;
+  if (u >= a.units) return;
+  const int hh = static_cast<int>(row - u * a.hpu);
+  const int64_t b = u / a.Hkv, grp = u - b * a.Hkv;
+  const int64_t R = a.meta[0], lo = a.pref_out[b], tu = a.pref_out[b + 1] - lo;
+  const int64_t off = a.Hkv * lo + grp * tu;
+  if (tu == 0) return;
+  const int64_t c0 = off / R, c1 = (off + tu - 1) / R;
+  if (c0 == c1) return;  // written by the attention kernel
+  auto part = [&](int64_t c) { return (c * 2 + (c * R >= off ? 0 : 1)) * a.hpu + hh; };
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  float M = SA_NEG_INF, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int64_t c = c0; c <= c1; c += 8) {
+    float2 e[8];
+    float4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[i] = make_float2(SA_NEG_INF, 0.f);
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + i <= c1) {
+        e[i] = __ldg(ml + part(c + i));
+        v[i] = __ldg(reinterpret_cast<const float4*>(a.part_o + part(c + i) * a.D + d));
+      }
+    }
+    float mn = M;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mn = fmaxf(mn, e[i].x);
+    if (mn == SA_NEG_INF) continue;
+    const float f0 = ex2(M - mn);
+    L *= f0;
+    acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+    M = mn;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (e[i].x == SA_NEG_INF) continue;
+      const float f = ex2(e[i].x - mn);
+      L += e[i].y * f;
+      acc.x = fmaf(v[i].x, f, acc.x);
+      acc.y = fmaf(v[i].y, f, acc.y);
+      acc.z = fmaf(v[i].z, f, acc.z);
+      acc.w = fmaf(v[i].w, f, acc.w);
+    }
+  }
+  const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
+  uint32_t* y = reinterpret_cast<uint32_t*>(static_cast<T*>(a.y) + (b * a.Hq + grp * a.hpu + hh) * a.D + d);
+  y[0] = pack2<T>(acc.x * inv, acc.y * inv);
+  y[1] = pack2<T>(acc.z * inv, acc.w * inv);
+}
+
 // A pool as rows of codes: [pages * heads, page_tokens, D] bytes, the page stride with
 // its scale bytes; boxes of 16 rows.
 template <int D, int NT>
@@ -591,13 +721,23 @@ int launch_t(const GatherArgs& a, int64_t pool_heads, int sms, cudaStream_t st) 
   CUtensorMap tk, tv;
   if (!pool_map<D, NT>(&tk, a.k, a, pool_heads) || !pool_map<D, NT>(&tv, a.v, a, pool_heads)) return -1;
   const size_t smem = 1024 + G::kOffPref + static_cast<size_t>(a.B + 1) * sizeof(int32_t);
-  if (cudaFuncSetAttribute(fp8_pages_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return -1;
+  if (!allow_smem(reinterpret_cast<const void*>(fp8_pages_kernel<T, D, NT>))) return -1;
+  mark_event(a.ev_before, st);
   // Ranges of at least two tiles: below that a warp's set-up and the merge of its
   // partial cost more than the tiles.
   fp8_pages_kernel<T, D, NT><<<static_cast<unsigned>(sms), G::kThreads, smem, st>>>(tk, tv, a, pool_heads, 2);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  if (cudaGetLastError() != cudaSuccess) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.units * a.hpu * (D / 4) + 127) / 128));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  mark_event(a.ev_after, st);
+  return cudaLaunchKernelEx(&cfg, fp8_combine_kernel<T>, a) == cudaSuccess ? 0 : -1;
 }
 
 template <typename T>

@@ -908,7 +908,7 @@ static bool plan_fp8_pages(const sa_paged_params* p, Plan& pl) {
   size_t off = 0;
   pl.off_meta = off;
   off += align_up(sizeof(int64_t) + static_cast<size_t>(g.B + 1) * sizeof(int32_t));
-  const size_t partials = static_cast<size_t>(device_shape().sms) * 2 * g.hpu;
+  const size_t partials = static_cast<size_t>(sa::sm_count()) * 2 * g.hpu;
   pl.off_part_o = off;
   off += align_up(partials * g.D * sizeof(float));
   pl.off_part_ml = off;
@@ -953,11 +953,9 @@ static int paged_fp8_decode(const sa_paged_params* p, cudaStream_t st) {
   g.pref_out = reinterpret_cast<int32_t*>(ws + pl.off_meta + sizeof(int64_t));
   g.part_o = reinterpret_cast<float*>(ws + pl.off_part_o);
   g.part_ml = reinterpret_cast<float*>(ws + pl.off_part_ml);
-  sa::mark_event(t_ev_before, st);
-  const int lrc = sa::launch_fp8_pages(g, p->Hkv, p->dtype, device_shape().sms, st);
-  sa::mark_event(t_ev_after, st);
-  if (lrc != 0 || sa::launch_stream_combine(g, p->dtype, st) != 0) return SA_ERR_LAUNCH;
-  return SA_OK;
+  g.ev_before = t_ev_before;
+  g.ev_after = t_ev_after;
+  return sa::launch_fp8_pages(g, p->Hkv, p->dtype, sa::sm_count(), st) == 0 ? SA_OK : SA_ERR_LAUNCH;
 }
 
 size_t paged_attn_decode_workspace(const sa_paged_params* p) {

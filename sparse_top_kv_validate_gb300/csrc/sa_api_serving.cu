@@ -3,6 +3,7 @@
 // checks and launches; nothing here allocates, frees or synchronises.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -106,6 +107,44 @@ bool rope_ok(const sa_rope* r) {
 }
 
 }  // namespace
+
+namespace sa {
+
+constexpr int kMaxDevices = 64;
+
+int sm_count() {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 152;
+  if (dev < kMaxDevices && known[dev].load(std::memory_order_relaxed) > 0)
+    return known[dev].load(std::memory_order_relaxed);
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  if (dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+bool allow_smem(const void* kernel, int bytes) {
+  constexpr int kSlots = 256;  // (kernel, device) pairs seen, open addressing
+  static std::atomic<uintptr_t> seen[kSlots];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+  const uintptr_t key = reinterpret_cast<uintptr_t>(kernel) * kMaxDevices + static_cast<uintptr_t>(dev);
+  const unsigned h = static_cast<unsigned>((key * 0x9E3779B97F4A7C15ull) >> 56);
+  for (int i = 0; i < kSlots; ++i) {
+    const uintptr_t at = seen[(h + i) % kSlots].load(std::memory_order_acquire);
+    if (at == key) return true;
+    if (at == 0) break;
+  }
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  for (int i = 0; i < kSlots; ++i) {
+    uintptr_t none = 0;
+    if (seen[(h + i) % kSlots].compare_exchange_strong(none, key, std::memory_order_acq_rel) || none == key) break;
+  }
+  return true;
+}
+
+}  // namespace sa
 
 extern "C" {
 

@@ -15,6 +15,14 @@ namespace sa {
 void* kernel_event_before();
 void* kernel_event_after();
 
+// Let a kernel use up to `bytes` of dynamic shared memory (the same for every call):
+// asked once per kernel and device, as the call costs about a microsecond.
+constexpr int kAllSmem = 227 * 1024;
+bool allow_smem(const void* kernel, int bytes = kAllSmem);
+
+// Multiprocessors of the current device, asked once per device.
+int sm_count();
+
 // ---- rotary positions ------------------------------------------------------------
 struct RotaryArgs {
   const void* x[2];           // queries, keys (H[1] == 0: queries only)
@@ -53,8 +61,8 @@ int launch_kv_read(const KvPagesArgs& a, int dtype, cudaStream_t st);
 
 // ---- decode over FP8 pages ------------------------------------------------------------
 // GatherArgs of the paged source with Hkv the number of query-head groups
-// (KV heads times sub-groups) and g = hpu heads per group; the stream kernel's
-// combine merges the units split across its CTAs (one per SM).
+// (KV heads times sub-groups) and g = hpu heads per group.  Launches the attention
+// kernel (one CTA per SM) and the merge of the units split across its CTAs.
 int64_t fp8_pages_max_heads(int D);           // query heads one group can hold
 int launch_fp8_pages(const GatherArgs& a, int64_t pool_heads, int dtype, int sms,
                      cudaStream_t st);
