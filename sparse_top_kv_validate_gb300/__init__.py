@@ -860,6 +860,13 @@ def csa_pool_weight(t, *, w=None, stream=None):
 
 # ---- the serving step around a paged cache --------------------------------------------------
 
+def _stream_handle(index):
+    """The current stream's handle on a device.  (``current_stream()`` builds a Stream
+    object first, which takes as long as the launch.)"""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 class _launching:
     """The tensors' device made current and the launching stream's handle:
     ``stream``'s, or the device's current one's.  Tensors allocated inside belong
@@ -873,11 +880,11 @@ class _launching:
     def __enter__(self):
         index = self.device.index
         if self.stream is None and index == torch.cuda.current_device():
-            return torch.cuda.current_stream().cuda_stream
+            return _stream_handle(index)
         self.stack = contextlib.ExitStack()
         self.stack.enter_context(torch.cuda.device(self.device))
         if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
+            return _stream_handle(index)
         self.stack.enter_context(torch.cuda.stream(self.stream))
         return self.stream.cuda_stream
 

@@ -129,6 +129,10 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
   const int gid = lane >> 2, tig = lane & 3;
   const int hpu = static_cast<int>(a.hpu);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + G::kOffBar) + warp * S;
+  if (threadIdx.x == 0) {
+    tc05::prefetch_tmap(&tk);
+    tc05::prefetch_tmap(&tv);
+  }
   if (lane < S) mbar_init(&full[lane], 1);
   if (lane < 2) parts[2 * warp + lane].where = -1;
   fence_mbar_init();
@@ -167,10 +171,10 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
     for (int64_t b = threadIdx.x; b <= a.B; b += blockDim.x) a.pref_out[b] = pref[b];
     if (threadIdx.x == 0) a.meta[0] = R * NW;
     // sequences without tiles still need a (zero) output
-    for (int64_t e = threadIdx.x; e < a.B * a.Hq * D; e += blockDim.x) {
-      const int64_t b = e / (a.Hq * D);
-      if (pref[b + 1] == pref[b]) static_cast<T*>(a.y)[e] = from_f32<T>(0.f);
-    }
+    for (int b = warp; b < a.B; b += NW)
+      if (pref[b + 1] == pref[b])
+        for (int64_t e = lane; e < a.Hq * D / 2; e += 32)
+          reinterpret_cast<uint32_t*>(a.y)[b * (a.Hq * D / 2) + e] = 0u;
   }
   const int64_t c_begin = static_cast<int64_t>(blockIdx.x) * NW * R;
   if (c_begin >= total) return;  // the whole CTA
@@ -585,24 +589,28 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
   __syncthreads();
 
   // ---- merge of the units that this CTA's warps share ----------------------------------------
-  // The partials are in tile order, a unit's next to one another.
+  // The partials are in tile order, a unit's next to one another.  The units are
+  // dealt out to the warps; where there are few, several warps share one.
   const float* fsm = reinterpret_cast<const float*>(sm);
-  for (int e = 0; e < 2 * NW;) {
+  static_assert(2 * NW <= 32, "a lane per partial");
+  Part mine{0, 0, 0, -1};
+  if (lane < 2 * NW) mine = parts[lane];
+  const uint32_t valid = __ballot_sync(0xffffffffu, mine.where >= 0);
+  const uint32_t before = valid & ((1u << lane) - 1u);
+  const int before_off = __shfl_sync(0xffffffffu, mine.unit_off, before ? 31 - __clz(before) : lane);
+  uint32_t starts = __ballot_sync(0xffffffffu, mine.where >= 0 && (!before || before_off != mine.unit_off));
+  const int units = __popc(starts), share = units > 0 && units < NW ? NW / units : 1;
+  const int part0 = warp % share;
+  for (int g = 0; starts; ++g) {
+    const int e = __ffs(starts) - 1;
+    starts &= starts - 1u;
+    const int last = starts ? __ffs(starts) - 2 : 2 * NW - 1;
+    if (g % (NW / share) != warp / share) continue;
     const Part p = parts[e];
-    if (p.where < 0) {
-      ++e;
-      continue;
-    }
-    int last = e;
-    for (int f = e; f < 2 * NW; ++f) {
-      if (parts[f].where < 0) continue;
-      if (parts[f].unit_off != p.unit_off) break;
-      last = f;
-    }
     const bool whole = p.unit_off >= c_begin && p.unit_off + p.unit_tu <= c_end;
     // slot 0: the CTA's range begins inside the unit (or with it), else 1
     const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (c_begin >= p.unit_off ? 0 : 1)) * a.hpu;
-    for (int x = threadIdx.x; x < hpu * (D / 4); x += G::kThreads) {
+    for (int x = part0 * 32 + lane; x < hpu * (D / 4); x += share * 32) {
       const int hh = x / (D / 4), d = (x - hh * (D / 4)) * 4;
       float M = SA_NEG_INF;
       for (int f = e; f <= last; ++f)
@@ -632,7 +640,6 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
         if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * (slot + hh)) = make_float2(M, L);
       }
     }
-    e = last + 1;
   }
 }
 
