@@ -17,7 +17,7 @@ namespace sa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kRingThreads;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTok = 16;  // tokens per block
 
@@ -42,18 +42,13 @@ struct Place {
   int32_t slot, pos;
 };
 
-// Where packed row r lives.  kWrite: the rows are the last of the context;
-// else its first.  Uniform over the warp.
+// Where packed row r of sequence b lives.  kWrite: the rows are the last of the
+// context; else its first.
 template <bool kWrite>
-__device__ __forceinline__ Place place_of(const KvPagesArgs& a, int r, int lane) {
+__device__ __forceinline__ Place place_in(const KvPagesArgs& a, int b, int r) {
   Place p{-1, 0, 0};
-  int b = r, first = r, n = 1;
-  if (a.seq_start) {
-    b = owner_of(a.seq_start, a.B, r, lane);
-    if (b < 0) return p;
-    first = __ldg(a.seq_start + b);
-    n = __ldg(a.seq_start + b + 1) - first;
-  }
+  const int first = a.seq_start ? __ldg(a.seq_start + b) : r;
+  const int n = a.seq_start ? __ldg(a.seq_start + b + 1) - first : 1;
   const int64_t ctx = __ldg(a.ctx_len + b);
   const int64_t pos = (kWrite ? ctx - n : 0) + (r - first);
   int32_t page = -1;
@@ -65,11 +60,37 @@ __device__ __forceinline__ Place place_of(const KvPagesArgs& a, int r, int lane)
     p.pos = static_cast<int32_t>(pos);
   }
   if (page < 0 || page >= a.num_pages) {
-    if (lane == 0 && a.err_word) atomicOr(a.err_word, SA_ERRBIT_PAGE);
+    if (a.err_word) atomicOr(a.err_word, SA_ERRBIT_PAGE);
     return p;
   }
   p.page = static_cast<int64_t>(page) * a.Hkv;
   return p;
+}
+
+// The same for a row whose sequence is not known: by a warp, uniform over it.
+template <bool kWrite>
+__device__ __forceinline__ Place place_of(const KvPagesArgs& a, int r, int lane) {
+  const int b = a.seq_start ? owner_of(a.seq_start, a.B, r, lane) : r;
+  return b < 0 ? Place{-1, 0, 0} : place_in<kWrite>(a, b, r);
+}
+
+// The places of a tile's `n` tokens, by the whole block.  A tile inside one
+// sequence, as most tiles of long spans are, takes one search and then a lane
+// per token; else each warp searches for its tokens.
+template <bool kWrite>
+__device__ __forceinline__ void tile_places(const KvPagesArgs& a, int t0, int n, Place* place) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (a.seq_start && n > 1) {
+    const int b = owner_of(a.seq_start, a.B, t0, lane);
+    if (b >= 0 && t0 + n <= __ldg(a.seq_start + b + 1)) {
+      if (threadIdx.x < n) place[threadIdx.x] = place_in<kWrite>(a, b, t0 + threadIdx.x);
+      return;
+    }
+  }
+  for (int k = warp; k < n; k += kWarps) {
+    const Place p = place_of<kWrite>(a, t0 + k, lane);
+    if (lane == 0) place[k] = p;
+  }
 }
 
 // Block 0 looks the starts over.
@@ -106,123 +127,135 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-template <typename T>
-__device__ __forceinline__ void load8_any(const T* p, int aligned, Raw8<T>& v) {
-  if (aligned) {
-    v = load8<T>(p);
-  } else {
-    T* e = reinterpret_cast<T*>(&v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = p[i];
-  }
+// The largest magnitude; a NaN among them stays one.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+
+// A block's threads over a tile of tokens: the low half of them has the keys,
+// the high half the values; a half's lane is (chunk c, token k, head hl) with
+// the chunk fastest, and takes the heads hl, hl + hs, ...: chunk, token and
+// tensor are a thread's own, and a step is an addition.
+struct Seat {
+  int w, c, k, hl, hs;
+};
+__device__ __forceinline__ Seat seat_of(int lanes, int tt) {
+  const int u = threadIdx.x % (kThreads / 2), slot = u >> (__ffs(lanes) - 1);
+  return Seat{threadIdx.x >= kThreads / 2, u & (lanes - 1), slot & (tt - 1),
+              slot >> (__ffs(tt) - 1), (kThreads / 2) >> (__ffs(lanes * tt) - 1)};
 }
 
 // ---- write, 16 elements per lane ------------------------------------------------------
 //
-// D / 16 lanes hold a row (two 8-element pieces each, chunk_dims), so a pair of
-// the half layout meets in one lane and the row's maximum in log2(D / 16)
-// shuffles.  A block takes `tt` tokens; a thread has up to kBatch rows in
-// flight.
-template <typename T, bool kFp8>
-__global__ void __launch_bounds__(kThreads)
+// D / 16 lanes hold a row (two 8-element pieces each, pieces_of), so a pair
+// meets in one lane and the row's maximum in log2(D / 16) shuffles.  A block takes `tt` tokens; a thread's first rows are on their way
+// (RowRing) before it knows where they go.
+template <typename T, bool kFp8, bool kInter>
+__global__ void __launch_bounds__(kThreads, 3)
     kv_write_kernel(const __grid_constant__ KvPagesArgs a, int tt) {
-  constexpr int kBatch = sizeof(T) == 4 ? 2 : 4;
-  extern __shared__ float2 cs_sm[];  // [tt][half] when the keys are rotated
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Place place[kMaxTok];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t0 = blockIdx.x * tt;
-  const int lanes = a.D / 16, c = tid % lanes, q0 = tid / lanes, rp = kThreads / lanes;
-  const int per_tok = 2 * a.Hkv, rows = min(tt, a.T - t0) * per_tok;
+  RowRing<T> ring(smem);
+  float* cs_sm = reinterpret_cast<float*>(smem + RowRing<T>::kBytes);  // [tt][cos, sin][half]
+  const int tid = threadIdx.x;
+  const int t0 = blockIdx.x * tt, n = min(tt, a.T - t0);
+  const int lanes = a.D / 16;
+  const Seat st = seat_of(lanes, tt);
   const int rot = a.has_rope ? a.rope.rotary_dim : 0, half = rot / 2;
-  const int inter = a.has_rope ? a.rope.interleaved : 1;
-  int d0, d1;
-  chunk_dims(c, rot, inter, d0, d1);
+  const Pieces pc = pieces_of<kInter>(st.c, a.D, st.w ? 0 : rot);
+  const int d0 = pc.d[0], d1 = pc.d[1];
+  const T* x = static_cast<const T*>(a.x[st.w]) + (t0 + st.k) * a.xs[st.w][0] +
+               st.hl * a.xs[st.w][1];
+  const int64_t xstep = st.hs * a.xs[st.w][1];
+  const int steps = (a.Hkv + st.hs - 1) / st.hs;  // rows of a thread, the last one perhaps nobody's
+  const int mine = st.k < n && st.hl < a.Hkv ? (a.Hkv - st.hl + st.hs - 1) / st.hs : 0;
+  auto fetch = [&](int i) {
+    if (i < mine) {
+      ring.fetch(i, 0, x + d0, a.aligned);
+      ring.fetch(i, 1, x + d1, a.aligned);
+      x += xstep;
+    }
+    ring.commit();
+  };
+  for (int i = 0; i < RowRing<T>::kRowsAhead; ++i) fetch(i);
   check_starts(a);
+  tile_places<true>(a, t0, n, place);
+  __syncthreads();
+  Turns turns{};
+  if (rot) {
+    for (int e = tid; e < n * half; e += kThreads) {
+      const int k = e / half, i = e - k * half;
+      const float2 cs = rope_cos_sin(place[k].pos, a.rope.turns[i], a.rope.mscale);
+      cs_sm[2 * k * half + i] = cs.x;
+      cs_sm[(2 * k + 1) * half + i] = cs.y;
+    }
+    __syncthreads();
+    if (!st.w && st.k < n) turns = turns_of<kInter>(cs_sm + 2 * st.k * half, half, pc);
+  }
+  const Place p = st.k < n ? place[st.k] : Place{-1, 0, 0};
+  // the row in its page, and the way to the next head's
+  const int64_t page = a.page_tokens * (kFp8 ? a.D + 1 : a.D * static_cast<int64_t>(sizeof(T)));
+  uint8_t* y = static_cast<uint8_t*>(a.pool[st.w]) + (p.page + st.hl) * page;
+  const int64_t ystep = st.hs * page;
+  const int64_t row = static_cast<int64_t>(p.slot) * a.D, scale = a.page_tokens * a.D + p.slot;
+  bool any_bad = false;
 
-  for (int rb = 0; rb < rows; rb += kBatch * rp) {  // the same trips for the whole block
-    Raw8<T> va[kBatch], vb[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = rb + q0 + i * rp;
-      if (r < rows) {
-        const int k = r / per_tok, e = r - k * per_tok, w = e >= a.Hkv, h = e - (w ? a.Hkv : 0);
-        const T* x = static_cast<const T*>(a.x[w]) + (t0 + k) * a.xs[w][0] + h * a.xs[w][1];
-        load8_any<T>(x + d0, a.aligned, va[i]);
-        load8_any<T>(x + d1, a.aligned, vb[i]);
-      }
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {  // the same trips for the whole block
+    ring.arrived();
+    // uniform over a row's lanes; the shuffles stay within them
+    const bool put = p.page >= 0 && i < mine;
+    const Raw8<T> va = ring.get(i, 0), vb = ring.get(i, 1);
+    float fa[8], fb[8];
+    unpack8<T>(va, fa);
+    unpack8<T>(vb, fb);
+    Piece pa = piece_from<kInter>(fa), pb = piece_from<kInter>(fb);
+    if (!st.w) {
+      rotate_pieces<kInter>(pa, pb, turns, pc);
+      piece_to<kInter>(pa, fa);
+      piece_to<kInter>(pb, fb);
     }
-    if (rb == 0) {  // the first batch's loads are on their way
-      for (int k = warp; k < tt; k += kWarps) {
-        Place p{-1, 0, 0};
-        if (t0 + k < a.T) p = place_of<true>(a, t0 + k, lane);
-        if (lane == 0) place[k] = p;
-      }
-      __syncthreads();
-      if (rot) {
-        for (int e = tid; e < tt * half; e += kThreads) {
-          const int k = e / half, i = e - k * half;
-          cs_sm[e] = rope_cos_sin(place[k].pos, a.rope.turns[i], a.rope.mscale);
-        }
-        __syncthreads();
-      }
-    }
+    if (kFp8) {
+      float mx = 0.f;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = rb + q0 + i * rp;
-      const bool live = r < rows;  // uniform over a row's lanes; the shuffles stay within them
-      const int k = live ? r / per_tok : 0, e = live ? r - k * per_tok : 0, w = e >= a.Hkv;
-      const int h = e - (w ? a.Hkv : 0);
-      const Place p = place[k];
-      const bool put = live && p.page >= 0;
-      float fa[8], fb[8];
-      unpack8<T>(va[i], fa);
-      unpack8<T>(vb[i], fb);
-      const bool turn = live && !w && 16 * c < rot;
-      if (turn) {
-        float2 cs[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) cs[j] = cs_sm[k * half + 8 * c + j];
-        rotate_chunk(fa, fb, cs, inter);
-      }
-      if (kFp8) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, max(abs_bits(fa[j]), abs_bits(fb[j])));
-        for (int o = lanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (!put) continue;
+      for (int j = 0; j < 8; ++j) mx = max_abs(mx, fa[j], fb[j]);
+      for (int o = lanes / 2; o > 0; o >>= 1)
+        mx = max_abs(mx, __shfl_xor_sync(0xffffffffu, mx, o), 0.f);
+      if (put) {
+        const uint32_t m = __float_as_uint(mx);
         const bool bad = m >= kInfBits;
         const int ex = bad ? 0 : row_exponent(m);
         const float mul = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        const F2 mul2 = f2(mul, mul);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          fa[j] = bad ? 0.f : fa[j] * mul;
-          fb[j] = bad ? 0.f : fb[j] * mul;
+        for (int j = 0; j < 4; ++j) {
+          pa.x[j] = f2_mul(pa.x[j], mul2);
+          pb.x[j] = f2_mul(pb.x[j], mul2);
         }
-        uint8_t* page = fp8_page(a, w, p.page, h);
-        uint8_t* codes = page + p.slot * a.D;
-        *reinterpret_cast<uint2*>(codes + d0) =
-            make_uint2(to_e4m3x4(fa[0], fa[1], fa[2], fa[3]), to_e4m3x4(fa[4], fa[5], fa[6], fa[7]));
-        *reinterpret_cast<uint2*>(codes + d1) =
-            make_uint2(to_e4m3x4(fb[0], fb[1], fb[2], fb[3]), to_e4m3x4(fb[4], fb[5], fb[6], fb[7]));
-        if (c == 0) {
-          page[a.page_tokens * a.D + p.slot] = static_cast<uint8_t>(bad ? 255 : ex + 127);
-          if (bad && a.err_word) atomicOr(a.err_word, SA_ERRBIT_NONFINITE);
-        }
-      } else if (put) {
-        T* y = static_cast<T*>(a.pool[w]) + ((p.page + h) * a.page_tokens + p.slot) * a.D;
-        if (turn) {
-          store8<T>(y + d0, fa);
-          store8<T>(y + d1, fb);
-        } else {  // an exact copy
-#pragma unroll
-          for (int j = 0; j < static_cast<int>(sizeof(T) / 2); ++j) {
-            *(reinterpret_cast<uint4*>(y + d0) + j) = va[i].r[j];
-            *(reinterpret_cast<uint4*>(y + d1) + j) = vb[i].r[j];
-          }
-        }
+        piece_to<kInter>(pa, fa);
+        piece_to<kInter>(pb, fb);
+        uint4 w = make_uint4(
+            to_e4m3x4(fa[0], fa[1], fa[2], fa[3]), to_e4m3x4(fa[4], fa[5], fa[6], fa[7]),
+            to_e4m3x4(fb[0], fb[1], fb[2], fb[3]), to_e4m3x4(fb[4], fb[5], fb[6], fb[7]));
+        if (bad) w = make_uint4(0u, 0u, 0u, 0u);
+        any_bad |= bad;
+        *reinterpret_cast<uint2*>(y + row + d0) = make_uint2(w.x, w.y);
+        *reinterpret_cast<uint2*>(y + row + d1) = make_uint2(w.z, w.w);
+        if (st.c == 0) y[scale] = static_cast<uint8_t>(bad ? 255 : ex + 127);
       }
+    } else if (put) {
+      T* o = reinterpret_cast<T*>(y) + row;
+      if (pc.turn[0]) store8<T>(o + d0, fa);
+      else store_raw<T>(o + d0, va);  // an exact copy
+      if (pc.turn[1]) store8<T>(o + d1, fb);
+      else store_raw<T>(o + d1, vb);
     }
+    y += ystep;
+    fetch(i + RowRing<T>::kRowsAhead);
   }
+  if (any_bad && st.c == 0 && a.err_word) atomicOr(a.err_word, SA_ERRBIT_NONFINITE);
 }
 
 // ---- write, any D and rotary_dim: a warp per row, the row in shared memory ----------------
@@ -299,8 +332,8 @@ __device__ __forceinline__ void store16(T* y, const uint4& codes, float scale, i
         : "=r"(h2)
         : "h"(static_cast<uint16_t>(wd[i / 2] >> (16 * (i & 1)))));
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-    f[i / 4][2 * (i % 4)] = v.x * scale;
-    f[i / 4][2 * (i % 4) + 1] = v.y * scale;
+    f2_split(f2_mul(f2(v.x, v.y), f2(scale, scale)), f[i / 4][2 * (i % 4)],
+             f[i / 4][2 * (i % 4) + 1]);
   }
   if (aligned) {
     store8<T>(y, f[0]);
@@ -318,50 +351,41 @@ __device__ __forceinline__ float e8m0(uint32_t byte) {
                        : __uint_as_float(byte << 23);
 }
 
-// FP8 pages -> rows: 16 codes per lane; a block takes `tt` rows of every head.
+// FP8 pages -> rows: 16 codes per lane, kBatch rows in flight per thread; a
+// block takes `tt` rows of every head.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     kv_read_fp8_kernel(const __grid_constant__ KvPagesArgs a, int tt) {
   constexpr int kBatch = 4;
   __shared__ Place place[kMaxTok];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t0 = blockIdx.x * tt;
-  const int lanes = a.D / 16, c = tid % lanes, q0 = tid / lanes, rp = kThreads / lanes;
-  const int n = min(tt, a.T - t0), rows = n * 2 * a.Hkv;
+  const int t0 = blockIdx.x * tt, n = min(tt, a.T - t0);
+  const Seat st = seat_of(a.D / 16, tt);
   check_starts(a);
-  for (int k = warp; k < n; k += kWarps) {
-    const Place p = place_of<false>(a, t0 + k, lane);
-    if (lane == 0) place[k] = p;
-  }
+  tile_places<false>(a, t0, n, place);
   __syncthreads();
-  // rows in the order (K or V, head, token): neighbours in a page are neighbours here
-  for (int r0 = q0; r0 < rows; r0 += kBatch * rp) {
+  const Place p = st.k < n ? place[st.k] : Place{-1, 0, 0};
+  if (p.page < 0) return;
+  const int64_t page = a.page_tokens * (a.D + 1), xstep = st.hs * page;
+  const uint8_t* x = static_cast<const uint8_t*>(a.pool[st.w]) + (p.page + st.hl) * page;
+  const int64_t row = static_cast<int64_t>(p.slot) * a.D + 16 * st.c;
+  const int64_t scale = a.page_tokens * a.D + p.slot;
+  T* y = static_cast<T*>(a.x[st.w]) + (t0 + st.k) * a.xs[st.w][0] + st.hl * a.xs[st.w][1] +
+         16 * st.c;
+  const int64_t ystep = st.hs * a.xs[st.w][1];
+  for (int h = st.hl; h < a.Hkv; h += kBatch * st.hs) {
     uint4 codes[kBatch];
     uint32_t sb[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + i * rp;
-      if (r < rows) {
-        const int e = r / n, k = r - e * n, w = e >= a.Hkv, h = e - (w ? a.Hkv : 0);
-        const Place p = place[k];
-        if (p.page >= 0) {
-          const uint8_t* page = fp8_page(a, w, p.page, h);
-          codes[i] = __ldg(reinterpret_cast<const uint4*>(page + p.slot * a.D) + c);
-          sb[i] = __ldg(page + a.page_tokens * a.D + p.slot);
-        }
+    for (int i = 0; i < kBatch; ++i)
+      if (h + i * st.hs < a.Hkv) {
+        codes[i] = __ldg(reinterpret_cast<const uint4*>(x + i * xstep + row));
+        sb[i] = __ldg(x + i * xstep + scale);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + i * rp;
-      if (r < rows) {
-        const int e = r / n, k = r - e * n, w = e >= a.Hkv, h = e - (w ? a.Hkv : 0);
-        if (place[k].page >= 0) {
-          T* y = static_cast<T*>(a.x[w]) + (t0 + k) * a.xs[w][0] + h * a.xs[w][1] + 16 * c;
-          store16<T>(y, codes[i], e8m0(sb[i]), a.aligned);
-        }
-      }
-    }
+    for (int i = 0; i < kBatch; ++i)
+      if (h + i * st.hs < a.Hkv) store16<T>(y + i * ystep, codes[i], e8m0(sb[i]), a.aligned);
+    x += kBatch * xstep;
+    y += kBatch * ystep;
   }
 }
 
@@ -391,12 +415,12 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Tokens per block: as many as give every thread a full batch of rows, once
-// the blocks still cover the SMs twice.
-int tokens_per_block(const KvPagesArgs& a, int batch) {
-  const int rp = kThreads / (a.D / 16);
+// Tokens per block: up to what a half's threads hold side by side, once the
+// blocks still cover the SMs twice.
+int tokens_per_block(const KvPagesArgs& a) {
+  const int most = kThreads / 2 / (a.D / 16);
   int tt = 1;
-  while (tt < kMaxTok && 2 * tt * 2 * a.Hkv <= batch * rp && a.T / (2 * tt) >= 2 * 152) tt *= 2;
+  while (2 * tt <= kMaxTok && 2 * tt <= most && a.T / (2 * tt) >= 2 * 152) tt *= 2;
   return tt;
 }
 
@@ -411,11 +435,13 @@ int write_t(const KvPagesArgs& a, cudaStream_t st) {
   const int L = a.D / 16;
   const bool chunks = a.D % 16 == 0 && rot % 16 == 0 && L <= 32 && (L & (L - 1)) == 0;
   if (chunks && (a.fp8 || a.aligned)) {
-    const int tt = tokens_per_block(a, sizeof(T) == 4 ? 2 : 4);
+    const int tt = tokens_per_block(a);
     const unsigned grid = static_cast<unsigned>((a.T + tt - 1) / tt);
-    const size_t smem = static_cast<size_t>(tt) * (rot / 2) * sizeof(float2);
-    if (a.fp8) kv_write_kernel<T, true><<<grid, kThreads, smem, st>>>(a, tt);
-    else kv_write_kernel<T, false><<<grid, kThreads, smem, st>>>(a, tt);
+    const size_t smem = RowRing<T>::kBytes + static_cast<size_t>(tt) * rot * sizeof(float);
+    const bool inter = a.has_rope && a.rope.interleaved;
+    auto kernel = a.fp8 ? (inter ? kv_write_kernel<T, true, true> : kv_write_kernel<T, true, false>)
+                        : (inter ? kv_write_kernel<T, false, true> : kv_write_kernel<T, false, false>);
+    kernel<<<grid, kThreads, smem, st>>>(a, tt);
   } else if (a.fp8) {
     kv_write_any_kernel<T, true><<<row_blocks(a), kThreads, 0, st>>>(a);
   } else {
@@ -427,7 +453,7 @@ int write_t(const KvPagesArgs& a, cudaStream_t st) {
 template <typename T>
 int read_t(const KvPagesArgs& a, cudaStream_t st) {
   if (a.fp8) {
-    const int tt = tokens_per_block(a, 4);
+    const int tt = tokens_per_block(a);
     const unsigned grid = static_cast<unsigned>((a.T + tt - 1) / tt);
     kv_read_fp8_kernel<T><<<grid, kThreads, 0, st>>>(a, tt);
   } else {

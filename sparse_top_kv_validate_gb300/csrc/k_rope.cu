@@ -18,7 +18,7 @@ namespace sa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kRingThreads;
 
 __device__ __forceinline__ int64_t position_of(const RotaryArgs& a, int b, int s) {
   return load_index(a.positions, b * a.pos_stride + s, a.pos_is_i64);
@@ -29,89 +29,122 @@ __device__ __forceinline__ int64_t token_off(const int64_t (&st)[3], int b, int 
   return b * st[0] + s * st[1];
 }
 
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads)
-    rotary_kernel(const __grid_constant__ RotaryArgs a, int tt, int lanes) {
-  extern __shared__ float2 cs_sm[];  // [tt][half]
+// The tokens' tables.
+__device__ __forceinline__ void fill_turns(const RotaryArgs& a, int t0, int tt, float* cs_sm) {
   const int half = a.rope.rotary_dim / 2;
-  const int t0 = blockIdx.x * tt;
-  const int tid = threadIdx.x;
-  // (cos, sin): a thread keeps one pair where the block holds whole rows of pairs
-  for (int e = tid; e < tt * half; e += kThreads) {
+  for (int e = threadIdx.x; e < tt * half; e += kThreads) {
     const int k = e / half, i = e - k * half, t = t0 + k;
     if (t < a.T) {
       const int b = t / a.S;
-      cs_sm[e] = rope_cos_sin(position_of(a, b, t - b * a.S), a.rope.turns[i], a.rope.mscale);
+      const float2 cs = rope_cos_sin(position_of(a, b, t - b * a.S), a.rope.turns[i], a.rope.mscale);
+      cs_sm[2 * k * half + i] = cs.x;
+      cs_sm[(2 * k + 1) * half + i] = cs.y;
     }
   }
+}
+
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(kThreads, 3)
+    rotary_kernel(const __grid_constant__ RotaryArgs a, int tt, int lanes) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  RowRing<T> ring(smem);
+  float* cs_sm = reinterpret_cast<float*>(smem + RowRing<T>::kBytes);  // [tt][cos, sin][half]
+  const int half = a.rope.rotary_dim / 2, t0 = blockIdx.x * tt;
+  const int c = threadIdx.x % lanes, slot = threadIdx.x / lanes;
+  const int k = slot % tt, hl = slot / tt, step = kThreads / (lanes * tt);
+  const int t = t0 + k, b = t / a.S, s = t - b * a.S;
+  const Pieces pc = pieces_of<kInter>(c, a.D, a.rope.rotary_dim);
+  const int d0 = pc.d[0], d1 = pc.d[1];
+  const bool turn = pc.turn[0] || pc.turn[1];
+  // this thread's rows: the first tensor's, then the second's
+  const T* x[2];
+  T* y[2];
+  int rows[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    x[w] = static_cast<const T*>(a.x[w]) + token_off(a.xs[w], b, s) + hl * a.xs[w][2];
+    y[w] = static_cast<T*>(a.y[w]) + token_off(a.ys[w], b, s) + hl * a.ys[w][2];
+    const bool live = hl < step && hl < a.H[w] && t < a.T && (turn || !a.in_place[w]);
+    rows[w] = live ? (a.H[w] - hl + step - 1) / step : 0;
+  }
+  const T* xp = x[0];
+  int64_t xstep = step * a.xs[0][2];
+  const int total = rows[0] + rows[1];
+  auto fetch = [&](int i) {
+    if (i < total) {
+      if (i == rows[0]) {
+        xp = x[1];
+        xstep = step * a.xs[1][2];
+      }
+      ring.fetch(i, 0, xp + d0, true);
+      ring.fetch(i, 1, xp + d1, true);
+      xp += xstep;
+    }
+    ring.commit();
+  };
+  for (int i = 0; i < RowRing<T>::kRowsAhead; ++i) fetch(i);
+  fill_turns(a, t0, tt, cs_sm);
   __syncthreads();
-  const int c = tid % lanes, qd = tid / lanes;
-  const int k = qd % tt, hl = qd / tt, hstep = kThreads / (lanes * tt);
+  const Turns turns = turns_of<kInter>(cs_sm + 2 * k * half, half, pc);
+  T* yp = y[0];
+  int64_t ystep = step * a.ys[0][2];
+#pragma unroll 1
+  for (int i = 0; i < total; ++i) {
+    if (i == rows[0]) {
+      yp = y[1];
+      ystep = step * a.ys[1][2];
+    }
+    ring.arrived();
+    const Raw8<T> va = ring.get(i, 0), vb = ring.get(i, 1);
+    float fa[8], fb[8];
+    unpack8<T>(va, fa);
+    unpack8<T>(vb, fb);
+    Piece pa = piece_from<kInter>(fa), pb = piece_from<kInter>(fb);
+    rotate_pieces<kInter>(pa, pb, turns, pc);
+    piece_to<kInter>(pa, fa);
+    piece_to<kInter>(pb, fb);
+    if (pc.turn[0]) store8<T>(yp + d0, fa);
+    else store_raw<T>(yp + d0, va);
+    if (pc.turn[1]) store8<T>(yp + d1, fb);
+    else store_raw<T>(yp + d1, vb);
+    yp += ystep;
+    fetch(i + RowRing<T>::kRowsAhead);
+  }
+}
+
+// Rows that are no whole chunks or not aligned: one pair, or one element past
+// rotary_dim, per lane.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    rotary_any_kernel(const __grid_constant__ RotaryArgs a, int tt, int lanes) {
+  extern __shared__ __align__(16) float cs_sm[];
+  const int half = a.rope.rotary_dim / 2, t0 = blockIdx.x * tt;
+  fill_turns(a, t0, tt, cs_sm);
+  __syncthreads();
+  const int c = threadIdx.x % lanes, slot = threadIdx.x / lanes;
+  const int k = slot % tt, hl = slot / tt, hstep = kThreads / (lanes * tt);
   const int t = t0 + k;
   if (hl >= hstep || t >= a.T) return;
   const int b = t / a.S, s = t - b * a.S;
-  const int heads = a.H[0] + a.H[1];
-  const int64_t xo[2] = {token_off(a.xs[0], b, s), token_off(a.xs[1], b, s)};
-  const int64_t yo[2] = {token_off(a.ys[0], b, s), token_off(a.ys[1], b, s)};
-
-  if (kVec) {
-    constexpr int kRows = sizeof(T) == 4 ? 2 : 4;  // rows in flight per thread
-    int d0, d1;
-    chunk_dims(c, a.rope.rotary_dim, a.rope.interleaved, d0, d1);
-    const bool turn = 16 * c < a.rope.rotary_dim;
-    float2 cs[8];
-    if (turn) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) cs[i] = cs_sm[k * half + 8 * c + i];
-    }
-    for (int h0 = hl; h0 < heads; h0 += kRows * hstep) {
-      Raw8<T> va[kRows], vb[kRows];
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const int hh = h0 + r * hstep;
-        if (hh < heads) {
-          const int w = hh >= a.H[0], h = hh - (w ? a.H[0] : 0);
-          if (turn || !a.in_place[w]) {
-            const T* x = static_cast<const T*>(a.x[w]) + xo[w] + h * a.xs[w][2];
-            va[r] = load8<T>(x + d0);
-            vb[r] = load8<T>(x + d1);
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const int hh = h0 + r * hstep;
-        if (hh < heads) {
-          const int w = hh >= a.H[0], h = hh - (w ? a.H[0] : 0);
-          if (turn || !a.in_place[w]) {
-            float fa[8], fb[8];
-            unpack8<T>(va[r], fa);
-            unpack8<T>(vb[r], fb);
-            if (turn) rotate_chunk(fa, fb, cs, a.rope.interleaved);
-            T* y = static_cast<T*>(a.y[w]) + yo[w] + h * a.ys[w][2];
-            store8<T>(y + d0, fa);
-            store8<T>(y + d1, fb);
-          }
-        }
-      }
-    }
-    return;
-  }
-  // one pair, or one element past rotary_dim, per lane
   const bool turn = c < half;
   const int d0 = turn ? (a.rope.interleaved ? 2 * c : c) : 2 * half + (c - half);
   const int d1 = a.rope.interleaved ? d0 + 1 : d0 + half;
-  const float2 cs = turn ? cs_sm[k * half + c] : make_float2(1.f, 0.f);
-  for (int hh = hl; hh < heads; hh += hstep) {
-    const int w = hh >= a.H[0], h = hh - (w ? a.H[0] : 0);
-    const T* x = static_cast<const T*>(a.x[w]) + xo[w] + h * a.xs[w][2];
-    T* y = static_cast<T*>(a.y[w]) + yo[w] + h * a.ys[w][2];
-    if (turn) {
-      const float u = to_f32<T>(x[d0]), v = to_f32<T>(x[d1]);
-      y[d0] = from_f32<T>(u * cs.x - v * cs.y);
-      y[d1] = from_f32<T>(u * cs.y + v * cs.x);
-    } else if (!a.in_place[w]) {
-      y[d0] = x[d0];
+  const float cs = turn ? cs_sm[2 * k * half + c] : 1.f;
+  const float sn = turn ? cs_sm[(2 * k + 1) * half + c] : 0.f;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const T* x = static_cast<const T*>(a.x[w]) + token_off(a.xs[w], b, s);
+    T* y = static_cast<T*>(a.y[w]) + token_off(a.ys[w], b, s);
+    for (int h = hl; h < a.H[w]; h += hstep) {
+      const T* xh = x + h * a.xs[w][2];
+      T* yh = y + h * a.ys[w][2];
+      if (turn) {
+        const float u = to_f32<T>(xh[d0]), v = to_f32<T>(xh[d1]);
+        yh[d0] = from_f32<T>(u * cs - v * sn);
+        yh[d1] = from_f32<T>(u * sn + v * cs);
+      } else if (!a.in_place[w]) {
+        yh[d0] = xh[d0];
+      }
     }
   }
 }
@@ -125,11 +158,13 @@ int launch_t(const RotaryArgs& a, cudaStream_t st) {
   int tt = 8;
   while (tt > 1 && ((a.T + tt - 1) / tt < 2 * 152 || lanes * tt > kThreads)) tt /= 2;
   const unsigned grid = static_cast<unsigned>((a.T + tt - 1) / tt);
-  const size_t smem = static_cast<size_t>(tt) * half * sizeof(float2);
+  const size_t smem =
+      (a.vec ? RowRing<T>::kBytes : 0) + static_cast<size_t>(tt) * 2 * half * sizeof(float);
   if (a.vec)
-    rotary_kernel<T, true><<<grid, kThreads, smem, st>>>(a, tt, lanes);
+    (a.rope.interleaved ? rotary_kernel<T, true> : rotary_kernel<T, false>)<<<grid, kThreads, smem, st>>>(
+        a, tt, lanes);
   else
-    rotary_kernel<T, false><<<grid, kThreads, smem, st>>>(a, tt, lanes);
+    rotary_any_kernel<T><<<grid, kThreads, smem, st>>>(a, tt, lanes);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
