@@ -10,6 +10,8 @@
 // the bound for long spans, the chain start -> context -> table entry for a
 // decode step's few rows.  The row data do not depend on that chain, so the
 // write loads its rows first and resolves the places meanwhile.
+#include <type_traits>
+
 #include "rope.cuh"
 #include "serving.h"
 
@@ -153,13 +155,12 @@ __device__ __forceinline__ Seat seat_of(int lanes, int tt) {
 // meets in one lane and the row's maximum in log2(D / 16) shuffles.  A block takes `tt` tokens; a thread's first rows are on their way
 // (RowRing) before it knows where they go.
 template <typename T, bool kFp8, bool kInter>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     kv_write_kernel(const __grid_constant__ KvPagesArgs a, int tt) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Place place[kMaxTok];
   RowRing<T> ring(smem);
   float* cs_sm = reinterpret_cast<float*>(smem + RowRing<T>::kBytes);  // [tt][cos, sin][half]
-  const int tid = threadIdx.x;
   const int t0 = blockIdx.x * tt, n = min(tt, a.T - t0);
   const int lanes = a.D / 16;
   const Seat st = seat_of(lanes, tt);
@@ -183,50 +184,49 @@ __global__ void __launch_bounds__(kThreads, 3)
   check_starts(a);
   tile_places<true>(a, t0, n, place);
   __syncthreads();
-  Turns turns{};
   if (rot) {
-    for (int e = tid; e < n * half; e += kThreads) {
-      const int k = e / half, i = e - k * half;
-      const float2 cs = rope_cos_sin(place[k].pos, a.rope.turns[i], a.rope.mscale);
-      cs_sm[2 * k * half + i] = cs.x;
-      cs_sm[(2 * k + 1) * half + i] = cs.y;
-    }
+    fill_turns<kThreads>(a.rope, n, [&](int k) { return place[k].pos; }, cs_sm);
     __syncthreads();
-    if (!st.w && st.k < n) turns = turns_of<kInter>(cs_sm + 2 * st.k * half, half, pc);
   }
   const Place p = st.k < n ? place[st.k] : Place{-1, 0, 0};
-  // the row in its page, and the way to the next head's
+  // the pieces in their page, and the way to the next head's
   const int64_t page = a.page_tokens * (kFp8 ? a.D + 1 : a.D * static_cast<int64_t>(sizeof(T)));
-  uint8_t* y = static_cast<uint8_t*>(a.pool[st.w]) + (p.page + st.hl) * page;
   const int64_t ystep = st.hs * page;
-  const int64_t row = static_cast<int64_t>(p.slot) * a.D, scale = a.page_tokens * a.D + p.slot;
+  uint8_t* base = static_cast<uint8_t*>(a.pool[st.w]) + (p.page + st.hl) * page;
+  uint8_t* y = base + (static_cast<int64_t>(p.slot) * a.D + d0) * (kFp8 ? 1 : sizeof(T));
+  uint8_t* scale = base + a.page_tokens * a.D + p.slot;
+  const int dd = d1 - d0;
   bool any_bad = false;
 
+  // A row's way; kTurn: a key to be rotated.  The same trips for the whole
+  // block, and `put` uniform over a row's lanes: the shuffles stay within them.
+  auto rows = [&](auto turn_tag) {
+    constexpr bool kTurn = decltype(turn_tag)::value;
 #pragma unroll 1
-  for (int i = 0; i < steps; ++i) {  // the same trips for the whole block
-    ring.arrived();
-    // uniform over a row's lanes; the shuffles stay within them
-    const bool put = p.page >= 0 && i < mine;
-    const Raw8<T> va = ring.get(i, 0), vb = ring.get(i, 1);
-    float fa[8], fb[8];
-    unpack8<T>(va, fa);
-    unpack8<T>(vb, fb);
-    Piece pa = piece_from<kInter>(fa), pb = piece_from<kInter>(fb);
-    if (!st.w) {
-      rotate_pieces<kInter>(pa, pb, turns, pc);
-      piece_to<kInter>(pa, fa);
-      piece_to<kInter>(pb, fb);
-    }
-    if (kFp8) {
-      float mx = 0.f;
+    for (int i = 0; i < steps; ++i) {
+      ring.arrived();
+      const bool put = p.page >= 0 && i < mine;
+      const Raw8<T> va = ring.get(i, 0), vb = ring.get(i, 1);
+      float fa[8], fb[8];
+      if (kFp8 || kTurn) {
+        unpack8<T>(va, fa);
+        unpack8<T>(vb, fb);
+      }
+      Piece pa = piece_from<kInter>(fa), pb = piece_from<kInter>(fb);
+      if (kTurn) {
+        rotate_pieces<kInter>(pa, pb, cs_sm + 2 * st.k * half, half, pc);
+        piece_to<kInter>(pa, fa);
+        piece_to<kInter>(pb, fb);
+      }
+      if (kFp8) {
+        float mx = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mx = max_abs(mx, fa[j], fb[j]);
-      for (int o = lanes / 2; o > 0; o >>= 1)
-        mx = max_abs(mx, __shfl_xor_sync(0xffffffffu, mx, o), 0.f);
-      if (put) {
+        for (int j = 0; j < 8; ++j) mx = max_abs(mx, fa[j], fb[j]);
+        for (int o = lanes / 2; o > 0; o >>= 1)
+          mx = max_abs(mx, __shfl_xor_sync(0xffffffffu, mx, o), 0.f);
         const uint32_t m = __float_as_uint(mx);
         const bool bad = m >= kInfBits;
-        const int ex = bad ? 0 : row_exponent(m);
+        const int ex = row_exponent(m);
         const float mul = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
         const F2 mul2 = f2(mul, mul);
 #pragma unroll
@@ -236,25 +236,31 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
         piece_to<kInter>(pa, fa);
         piece_to<kInter>(pb, fb);
-        uint4 w = make_uint4(
-            to_e4m3x4(fa[0], fa[1], fa[2], fa[3]), to_e4m3x4(fa[4], fa[5], fa[6], fa[7]),
-            to_e4m3x4(fb[0], fb[1], fb[2], fb[3]), to_e4m3x4(fb[4], fb[5], fb[6], fb[7]));
-        if (bad) w = make_uint4(0u, 0u, 0u, 0u);
-        any_bad |= bad;
-        *reinterpret_cast<uint2*>(y + row + d0) = make_uint2(w.x, w.y);
-        *reinterpret_cast<uint2*>(y + row + d1) = make_uint2(w.z, w.w);
-        if (st.c == 0) y[scale] = static_cast<uint8_t>(bad ? 255 : ex + 127);
+        uint2 wa = make_uint2(to_e4m3x4(fa[0], fa[1], fa[2], fa[3]),
+                              to_e4m3x4(fa[4], fa[5], fa[6], fa[7]));
+        uint2 wb = make_uint2(to_e4m3x4(fb[0], fb[1], fb[2], fb[3]),
+                              to_e4m3x4(fb[4], fb[5], fb[6], fb[7]));
+        if (put) {
+          if (bad) wa = wb = make_uint2(0u, 0u);
+          any_bad |= bad;
+          *reinterpret_cast<uint2*>(y) = wa;
+          *reinterpret_cast<uint2*>(y + dd) = wb;
+          if (st.c == 0) *scale = static_cast<uint8_t>(bad ? 255 : ex + 127);
+        }
+      } else if (put) {
+        T* o = reinterpret_cast<T*>(y);
+        if (kTurn && pc.turn[0]) store8<T>(o, fa);
+        else store_raw<T>(o, va);  // an exact copy
+        if (kTurn && pc.turn[1]) store8<T>(o + dd, fb);
+        else store_raw<T>(o + dd, vb);
       }
-    } else if (put) {
-      T* o = reinterpret_cast<T*>(y) + row;
-      if (pc.turn[0]) store8<T>(o + d0, fa);
-      else store_raw<T>(o + d0, va);  // an exact copy
-      if (pc.turn[1]) store8<T>(o + d1, fb);
-      else store_raw<T>(o + d1, vb);
+      y += ystep;
+      scale += ystep;
+      fetch(i + RowRing<T>::kRowsAhead);
     }
-    y += ystep;
-    fetch(i + RowRing<T>::kRowsAhead);
-  }
+  };
+  if (rot && !st.w) rows(std::true_type{});
+  else rows(std::false_type{});
   if (any_bad && st.c == 0 && a.err_word) atomicOr(a.err_word, SA_ERRBIT_NONFINITE);
 }
 
@@ -320,27 +326,24 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- read ------------------------------------------------------------------------------------
 
-// Sixteen codes times a scale -> sixteen elements.
+// Eight codes times a scale -> eight elements.
 template <typename T>
-__device__ __forceinline__ void store16(T* y, const uint4& codes, float scale, int aligned) {
-  const uint32_t wd[4] = {codes.x, codes.y, codes.z, codes.w};
-  float f[2][8];
+__device__ __forceinline__ void put8(T* y, const uint2& codes, float scale, int aligned) {
+  float f[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     uint32_t h2;
     asm("{\n\t.reg .b16 t;\n\tmov.b16 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
         : "=r"(h2)
-        : "h"(static_cast<uint16_t>(wd[i / 2] >> (16 * (i & 1)))));
+        : "h"(static_cast<uint16_t>((i / 2 ? codes.y : codes.x) >> (16 * (i & 1)))));
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-    f2_split(f2_mul(f2(v.x, v.y), f2(scale, scale)), f[i / 4][2 * (i % 4)],
-             f[i / 4][2 * (i % 4) + 1]);
+    f2_split(f2_mul(f2(v.x, v.y), f2(scale, scale)), f[2 * i], f[2 * i + 1]);
   }
   if (aligned) {
-    store8<T>(y, f[0]);
-    store8<T>(y + 8, f[1]);
+    store8<T>(y, f);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = from_f32<T>(f[i / 8][i % 8]);
+    for (int i = 0; i < 8; ++i) y[i] = from_f32<T>(f[i]);
   }
 }
 
@@ -351,8 +354,9 @@ __device__ __forceinline__ float e8m0(uint32_t byte) {
                        : __uint_as_float(byte << 23);
 }
 
-// FP8 pages -> rows: 16 codes per lane, kBatch rows in flight per thread; a
-// block takes `tt` rows of every head.
+// FP8 pages -> rows: 16 codes per lane, eight of each half of the row so that an
+// access of a row's lanes is one run; kBatch rows in flight per thread; a block
+// takes `tt` rows of every head.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     kv_read_fp8_kernel(const __grid_constant__ KvPagesArgs a, int tt) {
@@ -367,23 +371,28 @@ __global__ void __launch_bounds__(kThreads)
   if (p.page < 0) return;
   const int64_t page = a.page_tokens * (a.D + 1), xstep = st.hs * page;
   const uint8_t* x = static_cast<const uint8_t*>(a.pool[st.w]) + (p.page + st.hl) * page;
-  const int64_t row = static_cast<int64_t>(p.slot) * a.D + 16 * st.c;
+  const int64_t row = static_cast<int64_t>(p.slot) * a.D + 8 * st.c;
   const int64_t scale = a.page_tokens * a.D + p.slot;
   T* y = static_cast<T*>(a.x[st.w]) + (t0 + st.k) * a.xs[st.w][0] + st.hl * a.xs[st.w][1] +
-         16 * st.c;
+         8 * st.c;
   const int64_t ystep = st.hs * a.xs[st.w][1];
   for (int h = st.hl; h < a.Hkv; h += kBatch * st.hs) {
-    uint4 codes[kBatch];
+    uint2 codes[kBatch][2];
     uint32_t sb[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
       if (h + i * st.hs < a.Hkv) {
-        codes[i] = __ldg(reinterpret_cast<const uint4*>(x + i * xstep + row));
+        codes[i][0] = __ldg(reinterpret_cast<const uint2*>(x + i * xstep + row));
+        codes[i][1] = __ldg(reinterpret_cast<const uint2*>(x + i * xstep + row + a.D / 2));
         sb[i] = __ldg(x + i * xstep + scale);
       }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (h + i * st.hs < a.Hkv) store16<T>(y + i * ystep, codes[i], e8m0(sb[i]), a.aligned);
+      if (h + i * st.hs < a.Hkv) {
+        const float m = e8m0(sb[i]);
+        put8<T>(y + i * ystep, codes[i][0], m, a.aligned);
+        put8<T>(y + i * ystep + a.D / 2, codes[i][1], m, a.aligned);
+      }
     x += kBatch * xstep;
     y += kBatch * ystep;
   }

@@ -30,17 +30,14 @@ __device__ __forceinline__ int64_t token_off(const int64_t (&st)[3], int b, int 
 }
 
 // The tokens' tables.
-__device__ __forceinline__ void fill_turns(const RotaryArgs& a, int t0, int tt, float* cs_sm) {
-  const int half = a.rope.rotary_dim / 2;
-  for (int e = threadIdx.x; e < tt * half; e += kThreads) {
-    const int k = e / half, i = e - k * half, t = t0 + k;
-    if (t < a.T) {
-      const int b = t / a.S;
-      const float2 cs = rope_cos_sin(position_of(a, b, t - b * a.S), a.rope.turns[i], a.rope.mscale);
-      cs_sm[2 * k * half + i] = cs.x;
-      cs_sm[(2 * k + 1) * half + i] = cs.y;
-    }
-  }
+__device__ __forceinline__ void tile_turns(const RotaryArgs& a, int t0, int tt, float* cs_sm) {
+  fill_turns<kThreads>(
+      a.rope, min(tt, a.T - t0),
+      [&](int k) {
+        const int b = (t0 + k) / a.S;
+        return position_of(a, b, t0 + k - b * a.S);
+      },
+      cs_sm);
 }
 
 template <typename T, bool kInter>
@@ -83,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     ring.commit();
   };
   for (int i = 0; i < RowRing<T>::kRowsAhead; ++i) fetch(i);
-  fill_turns(a, t0, tt, cs_sm);
+  tile_turns(a, t0, tt, cs_sm);
   __syncthreads();
   const Turns turns = turns_of<kInter>(cs_sm + 2 * k * half, half, pc);
   T* yp = y[0];
@@ -119,7 +116,7 @@ __global__ void __launch_bounds__(kThreads)
     rotary_any_kernel(const __grid_constant__ RotaryArgs a, int tt, int lanes) {
   extern __shared__ __align__(16) float cs_sm[];
   const int half = a.rope.rotary_dim / 2, t0 = blockIdx.x * tt;
-  fill_turns(a, t0, tt, cs_sm);
+  tile_turns(a, t0, tt, cs_sm);
   __syncthreads();
   const int c = threadIdx.x % lanes, slot = threadIdx.x / lanes;
   const int k = slot % tt, hl = slot / tt, hstep = kThreads / (lanes * tt);

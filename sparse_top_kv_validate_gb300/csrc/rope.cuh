@@ -19,6 +19,26 @@ __device__ __forceinline__ float2 rope_cos_sin(int64_t pos, uint64_t turns, floa
   return make_float2(c * m, s * m);
 }
 
+// The tables of a tile's `n` tokens in shared memory, [n][cos, sin][half], by a
+// block of kThreads; pos(k) is token k's position.
+template <int kThreads, typename Pos>
+__device__ __forceinline__ void fill_turns(const sa_rope& rope, int n, Pos pos, float* table) {
+  const int half = rope.rotary_dim / 2;
+  const int dk = kThreads / half, di = kThreads - dk * half;
+  int k = threadIdx.x / half, i = threadIdx.x - k * half;
+  while (k < n) {
+    const float2 cs = rope_cos_sin(pos(k), rope.turns[i], rope.mscale);
+    table[2 * k * half + i] = cs.x;
+    table[(2 * k + 1) * half + i] = cs.y;
+    k += dk;
+    i += di;
+    if (i >= half) {
+      i -= half;
+      ++k;
+    }
+  }
+}
+
 // A lane's two 8-element pieces of a row of D elements, chunk c of D / 16:
 // neighbouring lanes' pieces are neighbours, so that an access of a row's lanes
 // is one run.  Half layout: the two sides of pairs 8c .. 8c + 7, and past
@@ -95,6 +115,14 @@ struct Turns {
 };
 
 // From a token's table in shared memory: `half` cosines, then `half` sines.
+__device__ __forceinline__ void four_turns(const float* at, int half, F2* c, F2* s) {
+  const float4 x = *reinterpret_cast<const float4*>(at);
+  const float4 y = *reinterpret_cast<const float4*>(at + half);
+  c[0] = f2(x.x, x.y);
+  c[1] = f2(x.z, x.w);
+  s[0] = f2(y.x, y.y);
+  s[1] = f2(y.z, y.w);
+}
 template <bool kInter>
 __device__ __forceinline__ Turns turns_of(const float* table, int half, const Pieces& p) {
   Turns t;
@@ -105,12 +133,7 @@ __device__ __forceinline__ Turns turns_of(const float* table, int half, const Pi
       continue;
     }
     const float* at = table + (kInter ? p.d[i] / 2 : p.d[0] + 4 * i);
-    const float4 x = *reinterpret_cast<const float4*>(at);
-    const float4 y = *reinterpret_cast<const float4*>(at + half);
-    t.c[2 * i] = f2(x.x, x.y);
-    t.c[2 * i + 1] = f2(x.z, x.w);
-    t.s[2 * i] = f2(y.x, y.y);
-    t.s[2 * i + 1] = f2(y.z, y.w);
+    four_turns(at, half, t.c + 2 * i, t.s + 2 * i);
   }
   return t;
 }
@@ -138,6 +161,26 @@ __device__ __forceinline__ void rotate_pieces(Piece& a, Piece& b, const Turns& t
   } else if (p.turn[0]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) rotate2(a.x[i], b.x[i], t.c[i], t.s[i]);
+  }
+}
+
+// The same with the turns read as they are needed: sixteen registers fewer.
+template <bool kInter>
+__device__ __forceinline__ void rotate_pieces(Piece& a, Piece& b, const float* table, int half,
+                                              const Pieces& p) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!p.turn[i]) continue;
+    F2 c[2], s[2];
+    four_turns(table + (kInter ? p.d[i] / 2 : p.d[0] + 4 * i), half, c, s);
+    if (kInter) {
+      Piece& x = i ? b : a;
+      rotate2(x.x[0], x.x[1], c[0], s[0]);
+      rotate2(x.x[2], x.x[3], c[1], s[1]);
+    } else {
+      rotate2(a.x[2 * i], b.x[2 * i], c[0], s[0]);
+      rotate2(a.x[2 * i + 1], b.x[2 * i + 1], c[1], s[1]);
+    }
   }
 }
 
@@ -188,7 +231,7 @@ struct RowRing {
 
   __device__ __forceinline__ explicit RowRing(void* smem)
       : own(static_cast<uint4*>(smem) + threadIdx.x) {}
-  __device__ __forceinline__ uint4* part(int row, int piece, int i) {
+  __device__ __forceinline__ uint4* part(uint32_t row, int piece, int i) {
     return own + (((row % kRowsAhead) * 2 + piece) * kParts + i) * kRingThreads;
   }
   __device__ __forceinline__ void fetch(int row, int piece, const T* p, bool aligned) {
@@ -201,6 +244,7 @@ struct RowRing {
                      : "memory");
       } else {
         T* e = reinterpret_cast<T*>(part(row, piece, i));
+#pragma unroll 1
         for (int j = 0; j < static_cast<int>(16 / sizeof(T)); ++j)
           e[j] = p[i * (16 / sizeof(T)) + j];
       }
