@@ -589,8 +589,8 @@ int attn_prefill(const sa_prefill_params* p, void* stream);
  * dtype SA_F16 / SA_BF16 / SA_F32; scale 0 means 1/sqrt(D).  Workspace rules
  * as for sparse_attn_decode.
  * pool_format SA_FP8_E4M3_PAGE: quantised pages (q and y SA_F16 or SA_BF16, D
- * 64 / 128 / 256, page_tokens a multiple of 16, B <= 4096, pools 16-byte aligned, options
- * 0); k_new / v_new are quantised as paged_kv_write does.  The codes' values
+ * 64 / 128 / 256, page_tokens a multiple of 16, B <= 4096, q, y and pools 16-byte
+ * aligned, options 0); k_new / v_new are quantised as paged_kv_write does.  The codes' values
  * enter the products exactly and the scales in fp32.
  */
 typedef struct {

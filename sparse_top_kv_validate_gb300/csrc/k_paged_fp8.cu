@@ -59,7 +59,11 @@ struct FGeo {
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kHeads = 8 * NT;
   // per CTA: rings | partials | stage scales | barriers | merge lists | tile prefix
-  static constexpr int kPartFloats = kHeads * (D + 2);     // o, then m and l per head
+  // a partial: o (rows 16 bytes apart in the banks, so that the lanes' stores to
+  // different heads do not meet), then m and l per head
+  static constexpr int kPartRow = D + 4;
+  static constexpr int kPartMl = kHeads * kPartRow;
+  static constexpr int kPartFloats = kPartMl + 2 * kHeads;
   static constexpr int kOffPart = kWarps * kStages * kStageBytes;
   static constexpr int kOffScale = kOffPart + kWarps * kPartFloats * 4;
   static constexpr int kOffBar = kOffScale + kWarps * kStages * 32;
@@ -281,19 +285,23 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
         const int hh = nt * 8 + gid;
         const bool live = hh < hpu;
         const T* qr = qp + (cur.b * a.Hq + cur.grp * a.hpu + (live ? hh : 0)) * D;
+        // this lane's dims as they lie: two contraction steps per load
+#pragma unroll
+        for (int kk = 0; kk < G::kKs; kk += 2) {
+          const uint4 r = __ldg(reinterpret_cast<const uint4*>(qr + q_dim(kk)));
+          qf[nt][kk][0] = r.x;
+          qf[nt][kk][1] = r.y;
+          qf[nt][kk + 1][0] = r.z;
+          qf[nt][kk + 1][1] = r.w;
+        }
         float amax = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < G::kKs; ++kk) {
-          float f[4];
+        for (int kk = 0; kk < G::kKs; ++kk)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[e] = to_f32<T>(qr[q_dim(kk) + e]);
-            amax = fmaxf(amax, fabsf(f[e]));
+          for (int e = 0; e < 2; ++e) {
+            const T* x = reinterpret_cast<const T*>(&qf[nt][kk][e]);
+            amax = fmaxf(amax, fmaxf(fabsf(to_f32<T>(x[0])), fabsf(to_f32<T>(x[1]))));
           }
-          // kept raw in T's own 16 bits until the row's maximum is known
-          qf[nt][kk][0] = pack2<T>(f[0], f[1]);
-          qf[nt][kk][1] = pack2<T>(f[2], f[3]);
-        }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // a power of two that puts amax into [2^14, 2^15); kept inside fp32's exponents
@@ -351,16 +359,21 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
             const float inv = (m_run[nt][j] == SA_NEG_INF || l == 0.f) ? 0.f : up_v / l;
             T* yp = static_cast<T*>(a.y) + static_cast<int64_t>(head0 + hh) * D;
 #pragma unroll
-            for (int mt = 0; mt < G::kKs; ++mt)
-              *reinterpret_cast<uint32_t*>(yp + dim_of(mt)) = pack2<T>(o[mt][nt][j] * inv, o[mt][nt][2 + j] * inv);
+            for (int mt = 0; mt < G::kKs; mt += 4) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack2<T>(o[mt + i][nt][j] * inv, o[mt + i][nt][2 + j] * inv);
+              *reinterpret_cast<uint4*>(yp + dim_of(mt)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           } else {
 #pragma unroll
-            for (int mt = 0; mt < G::kKs; ++mt)
-              *reinterpret_cast<float2*>(po + hh * D + dim_of(mt)) = make_float2(o[mt][nt][j] * up_v, o[mt][nt][2 + j] * up_v);
-            if (gid == 0) {
-              po[G::kHeads * D + 2 * hh] = m_run[nt][j];
-              po[G::kHeads * D + 2 * hh + 1] = l;
-            }
+            for (int mt = 0; mt < G::kKs; mt += 2)
+              *reinterpret_cast<float4*>(po + hh * G::kPartRow + dim_of(mt)) =
+                  make_float4(o[mt][nt][j] * up_v, o[mt][nt][2 + j] * up_v,
+                              o[mt + 1][nt][j] * up_v, o[mt + 1][nt][2 + j] * up_v);
+            if (gid == 0)
+              *reinterpret_cast<float2*>(po + G::kPartMl + 2 * hh) = make_float2(m_run[nt][j], l);
           }
         }
     };
@@ -614,17 +627,17 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
       const int hh = x / (D / 4), d = (x - hh * (D / 4)) * 4;
       float M = SA_NEG_INF;
       for (int f = e; f <= last; ++f)
-        if (parts[f].where >= 0) M = fmaxf(M, fsm[parts[f].where + G::kHeads * D + 2 * hh]);
+        if (parts[f].where >= 0) M = fmaxf(M, fsm[parts[f].where + G::kPartMl + 2 * hh]);
       float L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int f = e; f <= last; ++f) {
         const int w = parts[f].where;
         if (w < 0) continue;
-        const float m = fsm[w + G::kHeads * D + 2 * hh];
-        if (m == SA_NEG_INF) continue;
-        const float c = ex2(m - M);
-        const float4 v = *reinterpret_cast<const float4*>(fsm + w + hh * D + d);
-        L += fsm[w + G::kHeads * D + 2 * hh + 1] * c;
+        const float2 ml = *reinterpret_cast<const float2*>(fsm + w + G::kPartMl + 2 * hh);
+        if (ml.x == SA_NEG_INF) continue;
+        const float c = ex2(ml.x - M);
+        const float4 v = *reinterpret_cast<const float4*>(fsm + w + hh * G::kPartRow + d);
+        L += ml.y * c;
         acc.x = fmaf(v.x, c, acc.x);
         acc.y = fmaf(v.y, c, acc.y);
         acc.z = fmaf(v.z, c, acc.z);
@@ -632,9 +645,8 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
       }
       if (whole) {
         const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
-        uint32_t* yp = reinterpret_cast<uint32_t*>(static_cast<T*>(a.y) + static_cast<int64_t>(p.head0 + hh) * D + d);
-        yp[0] = pack2<T>(acc.x * inv, acc.y * inv);
-        yp[1] = pack2<T>(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.y) + static_cast<int64_t>(p.head0 + hh) * D + d) =
+            make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
       } else {
         *reinterpret_cast<float4*>(a.part_o + (slot + hh) * D + d) = acc;
         if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * (slot + hh)) = make_float2(M, L);
@@ -700,9 +712,8 @@ __global__ void __launch_bounds__(128) fp8_combine_kernel(const GatherArgs a) {
     }
   }
   const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
-  uint32_t* y = reinterpret_cast<uint32_t*>(static_cast<T*>(a.y) + (b * a.Hq + grp * a.hpu + hh) * a.D + d);
-  y[0] = pack2<T>(acc.x * inv, acc.y * inv);
-  y[1] = pack2<T>(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.y) + (b * a.Hq + grp * a.hpu + hh) * a.D + d) =
+      make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
 }
 
 // A pool as rows of codes: [pages * heads, page_tokens, D] bytes, the page stride with
