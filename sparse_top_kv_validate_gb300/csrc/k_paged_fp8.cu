@@ -111,6 +111,17 @@ __device__ __forceinline__ Unit unit_at(const GatherArgs& a, const int32_t* pref
   return r;
 }
 
+// The unit after u (there is one: the caller's range goes on).
+__device__ __forceinline__ void next_unit(const GatherArgs& a, const int32_t* pref, Unit& u) {
+  u.off += u.tu;
+  if (++u.grp < static_cast<int32_t>(a.Hkv)) return;
+  u.grp = 0;
+  do ++u.b;
+  while (pref[u.b + 1] == pref[u.b]);
+  u.tu = pref[u.b + 1] - pref[u.b];
+  u.ctx = __ldg(a.ctx_len + u.b);
+}
+
 // A unit's partial result in shared memory: where, whose, and what of it it covers.
 struct Part {
   int32_t unit_off, unit_tu;   // first tile and tiles of the unit
@@ -213,8 +224,12 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
     enter(t_begin);
     auto look = [&](int32_t t) {
       if (n_left == 0) {
-        nxt = unit_at(a, pref, t);
+        next_unit(a, pref, nxt);
         enter(t);
+        // its queries, wanted in S tiles' time
+        const T* qr = static_cast<const T*>(a.q) + (nxt.b * a.Hq + nxt.grp * a.hpu) * D;
+        for (int x = lane * 64; x < hpu * D; x += 32 * 64)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(qr + x));
       }
       const Ahead h{__ldg(table), n_slot, n_head};
       n_slot += 16;
@@ -388,7 +403,7 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
     for (int32_t t = t_begin; t < t_end; ++t, left -= 16) {
       if (left <= 0) {
         flush_unit();
-        cur = unit_at(a, pref, t);
+        next_unit(a, pref, cur);
         left = cur.ctx;
         start_unit();
       }
