@@ -51,7 +51,6 @@
 
 #include <cmath>
 #include <cstring>
-#include <mutex>
 #include <type_traits>
 #include <utility>
 
@@ -69,8 +68,10 @@ constexpr int kLead = 2;                 // K tiles loaded ahead of the V tiles
 constexpr int kTile = 128;               // rows of a query tile; keys of a K/V tile
 constexpr int kSlabBytes = kTile * 128;  // 128 rows x 64 sixteen-bit columns
 constexpr float kRescaleLog2 = 8.0f;     // lazy-maximum slack (factor 256)
-constexpr int kTanhTerms = 5;            // tanh(x) ~= x * sum_k c_k (x^2)^k
-constexpr float kTanhPolyBound = 0.625f; // |x| range of the fit (abs error ~1e-7)
+// tanh(x) ~= x * sum_k c_k (x^2)^k: the terms and the |x| range of two fits, of an
+// absolute error of 1e-7 both
+constexpr int kTanhTerms = 5, kTanhShortTerms = 3;
+constexpr float kTanhBound = 0.625f, kTanhShortBound = 0.25f;
 constexpr float kFixedOffsetMaxLog2 = 97.0f;  // softcap * log2(e) up to which 2^logit needs no offset
 constexpr int kMaxSeqs = 1024;           // sequences per launch
 constexpr int kSmemLimit = 227 * 1024;
@@ -116,9 +117,11 @@ struct Params {
   int tpt;                 // tokens per query tile: 128 / g
   int causal;
   int cap_items;           // places in the item list
-  float k1;                // x = score * k1 (scale / softcap), or the raw score
-  float c_log2;            // log2-domain multiplier of tanh(x) (softcap * log2e) or of x (scale * log2e)
-  float tq[kTanhTerms];    // c_log2 * c_k: the tanh polynomial already in log2 units
+  float k1;                // x = score * k1 (scale / softcap)
+  float c_log2;            // log2-domain multiplier of tanh(x) (softcap * log2e) or of the score (scale * log2e)
+  // c_log2 tanh(k1 s) as polynomials in the score s, and the |s| up to which they hold
+  float tq[kTanhTerms], tq_bound;
+  float ts[kTanhShortTerms], ts_bound;
 };
 
 // ---- work items -----------------------------------------------------------------------
@@ -462,36 +465,45 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
   tc05::tmem_st_wait();
 }
 
-// How the log2-domain logit of x is formed: c_log2 * x (no softcap), or
-// c_log2 * tanh(x) by the fitted polynomial (kPoly) or, where a score of the
-// warp lies outside its range, from the hardware exponential and reciprocal.
-enum ScoreMode { kPlain = 0, kPoly = 1, kFar = 2 };
+// How the log2-domain logit of a score s is formed: c_log2 s (no softcap), or
+// c_log2 tanh(k1 s) by the fitted polynomials (kShort, kPoly) or, where a score of
+// the warp lies outside their ranges, from the hardware exponential and reciprocal.
+enum ScoreMode { kPlain = 0, kShort = 1, kPoly = 2, kFar = 3 };
+
+// The constants of that: c2 = c_log2, k1 and the polynomials.
+struct Logits {
+  float c2, k1;
+  float tq[kTanhTerms], ts[kTanhShortTerms];
+};
 
 __device__ __forceinline__ float tanh_far(float x) {
   // 1 - 2 / (e^2x + 1), absolute error below 2^-20; saturates cleanly
   return 1.0f - 2.0f * rcp(ex2(x * (2.0f * kLog2e)) + 1.0f);
 }
 
-__device__ __forceinline__ float poly_logit(float x, const float (&tq)[kTanhTerms]) {
+template <int N>
+__device__ __forceinline__ float poly_logit(float x, const float (&tq)[N]) {
   const float y = x * x;
-  float q = tq[kTanhTerms - 1];
+  float q = tq[N - 1];
 #pragma unroll
-  for (int k = kTanhTerms - 2; k >= 0; --k) q = fmaf(q, y, tq[k]);
+  for (int k = N - 2; k >= 0; --k) q = fmaf(q, y, tq[k]);
   return x * q;
 }
+template <int N>
+__device__ __forceinline__ uint64_t poly_logit2(uint64_t x, const float (&tq)[N], uint64_t add) {
+  const uint64_t y = f2_mul(x, x);
+  uint64_t q = f2_pack(tq[N - 1], tq[N - 1]);
+#pragma unroll
+  for (int k = N - 2; k >= 0; --k) q = f2_fma(q, y, f2_pack(tq[k], tq[k]));
+  return f2_fma(x, q, add);
+}
 
-// x = s * k1 of 32 scores in place (softcap), and their largest magnitude.
-__device__ __forceinline__ float scale_chunk(uint32_t (&r)[32], float k1) {
-  const uint64_t k2 = f2_pack(k1, k1);
+// The largest magnitude of 32 scores.
+__device__ __forceinline__ float largest(const uint32_t (&r)[32]) {
   float ax[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float a, b;
-    f2_unpack(f2_mul(f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), k2), a, b);
-    r[2 * i] = __float_as_uint(a);
-    r[2 * i + 1] = __float_as_uint(b);
-    ax[i & 1] = max3(ax[i & 1], fabsf(a), fabsf(b));
-  }
+  for (int i = 0; i < 16; ++i)
+    ax[i & 1] = max3(ax[i & 1], fabsf(__uint_as_float(r[2 * i])), fabsf(__uint_as_float(r[2 * i + 1])));
   return fmaxf(ax[0], ax[1]);
 }
 
@@ -510,29 +522,20 @@ __device__ __forceinline__ float max_chunk(uint32_t (&r)[32], int rel, float m) 
   return fmaxf(mx[0], mx[1]);
 }
 
-// p = 2^(logit(x) - m) of 32 columns, masked ones 0, as 16 packed pairs; added to
+// p = 2^(logit - m) of 32 columns, masked ones 0, as 16 packed pairs; added to
 // the two partial sums.
 template <int kMode, bool kMask, typename T>
-__device__ __forceinline__ void exp_chunk(const uint32_t (&r)[32], uint32_t (&pk)[16], float c2, float neg_m,
-                                          const float (&tq)[kTanhTerms], int rel, uint64_t (&ls)[2]) {
-  const uint64_t c2x2 = f2_pack(c2, c2), nm2 = f2_pack(neg_m, neg_m);
+__device__ __forceinline__ void exp_chunk(const uint32_t (&r)[32], uint32_t (&pk)[16], const Logits& lg, float neg_m,
+                                          int rel, uint64_t (&ls)[2]) {
+  const uint64_t c2x2 = f2_pack(lg.c2, lg.c2), nm2 = f2_pack(neg_m, neg_m);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float x0 = __uint_as_float(r[2 * i]), x1 = __uint_as_float(r[2 * i + 1]);
     uint64_t v;
-    if (kMode == kPlain) {
-      v = f2_fma(f2_pack(x0, x1), c2x2, nm2);
-    } else if (kMode == kFar) {
-      v = f2_fma(f2_pack(tanh_far(x0), tanh_far(x1)), c2x2, nm2);
-    } else {
-      const uint64_t xx = f2_pack(x0, x1);
-      const uint64_t y = f2_mul(xx, xx);
-      uint64_t q = f2_fma(f2_pack(tq[4], tq[4]), y, f2_pack(tq[3], tq[3]));
-      q = f2_fma(q, y, f2_pack(tq[2], tq[2]));
-      q = f2_fma(q, y, f2_pack(tq[1], tq[1]));
-      q = f2_fma(q, y, f2_pack(tq[0], tq[0]));
-      v = f2_fma(xx, q, nm2);
-    }
+    if (kMode == kPlain) v = f2_fma(f2_pack(x0, x1), c2x2, nm2);
+    else if (kMode == kFar) v = f2_fma(f2_pack(tanh_far(x0 * lg.k1), tanh_far(x1 * lg.k1)), c2x2, nm2);
+    else if (kMode == kPoly) v = poly_logit2(f2_pack(x0, x1), lg.tq, nm2);
+    else v = poly_logit2(f2_pack(x0, x1), lg.ts, nm2);
     float a, b;
     f2_unpack(v, a, b);
     if (kMask) {
@@ -569,10 +572,13 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
   const uint32_t tS0 = tmem + lanes + G::kColS, tO = tmem + lanes + G::kColO;
   volatile float* xch = reinterpret_cast<volatile float*>(sm + G::kOffXch) + row;
   const int rt = row / p.g;  // token of the tile that this row belongs to
-  const float c2 = p.c_log2, k1 = p.k1;
-  float tq[kTanhTerms];
+  Logits lg;
+  lg.c2 = p.c_log2;
+  lg.k1 = p.k1;
 #pragma unroll
-  for (int i = 0; i < kTanhTerms; ++i) tq[i] = p.tq[i];
+  for (int i = 0; i < kTanhTerms; ++i) lg.tq[i] = p.tq[i];
+#pragma unroll
+  for (int i = 0; i < kTanhShortTerms; ++i) lg.ts[i] = p.ts[i];
   // The other warpgroup's post after its tile u (every one is waited for, in order).
   auto posted = [&](uint32_t u) {
     return wait_or_abort_warp(&bars[G::kBarPost + 2 * (wg ^ 1) + ((u >> 1) & 1)], (u >> 2) & 1, abort_flag, p.err_word);
@@ -612,7 +618,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       }
       float ax = 0.f, mx = SA_NEG_INF;
       auto look = [&](uint32_t (&x)[32], int c) {
-        if (kCap) ax = fmaxf(ax, scale_chunk(x, k1));
+        if (kCap) ax = fmaxf(ax, largest(x));
         if (!kFixed) mx = masked ? max_chunk<true>(x, rel - 32 * c, mx) : max_chunk<false>(x, 0, mx);
       };
 #pragma unroll 1
@@ -625,11 +631,15 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
         look(r[1], c + 1);
       }
       int mode = kPlain;
-      if (kCap) mode = __any_sync(0xffffffffu, ax > kTanhPolyBound) ? kFar : kPoly;
+      if (kCap)
+        mode = !__any_sync(0xffffffffu, !(ax <= p.ts_bound)) ? kShort : !__any_sync(0xffffffffu, !(ax <= p.tq_bound)) ? kPoly : kFar;
       if (!kFixed) {
         float mt = SA_NEG_INF;
         if (mx != SA_NEG_INF)
-          mt = mode == kPlain ? mx * c2 : mode == kPoly ? poly_logit(mx, tq) : tanh_far(mx) * c2;
+          mt = mode == kPlain   ? mx * lg.c2
+               : mode == kShort ? poly_logit(mx, lg.ts)
+               : mode == kPoly  ? poly_logit(mx, lg.tq)
+                                : tanh_far(mx * lg.k1) * lg.c2;
         const bool up = mt > m + kRescaleLog2 || (m == SA_NEG_INF && mt > m);
         xch[(2 * wg + ((u >> 1) & 1)) * kTile] = up ? mt : m;
         __syncwarp();
@@ -656,12 +666,12 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       auto exps = [&](uint32_t (&x)[32], int c) {
         const int rc = rel - 32 * c;
         uint32_t pk[16];
-        if (kCap) scale_chunk(x, k1);
-        if (!kCap && masked) exp_chunk<kPlain, true, T>(x, pk, c2, neg_m, tq, rc, ls);
-        else if (!kCap) exp_chunk<kPlain, false, T>(x, pk, c2, neg_m, tq, 0, ls);
-        else if (mode == kFar) exp_chunk<kFar, true, T>(x, pk, c2, neg_m, tq, masked ? rc : kTile, ls);
-        else if (masked) exp_chunk<kPoly, true, T>(x, pk, c2, neg_m, tq, rc, ls);
-        else exp_chunk<kPoly, false, T>(x, pk, c2, neg_m, tq, rc, ls);
+        if (!kCap && masked) exp_chunk<kPlain, true, T>(x, pk, lg, neg_m, rc, ls);
+        else if (!kCap) exp_chunk<kPlain, false, T>(x, pk, lg, neg_m, 0, ls);
+        else if (mode == kFar) exp_chunk<kFar, true, T>(x, pk, lg, neg_m, masked ? rc : kTile, ls);
+        else if (mode == kPoly) exp_chunk<kPoly, true, T>(x, pk, lg, neg_m, masked ? rc : kTile, ls);
+        else if (masked) exp_chunk<kShort, true, T>(x, pk, lg, neg_m, rc, ls);
+        else exp_chunk<kShort, false, T>(x, pk, lg, neg_m, 0, ls);
         tc05::tmem_st16(tS + c * 16, pk);
       };
 #pragma unroll 1
@@ -879,44 +889,62 @@ bool rows_map(CUtensorMap* m, const void* base, int dtype, int64_t D, int64_t H,
 // Least-squares fit of tanh(x) / x = sum_k c_k (x^2)^k over 0 < x <= B (Chebyshev
 // nodes in x; normal equations in u = x^2 / B^2, solved in double by Gaussian
 // elimination with partial pivoting).
-void fit_tanh(double (&c)[kTanhTerms]) {
+template <int N>
+void fit_tanh(double B, double (&c)[N]) {
   constexpr int kNodes = 2048;
-  const double B = kTanhPolyBound, pi = 3.14159265358979323846;
-  double A[kTanhTerms][kTanhTerms + 1] = {};
+  const double pi = 3.14159265358979323846;
+  double A[N][N + 1] = {};
   for (int i = 0; i < kNodes; ++i) {
     const double x = B * std::cos(pi * (i + 0.5) / (2.0 * kNodes));
     const double u = x * x / (B * B), f = std::tanh(x) / x;
-    double pw[kTanhTerms];
+    double pw[N];
     pw[0] = 1.0;
-    for (int k = 1; k < kTanhTerms; ++k) pw[k] = pw[k - 1] * u;
-    for (int r = 0; r < kTanhTerms; ++r) {
-      for (int q = 0; q < kTanhTerms; ++q) A[r][q] += pw[r] * pw[q];
-      A[r][kTanhTerms] += pw[r] * f;
+    for (int k = 1; k < N; ++k) pw[k] = pw[k - 1] * u;
+    for (int r = 0; r < N; ++r) {
+      for (int q = 0; q < N; ++q) A[r][q] += pw[r] * pw[q];
+      A[r][N] += pw[r] * f;
     }
   }
-  for (int col = 0; col < kTanhTerms; ++col) {
+  for (int col = 0; col < N; ++col) {
     int piv = col;
-    for (int r = col + 1; r < kTanhTerms; ++r)
+    for (int r = col + 1; r < N; ++r)
       if (std::fabs(A[r][col]) > std::fabs(A[piv][col])) piv = r;
-    for (int q = 0; q <= kTanhTerms; ++q) std::swap(A[col][q], A[piv][q]);
-    for (int r = 0; r < kTanhTerms; ++r) {
+    for (int q = 0; q <= N; ++q) std::swap(A[col][q], A[piv][q]);
+    for (int r = 0; r < N; ++r) {
       if (r == col) continue;
       const double f = A[r][col] / A[col][col];
-      for (int q = col; q <= kTanhTerms; ++q) A[r][q] -= f * A[col][q];
+      for (int q = col; q <= N; ++q) A[r][q] -= f * A[col][q];
     }
   }
   double scale = 1.0;  // 1 / B^(2k): back from u to x^2
-  for (int k = 0; k < kTanhTerms; ++k) {
-    c[k] = A[k][kTanhTerms] / A[k][k] * scale;
+  for (int k = 0; k < N; ++k) {
+    c[k] = A[k][N] / A[k][k] * scale;
     scale /= B * B;
   }
 }
 
-const double* tanh_coefficients() {
-  static std::once_flag once;
-  static double c[kTanhTerms];
-  std::call_once(once, [] { fit_tanh(c); });
-  return c;
+struct TanhFits {
+  double full[kTanhTerms], brief[kTanhShortTerms];
+  TanhFits() {
+    fit_tanh(kTanhBound, full);
+    fit_tanh(kTanhShortBound, brief);
+  }
+};
+
+// c_log2 tanh(k1 s) as a polynomial in s: coefficient k is c_log2 c_k k1^(2k + 1).
+// The largest |s| of the fit's range; -1, so that no score is in it, where a
+// coefficient leaves fp32's normal range (a scale very far from the softcap).
+template <int N>
+float score_polynomial(const double (&c)[N], double bound, double softcap, double k1, float (&out)[N]) {
+  double f = softcap * 1.4426950408889634 * k1;
+  bool ok = true;
+  for (int k = 0; k < N; ++k) {
+    out[k] = static_cast<float>(c[k] * f);
+    ok = ok && std::isnormal(out[k]);
+    f *= k1 * k1;
+  }
+  const double most = bound / k1;
+  return ok && most < 1e18 ? static_cast<float>(most) : -1.0f;  // (s^2 is a finite fp32)
 }
 
 // Shared memory with `seqs` sequences and `items` places in the item list.
@@ -960,11 +988,10 @@ int launch_t(const PackedArgs& a, cudaStream_t st) {
     p.k1 = a.scale / a.softcap;
     p.c_log2 = a.softcap * log2e;
     variant = p.c_log2 <= kFixedOffsetMaxLog2 ? kVarCapFixed : kVarCapMax;
-    const double* c = tanh_coefficients();
-    for (int k = 0; k < kTanhTerms; ++k)
-      p.tq[k] = static_cast<float>(c[k] * static_cast<double>(a.softcap) * 1.4426950408889634);
+    static const TanhFits fits;
+    p.tq_bound = score_polynomial(fits.full, kTanhBound, a.softcap, p.k1, p.tq);
+    p.ts_bound = score_polynomial(fits.brief, kTanhShortBound, a.softcap, p.k1, p.ts);
   } else {
-    p.k1 = 1.0f;
     p.c_log2 = a.scale * log2e;
   }
   const int sms = sm_count();
