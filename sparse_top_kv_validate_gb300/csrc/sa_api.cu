@@ -847,7 +847,8 @@ static int check_paged(const sa_paged_params* p, int query = 0) {
         p->options != 0 || p->B > kFp8PagesMaxBatch)
       return SA_ERR_UNSUPPORTED;
     if ((p->k_new == nullptr) != (p->v_new == nullptr)) return SA_ERR_NULL;
-    if (!aligned16(p->k_pool) || !aligned16(p->v_pool) || !aligned16(p->q) || !aligned16(p->y))
+    if (!aligned16(p->k_pool) || !aligned16(p->v_pool) || !aligned16(p->q) || !aligned16(p->y) ||
+        (reinterpret_cast<uintptr_t>(p->k_new) | reinterpret_cast<uintptr_t>(p->v_new)) % 2)
       return SA_ERR_ALIGN;
   }
   if (p->num_pages * p->Hkv * p->page_tokens >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;

@@ -122,6 +122,11 @@ def test_fp8_page_decode_refusals(host_lib, change, status):  # noqa: F811
     assert host_lib.paged_attn_decode(C.byref(_set(_fp8_decode(), **change)), None) == status
 
 
+@pytest.mark.parametrize("change", [dict(q=0x100008), dict(y=0x200008), dict(k_new=0x700001, v_new=0x800000)])
+def test_fp8_page_decode_wants_aligned_rows(host_lib, change):  # noqa: F811
+    assert host_lib.paged_attn_decode(C.byref(_set(_fp8_decode(), **change)), None) == -4
+
+
 def test_fp8_page_decode_needs_its_workspace(host_lib):  # noqa: F811
     p = _fp8_decode()
     need = host_lib.paged_attn_decode_workspace(C.byref(p))
