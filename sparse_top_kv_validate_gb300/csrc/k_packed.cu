@@ -17,13 +17,15 @@
 //    softmax, PV, buffer free) takes about four times as long as its MMAs: three
 //    tiles on the way at once, two of them in softmax, keep the tensor cores
 //    about half busy.  Measured, 4 x 4,096 tokens, 32 / 8 heads of 128, causal,
-//    bf16: 463 us, 1,189 TFLOP/s.  Other orders tried: two row tiles per item
-//    that share K and V, a score buffer and a warpgroup each, 500 us; the same
-//    with two MMA lanes that interleave, so that both tiles' softmax runs at the
-//    same time, 625 us; with two warpgroups per row tile, half the columns
-//    each, 646 us.
-//  * A thread reads its 128 scores from tensor memory twice, in a loop over
-//    chunks of 32 columns.  Kept in registers they spill, and local memory
+//    bf16: 453 us, 1,214 TFLOP/s (softcap 50: 478 us).  Other orders tried, at
+//    463 us for this one: two row tiles per item that share K and V, a score
+//    buffer and a warpgroup each, 500 us; the same with two MMA lanes that
+//    interleave, so that both tiles' softmax runs at the same time, 625 us; with
+//    two warpgroups per row tile, half the columns each, 646 us.
+//  * P is passed on in halves: the PV of the first 64 keys runs while the other
+//    64 probabilities are still being formed (463 -> 453 us).
+//  * A thread reads its 128 scores from tensor memory twice (once where the
+//    offset is fixed, below), in a loop over chunks of 32 columns.  Kept in registers they spill, and local memory
 //    shares its path with the MMAs' shared-memory operands; unrolled, the
 //    roles' loops no longer fit the instruction cache together (both measured:
 //    575 us).
@@ -86,13 +88,13 @@ struct Geo {
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffBar = kOffV + kStages * kTileBytes;
   // barriers: per Q buffer q_full, q_empty; per ring slot k_full, k_empty, v_full,
-  // v_ready (past warp 2), v_empty; per score buffer s_full, p_full, pv_done; o_full,
+  // v_ready (past warp 2), v_empty; per score buffer s_full, p_full (two halves), pv_done; o_full,
   // o_read; per warpgroup and turn posted (offsets), sums; per MMA lane done.  (A
   // warpgroup may be one post ahead of the other's wait, never two.)
   static constexpr int kBarQFull = 0, kBarQEmpty = 2, kBarKFull = 4, kBarKEmpty = kBarKFull + kStages,
                        kBarVFull = kBarKEmpty + kStages, kBarVReady = kBarVFull + kStages,
                        kBarVEmpty = kBarVReady + kStages, kBarS = kBarVEmpty + kStages,
-                       kBarP = kBarS + kSBufs, kBarPv = kBarP + kSBufs, kBarO = kBarPv + kSBufs,
+                       kBarP = kBarS + kSBufs, kBarPv = kBarP + 2 * kSBufs, kBarO = kBarPv + kSBufs,
                        kBarORead = kBarO + 1, kBarPost = kBarORead + 1, kBarSum = kBarPost + 4,
                        kBarDone = kBarSum + 4, kNumBars = kBarDone + 2;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
@@ -421,14 +423,20 @@ __device__ void value_lane(const Params& p, const Work& work, uint8_t* sm, uint6
     for (int j = 0; ok && j < it.n; ++j, ++t) {
       const uint32_t slot = t % G::kStages;
       ok = wait_or_abort(&bars[G::kBarVReady + slot], (t / G::kStages) & 1, abort_flag, p.err_word) &&
-           wait_or_abort(&bars[G::kBarP + buf], buf_use & 1, abort_flag, p.err_word);
+           wait_or_abort(&bars[G::kBarP + 2 * buf], buf_use & 1, abort_flag, p.err_word);
       if (!ok) break;
       tc05::fence_after_sync();
       const uint64_t v0 = dV + ((slot * G::kTileBytes) >> 4);
       const uint32_t tP = tmem + G::kColS + buf * kTile;
 #pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
+      for (int kk = 0; kk < kTile / 32; ++kk)
         tc05::mma_ts(tmem + G::kColO, tP + kk * 8, v0 + ((kk * 2048) >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+      ok = wait_or_abort(&bars[G::kBarP + 2 * buf + 1], buf_use & 1, abort_flag, p.err_word);
+      if (!ok) break;
+      tc05::fence_after_sync();
+#pragma unroll
+      for (int kk = kTile / 32; kk < kTile / 16; ++kk)
+        tc05::mma_ts(tmem + G::kColO, tP + kk * 8, v0 + ((kk * 2048) >> 4), id_o, 1u);
       tc05::commit(&bars[G::kBarPv + buf]);
       tc05::commit(&bars[G::kBarVEmpty + slot]);
       if (j == it.n - 1) tc05::commit(&bars[G::kBarO]);
@@ -616,23 +624,30 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
           m = o;
         }
       }
-      float ax = 0.f, mx = SA_NEG_INF;
-      auto look = [&](uint32_t (&x)[32], int c) {
-        if (kCap) ax = fmaxf(ax, largest(x));
-        if (!kFixed) mx = masked ? max_chunk<true>(x, rel - 32 * c, mx) : max_chunk<false>(x, 0, mx);
+      auto mode_of = [&](float most) {  // the cheapest form that holds for the warp's scores
+        return !__any_sync(0xffffffffu, !(most <= p.ts_bound))   ? kShort
+               : !__any_sync(0xffffffffu, !(most <= p.tq_bound)) ? kPoly
+                                                                 : kFar;
       };
-#pragma unroll 1
-      for (int c = 0; c < 4; c += 2) {  // the next chunk (at last the first again) is on its way meanwhile
-        tc05::tmem_ld_wait();
-        tc05::tmem_ld32(tS + 32 * (c + 1), r[1]);
-        look(r[0], c);
-        tc05::tmem_ld_wait();
-        tc05::tmem_ld32(tS + 32 * ((c + 2) & 3), r[0]);
-        look(r[1], c + 1);
-      }
       int mode = kPlain;
-      if (kCap)
-        mode = !__any_sync(0xffffffffu, !(ax <= p.ts_bound)) ? kShort : !__any_sync(0xffffffffu, !(ax <= p.tq_bound)) ? kPoly : kFar;
+      float mx = SA_NEG_INF;
+      if (!kFixed) {
+        float ax = 0.f;
+        auto look = [&](uint32_t (&x)[32], int c) {
+          if (kCap) ax = fmaxf(ax, largest(x));
+          mx = masked ? max_chunk<true>(x, rel - 32 * c, mx) : max_chunk<false>(x, 0, mx);
+        };
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {  // the next chunk (at last the first again) is on its way meanwhile
+          tc05::tmem_ld_wait();
+          tc05::tmem_ld32(tS + 32 * (c + 1), r[1]);
+          look(r[0], c);
+          tc05::tmem_ld_wait();
+          tc05::tmem_ld32(tS + 32 * ((c + 2) & 3), r[0]);
+          look(r[1], c + 1);
+        }
+        if (kCap) mode = mode_of(ax);
+      }
       if (!kFixed) {
         float mt = SA_NEG_INF;
         if (mx != SA_NEG_INF)
@@ -666,6 +681,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       auto exps = [&](uint32_t (&x)[32], int c) {
         const int rc = rel - 32 * c;
         uint32_t pk[16];
+        if (kFixed) mode = mode_of(largest(x));
         if (!kCap && masked) exp_chunk<kPlain, true, T>(x, pk, lg, neg_m, rc, ls);
         else if (!kCap) exp_chunk<kPlain, false, T>(x, pk, lg, neg_m, 0, ls);
         else if (mode == kFar) exp_chunk<kFar, true, T>(x, pk, lg, neg_m, masked ? rc : kTile, ls);
@@ -682,11 +698,12 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
         tc05::tmem_ld_wait();
         if (c == 0) tc05::tmem_ld32(tS + 64, r[0]);
         exps(r[1], c + 1);
+        // half of P is there: its PV need not wait for the other half
+        tc05::tmem_st_wait();
+        tc05::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[G::kBarP + 2 * buf + c / 2]);
       }
-      tc05::tmem_st_wait();
-      tc05::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[G::kBarP + buf]);
       j += 2;
     }
 
@@ -818,7 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&bars[G::kBarS + i], 1);
-      mbar_init(&bars[G::kBarP + i], 4);
+      mbar_init(&bars[G::kBarP + 2 * i], 4);
+      mbar_init(&bars[G::kBarP + 2 * i + 1], 4);
       mbar_init(&bars[G::kBarPv + i], 1);
     }
     mbar_init(&bars[G::kBarO], 1);
