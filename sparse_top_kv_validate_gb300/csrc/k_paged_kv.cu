@@ -23,20 +23,31 @@ constexpr int kThreads = kRingThreads;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTok = 16;  // tokens per block
 
-// Sequence that owns packed row r: the largest b with start[b] <= r, found by
-// the whole warp, 32 probes per step (two dependent loads for 1,024
-// sequences).  Negative when the row is nobody's.
-__device__ __forceinline__ int owner_of(const int32_t* start, int B, int r, int lane) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
+// Sequence b = the largest with start[b] <= r, its rows and context: found by the
+// whole warp, 32 probes per step, the last step's bringing all of it at once (one
+// load's latency up to 32 sequences).  b < 0 when the row is nobody's.
+struct Owner {
+  int b, first, next, ctx;
+};
+__device__ __forceinline__ Owner owner_of(const KvPagesArgs& a, int r, int lane) {
+  int lo = 0, hi = a.B;
+  while (hi - lo > 32) {
     const int step = (hi - lo + 31) / 32;
     const int at = lo + lane * step;
-    const bool le = at < hi && __ldg(start + at) <= r;
+    const bool le = at < hi && __ldg(a.seq_start + at) <= r;
     const int n = __popc(__ballot_sync(0xffffffffu, le));
     if (n > 1) lo += (n - 1) * step;  // starts out of order: still below hi
     hi = min(lo + step, hi);
   }
-  return (__ldg(start + lo) <= r && r < __ldg(start + lo + 1)) ? lo : -1;
+  const int at = min(lo + lane, hi - 1);
+  Owner o{at, __ldg(a.seq_start + at), __ldg(a.seq_start + at + 1), __ldg(a.ctx_len + at)};
+  const int n = __popc(__ballot_sync(0xffffffffu, lo + lane < hi && o.first <= r)), from = max(n - 1, 0);
+  o.b = __shfl_sync(0xffffffffu, o.b, from);
+  o.first = __shfl_sync(0xffffffffu, o.first, from);
+  o.next = __shfl_sync(0xffffffffu, o.next, from);
+  o.ctx = __shfl_sync(0xffffffffu, o.ctx, from);
+  if (!(o.first <= r && r < o.next)) o.b = -1;
+  return o;
 }
 
 struct Place {
@@ -44,20 +55,17 @@ struct Place {
   int32_t slot, pos;
 };
 
-// Where packed row r of sequence b lives.  kWrite: the rows are the last of the
+// Where packed row r of a sequence lives.  kWrite: the rows are the last of the
 // context; else its first.
 template <bool kWrite>
-__device__ __forceinline__ Place place_in(const KvPagesArgs& a, int b, int r) {
+__device__ __forceinline__ Place place_in(const KvPagesArgs& a, const Owner& o, int r) {
   Place p{-1, 0, 0};
-  const int first = a.seq_start ? __ldg(a.seq_start + b) : r;
-  const int n = a.seq_start ? __ldg(a.seq_start + b + 1) - first : 1;
-  const int64_t ctx = __ldg(a.ctx_len + b);
-  const int64_t pos = (kWrite ? ctx - n : 0) + (r - first);
+  const int64_t pos = (kWrite ? static_cast<int64_t>(o.ctx) - (o.next - o.first) : 0) + (r - o.first);
   int32_t page = -1;
-  if (pos >= 0 && pos < ctx && ctx <= a.max_pages * a.page_tokens) {
+  if (pos >= 0 && pos < o.ctx && o.ctx <= a.max_pages * a.page_tokens) {
     // a context is an int32: 32-bit division
     const uint32_t pi = static_cast<uint32_t>(pos) / static_cast<uint32_t>(a.page_tokens);
-    page = __ldg(a.block_table + b * a.max_pages + pi);
+    page = __ldg(a.block_table + o.b * a.max_pages + pi);
     p.slot = static_cast<int32_t>(pos - static_cast<int64_t>(pi) * a.page_tokens);
     p.pos = static_cast<int32_t>(pos);
   }
@@ -69,11 +77,11 @@ __device__ __forceinline__ Place place_in(const KvPagesArgs& a, int b, int r) {
   return p;
 }
 
-// The same for a row whose sequence is not known: by a warp, uniform over it.
+// Row r's place, by a warp, uniform over it.
 template <bool kWrite>
 __device__ __forceinline__ Place place_of(const KvPagesArgs& a, int r, int lane) {
-  const int b = a.seq_start ? owner_of(a.seq_start, a.B, r, lane) : r;
-  return b < 0 ? Place{-1, 0, 0} : place_in<kWrite>(a, b, r);
+  const Owner o = a.seq_start ? owner_of(a, r, lane) : Owner{r, r, r + 1, __ldg(a.ctx_len + r)};
+  return o.b < 0 ? Place{-1, 0, 0} : place_in<kWrite>(a, o, r);
 }
 
 // The places of a tile's `n` tokens, by the whole block.  A tile inside one
@@ -83,9 +91,9 @@ template <bool kWrite>
 __device__ __forceinline__ void tile_places(const KvPagesArgs& a, int t0, int n, Place* place) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (a.seq_start && n > 1) {
-    const int b = owner_of(a.seq_start, a.B, t0, lane);
-    if (b >= 0 && t0 + n <= __ldg(a.seq_start + b + 1)) {
-      if (threadIdx.x < n) place[threadIdx.x] = place_in<kWrite>(a, b, t0 + threadIdx.x);
+    const Owner o = owner_of(a, t0, lane);
+    if (o.b >= 0 && t0 + n <= o.next) {
+      if (threadIdx.x < n) place[threadIdx.x] = place_in<kWrite>(a, o, t0 + threadIdx.x);
       return;
     }
   }
@@ -180,12 +188,13 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     ring.commit();
   };
+  TurnTables<kThreads> tables(a.rope);
   for (int i = 0; i < RowRing<T>::kRowsAhead; ++i) fetch(i);
   check_starts(a);
   tile_places<true>(a, t0, n, place);
   __syncthreads();
   if (rot) {
-    fill_turns<kThreads>(a.rope, n, [&](int k) { return place[k].pos; }, cs_sm);
+    tables.fill(a.rope, n, [&](int k) { return place[k].pos; }, cs_sm);
     __syncthreads();
   }
   const Place p = st.k < n ? place[st.k] : Place{-1, 0, 0};

@@ -30,8 +30,9 @@ __device__ __forceinline__ int64_t token_off(const int64_t (&st)[3], int b, int 
 }
 
 // The tokens' tables.
-__device__ __forceinline__ void tile_turns(const RotaryArgs& a, int t0, int tt, float* cs_sm) {
-  fill_turns<kThreads>(
+__device__ __forceinline__ void tile_turns(const RotaryArgs& a, TurnTables<kThreads>& tables, int t0, int tt,
+                                           float* cs_sm) {
+  tables.fill(
       a.rope, min(tt, a.T - t0),
       [&](int k) {
         const int b = (t0 + k) / a.S;
@@ -79,8 +80,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     ring.commit();
   };
+  TurnTables<kThreads> tables(a.rope);
   for (int i = 0; i < RowRing<T>::kRowsAhead; ++i) fetch(i);
-  tile_turns(a, t0, tt, cs_sm);
+  tile_turns(a, tables, t0, tt, cs_sm);
   __syncthreads();
   const Turns turns = turns_of<kInter>(cs_sm + 2 * k * half, half, pc);
   T* yp = y[0];
@@ -116,7 +118,8 @@ __global__ void __launch_bounds__(kThreads)
     rotary_any_kernel(const __grid_constant__ RotaryArgs a, int tt, int lanes) {
   extern __shared__ __align__(16) float cs_sm[];
   const int half = a.rope.rotary_dim / 2, t0 = blockIdx.x * tt;
-  tile_turns(a, t0, tt, cs_sm);
+  TurnTables<kThreads> tables(a.rope);
+  tile_turns(a, tables, t0, tt, cs_sm);
   __syncthreads();
   const int c = threadIdx.x % lanes, slot = threadIdx.x / lanes;
   const int k = slot % tt, hl = slot / tt, hstep = kThreads / (lanes * tt);

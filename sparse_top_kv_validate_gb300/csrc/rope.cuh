@@ -19,25 +19,47 @@ __device__ __forceinline__ float2 rope_cos_sin(int64_t pos, uint64_t turns, floa
   return make_float2(c * m, s * m);
 }
 
-// The tables of a tile's `n` tokens in shared memory, [n][cos, sin][half], by a
-// block of kThreads; pos(k) is token k's position.
-template <int kThreads, typename Pos>
-__device__ __forceinline__ void fill_turns(const sa_rope& rope, int n, Pos pos, float* table) {
-  const int half = rope.rotary_dim / 2;
-  const int dk = kThreads / half, di = kThreads - dk * half;
-  int k = threadIdx.x / half, i = threadIdx.x - k * half;
-  while (k < n) {
-    const float2 cs = rope_cos_sin(pos(k), rope.turns[i], rope.mscale);
-    table[2 * k * half + i] = cs.x;
-    table[(2 * k + 1) * half + i] = cs.y;
-    k += dk;
-    i += di;
-    if (i >= half) {
-      i -= half;
-      ++k;
+// The fraction of pair i, by an ordinary load: the kernel's parameters lie in
+// constant memory, which serves a warp one address at a time (read that way, the
+// tables took 6 of the page write's 31 us for 16,384 tokens).
+__device__ __forceinline__ uint64_t turn_of(const sa_rope& rope, int i) {
+  uint64_t f;
+  asm volatile("ld.u64 %0, [%1];" : "=l"(f) : "l"(&rope.turns[i]));
+  return f;
+}
+
+// The tables of a tile's tokens in shared memory, [n][cos, sin][half], by a block of
+// kThreads.  Made before the positions are known, so that its load is under way.
+template <int kThreads>
+struct TurnTables {
+  int half, dk, di, k, i;
+  uint64_t f;
+  __device__ __forceinline__ explicit TurnTables(const sa_rope& rope) {
+    half = max(rope.rotary_dim / 2, 1);  // (no rotation: one pair's table, not filled)
+    dk = kThreads / half;
+    di = kThreads - dk * half;
+    k = threadIdx.x / half;
+    i = threadIdx.x - k * half;
+    f = turn_of(rope, i);
+  }
+  // pos(k): token k's position, for n tokens.
+  template <typename Pos>
+  __device__ __forceinline__ void fill(const sa_rope& rope, int n, Pos pos, float* table) {
+    while (k < n) {
+      const float2 cs = rope_cos_sin(pos(k), f, rope.mscale);
+      table[2 * k * half + i] = cs.x;
+      table[(2 * k + 1) * half + i] = cs.y;
+      k += dk;
+      if (di == 0) continue;
+      i += di;
+      if (i >= half) {
+        i -= half;
+        ++k;
+      }
+      f = turn_of(rope, i);
     }
   }
-}
+};
 
 // A lane's two 8-element pieces of a row of D elements, chunk c of D / 16:
 // neighbouring lanes' pieces are neighbours, so that an access of a row's lanes
