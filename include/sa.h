@@ -713,7 +713,7 @@ int rotary_embed(const sa_rotary_params* p, void* stream);
  * ctx_len outside [0, max_pages * page_tokens] sets SA_ERRBIT_PAGE, starts that
  * decrease or leave [0, T] set SA_ERRBIT_SEQ (err_word nullable); such rows are
  * skipped, and no access leaves the tensors.  Two rows written to one slot (a
- * page shared by two sequences) leave either row's bytes there.
+ * page shared by two sequences) leave bytes of both there, in no order.
  * pool_format 0 (pages [num_pages, Hkv, page_tokens, D] of dtype) serves any D
  * up to 1024; the rope then needs rotary_dim <= D.  No workspace.
  */

@@ -35,6 +35,16 @@
 //    split across CTAs leaves partials, one per CTA, for fp8_combine_kernel.
 //    (With a partial per warp the merge of a 131,072-token context, 282 partials
 //    per unit, took longer than the attention.)
+//  * Where a warp goes from one unit to the next, the unit follows by a step (no
+//    search), and its queries were prefetched when its first tile was issued: short
+//    contexts, many units per warp, are bound by these changes.
+//
+// Measured (8 KV heads of 128, pages of 16 or 32; 6.80 TB/s copy): 128 sequences of
+// 1,024 to 32,768 tokens, 4.5 GB, 727 us, 90% of the copy bandwidth; one context of
+// 131,072 among 23 of some hundred, 290 MB, 79 us (54%; about 20 us are launch, tile
+// space, the rings' first fill and the merges, the rest the short contexts' changes
+// of unit on ten CTAs); one sequence of 1,500, 16.4 us, latency.  Twelve warps per CTA
+// with three stages: sixteen with two 800 us and 85 us, ten with four 848 and 95.
 #include "gather_common.cuh"
 #include "serving.h"
 #include "tc05.cuh"
@@ -85,7 +95,34 @@ __device__ __forceinline__ float e8m0_f32(uint32_t byte) {
   return __uint_as_float((byte << 23) | odd);
 }
 
-// (tile indices stay below 2^31, checked on the host)
+// (tile indices and places stay below 2^31, checked on the host)
+//
+// Ranges are cut in a space that gives every unit kFp8UnitCost places before its
+// tiles, for what a warp does at a change of unit: tile i of a unit at `place` lies
+// at place + kFp8UnitCost + i, and a warp takes the tiles of its R places.  (One
+// context of 131,072 among 23 short ones: 68 us, 79 with a cost of 0; 400 contexts of
+// 350: 73.4, 72.6 with 0, 75.9 with 8.)
+__device__ __forceinline__ int32_t unit_place(const GatherArgs& a, int32_t seq_tiles_before, int32_t b, int32_t grp,
+                                              int32_t tu) {
+  return static_cast<int32_t>(a.Hkv) * (seq_tiles_before + kFp8UnitCost * b) + grp * (tu + kFp8UnitCost);
+}
+
+// Tiles that lie before place x.
+__device__ __forceinline__ int32_t tiles_before(const GatherArgs& a, const int32_t* pref, int32_t x) {
+  int lo = 0, hi = static_cast<int>(a.B);  // largest b whose first place is <= x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (unit_place(a, pref[mid], mid, 0, 0) <= x) lo = mid;
+    else hi = mid;
+  }
+  const int32_t heads = static_cast<int32_t>(a.Hkv);
+  const int32_t tb = pref[lo + 1] - pref[lo], y = x - unit_place(a, pref[lo], lo, 0, 0);
+  const int32_t q = static_cast<int32_t>(static_cast<uint32_t>(y) / static_cast<uint32_t>(tb + kFp8UnitCost));
+  const int32_t grp = min(q, heads);  // (heads: past the last sequence)
+  const int32_t z = y - grp * (tb + kFp8UnitCost) - kFp8UnitCost;
+  return heads * pref[lo] + grp * tb + (grp < heads && z > 0 ? z : 0);
+}
+
 struct Unit {
   int32_t off, tu;      // first tile, tiles
   int32_t b, grp;       // sequence, head group
@@ -124,8 +161,8 @@ __device__ __forceinline__ void next_unit(const GatherArgs& a, const int32_t* pr
 
 // A unit's partial result in shared memory: where, whose, and what of it it covers.
 struct Part {
-  int32_t unit_off, unit_tu;   // first tile and tiles of the unit
-  int32_t head0;               // b * Hq + first query head
+  int32_t unit_off;            // first tile of the unit
+  int32_t b, grp;              // sequence, head group
   int32_t where;               // float offset of o from the shared-memory base (-1: none)
 };
 
@@ -177,7 +214,7 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
     }
   }
   __syncthreads();
-  const int64_t total = a.Hkv * static_cast<int64_t>(pref[a.B]);
+  const int32_t total = unit_place(a, pref[a.B], static_cast<int32_t>(a.B), 0, 0);
   const int64_t gw_total = static_cast<int64_t>(gridDim.x) * NW;
   int64_t R = (total + gw_total - 1) / gw_total;
   if (R < min_range) R = min_range;
@@ -191,11 +228,15 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
         for (int64_t e = lane; e < a.Hq * D / 2; e += 32)
           reinterpret_cast<uint32_t*>(a.y)[b * (a.Hq * D / 2) + e] = 0u;
   }
-  const int64_t c_begin = static_cast<int64_t>(blockIdx.x) * NW * R;
-  if (c_begin >= total) return;  // the whole CTA
-  const int32_t c_end = static_cast<int32_t>(min(c_begin + NW * R, total));
-  const int32_t t_begin = static_cast<int32_t>(min(c_begin + warp * R, total));
-  const int32_t t_end = static_cast<int32_t>(min(c_begin + (warp + 1) * R, total));
+  const int64_t c_first = static_cast<int64_t>(blockIdx.x) * NW * R;
+  if (c_first >= total) return;  // the whole CTA
+  const int32_t c_place = static_cast<int32_t>(c_first), c_end = c_place + NW * static_cast<int32_t>(R);
+  int32_t t_begin, t_end;
+  {
+    const int32_t t = tiles_before(a, pref, c_place + (warp + (lane & 1)) * static_cast<int32_t>(R));
+    t_begin = __shfl_sync(0xffffffffu, t, 0);
+    t_end = __shfl_sync(0xffffffffu, t, 1);
+  }
 
   if (t_begin < t_end) {
     uint8_t* ring = sm + warp * S * G::kStageBytes;
@@ -359,7 +400,7 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
                          : reinterpret_cast<float*>(sm + G::kOffPart) + warp * G::kPartFloats;
       const int32_t head0 = static_cast<int32_t>(cur.b * a.Hq + cur.grp * a.hpu);
       if (!whole && lane == 0)
-        parts[2 * warp + second] = Part{cur.off, cur.tu, head0, static_cast<int32_t>(po - reinterpret_cast<float*>(sm))};
+        parts[2 * warp + second] = Part{cur.off, cur.b, cur.grp, static_cast<int32_t>(po - reinterpret_cast<float*>(sm))};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -635,9 +676,11 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
     const int last = starts ? __ffs(starts) - 2 : 2 * NW - 1;
     if (g % (NW / share) != warp / share) continue;
     const Part p = parts[e];
-    const bool whole = p.unit_off >= c_begin && p.unit_off + p.unit_tu <= c_end;
-    // slot 0: the CTA's range begins inside the unit (or with it), else 1
-    const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (c_begin >= p.unit_off ? 0 : 1)) * a.hpu;
+    const int32_t tu = pref[p.b + 1] - pref[p.b], place = unit_place(a, pref[p.b], p.b, p.grp, tu);
+    const bool whole = place + kFp8UnitCost >= c_place && place + kFp8UnitCost + tu <= c_end;
+    const int64_t head0 = p.b * a.Hq + p.grp * a.hpu;
+    // slot 0: the CTA's places begin inside the unit's (or with them), else 1
+    const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (c_place >= place ? 0 : 1)) * a.hpu;
     for (int x = part0 * 32 + lane; x < hpu * (D / 4); x += share * 32) {
       const int hh = x / (D / 4), d = (x - hh * (D / 4)) * 4;
       float M = SA_NEG_INF;
@@ -660,7 +703,7 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
       }
       if (whole) {
         const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.y) + static_cast<int64_t>(p.head0 + hh) * D + d) =
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.y) + (head0 + hh) * D + d) =
             make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
       } else {
         *reinterpret_cast<float4*>(a.part_o + (slot + hh) * D + d) = acc;
@@ -685,13 +728,14 @@ __global__ void __launch_bounds__(128) fp8_combine_kernel(const GatherArgs a) {
   const int64_t u = row / a.hpu;
   if (u >= a.units) return;
   const int hh = static_cast<int>(row - u * a.hpu);
-  const int64_t b = u / a.Hkv, grp = u - b * a.Hkv;
-  const int64_t R = a.meta[0], lo = a.pref_out[b], tu = a.pref_out[b + 1] - lo;
-  const int64_t off = a.Hkv * lo + grp * tu;
+  const int32_t b = static_cast<int32_t>(u / a.Hkv), grp = static_cast<int32_t>(u - b * a.Hkv);
+  const int64_t R = a.meta[0];  // places per CTA
+  const int32_t lo = a.pref_out[b], tu = a.pref_out[b + 1] - lo;
+  const int32_t place = unit_place(a, lo, b, grp, tu), first = place + kFp8UnitCost;
   if (tu == 0) return;
-  const int64_t c0 = off / R, c1 = (off + tu - 1) / R;
+  const int64_t c0 = first / R, c1 = (first + tu - 1) / R;
   if (c0 == c1) return;  // written by the attention kernel
-  auto part = [&](int64_t c) { return (c * 2 + (c * R >= off ? 0 : 1)) * a.hpu + hh; };
+  auto part = [&](int64_t c) { return (c * 2 + (c * R >= place ? 0 : 1)) * a.hpu + hh; };
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
   float M = SA_NEG_INF, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -903,7 +903,9 @@ static bool plan_fp8_pages(const sa_paged_params* p, Plan& pl) {
   g.units = g.B * g.Hkv;
   const int64_t context = p->max_pages * p->page_tokens;
   if (context >= (int64_t(1) << 31) || p->num_pages * p->Hkv >= (int64_t(1) << 31) ||
-      p->B * p->Hq >= (int64_t(1) << 31) || g.units * ((context + 15) / 16) >= (int64_t(1) << 31))
+      p->B * p->Hq >= (int64_t(1) << 31) ||
+      // (the last CTA's range may end past the last tile)
+      g.units * ((context + 15) / 16 + sa::kFp8UnitCost) >= (int64_t(1) << 31) - (int64_t(1) << 20))
     return false;
   size_t off = 0;
   pl.off_meta = off;

@@ -63,6 +63,7 @@ int launch_kv_read(const KvPagesArgs& a, int dtype, cudaStream_t st);
 // GatherArgs of the paged source with Hkv the number of query-head groups
 // (KV heads times sub-groups) and g = hpu heads per group.  Launches the attention
 // kernel (one CTA per SM) and the merge of the units split across its CTAs.
+constexpr int kFp8UnitCost = 2;               // tiles that a change of unit costs a warp
 int64_t fp8_pages_max_heads(int D);           // query heads one group can hold
 int launch_fp8_pages(const GatherArgs& a, int64_t pool_heads, int dtype, int sms,
                      cudaStream_t st);
