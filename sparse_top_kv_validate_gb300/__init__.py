@@ -17,6 +17,7 @@ from __future__ import annotations
 import contextlib
 import ctypes as C
 import os
+import struct
 import threading
 
 import torch
@@ -181,6 +182,14 @@ class PackedParams(C.Structure):
     ]
 
 
+# The serving-step calls pack their parameters as bytes of the structures above (filling
+# a ctypes structure field by field takes as long as the launch).
+_ROTARY = struct.Struct("6P2i18q")
+_KV_PAGES = struct.Struct("9P2i11q")
+_PACKED = struct.Struct("7P2i14q2f")
+_PAGED = struct.Struct("8PiI7qfi2PN")
+
+
 class SAError(RuntimeError):
     def __init__(self, call: str, status: int):
         super().__init__(f"{call}: status {status} ({status_string(status)})")
@@ -251,15 +260,13 @@ def load():
         L.paged_attn_decode_workspace.restype = C.c_size_t
         L.paged_attn_decode_workspace.argtypes = [C.POINTER(PagedParams)]
         L.paged_attn_decode.restype = C.c_int
-        L.paged_attn_decode.argtypes = [C.POINTER(PagedParams), _p]
+        L.paged_attn_decode.argtypes = [_p, _p]
         L.sa_rope_table.restype = C.c_int
         L.sa_rope_table.argtypes = [C.POINTER(_RopeConfig), C.POINTER(RopeTable)]
-        for name, params in (("rotary_embed", RotaryParams), ("paged_kv_write", KvPagesParams),
-                             ("paged_kv_read", KvPagesParams),
-                             ("attn_prefill_packed", PackedParams)):
+        for name in ("rotary_embed", "paged_kv_write", "paged_kv_read", "attn_prefill_packed"):
             fn = getattr(L, name)
             fn.restype = C.c_int
-            fn.argtypes = [C.POINTER(params), _p]
+            fn.argtypes = [_p, _p]
         _lib = L
         return _lib
 
@@ -319,6 +326,10 @@ def _dev(t, name):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
@@ -603,8 +614,8 @@ def paged_attn_decode(q, k_pool, v_pool, block_table, ctx_len, *, k_new=None, v_
 
 def _paged_fp8_decode(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, scale, err_word,
                       y, workspace, stream, options):
-    shape = q.shape
-    B, D, Hkv = shape[0], shape[-1], k_pool.shape[1]
+    shape, pool = q.shape, k_pool.shape
+    B, D, Hkv = shape[0], shape[-1], pool[1]
     if not (len(shape) == 3 or (len(shape) == 4 and shape[2] == 1)):
         raise ValueError("q must be [B, Hq, 1, D] or [B, Hq, D]")
     device = _same_device(q, (k_pool, v_pool, block_table, ctx_len, k_new, v_new, err_word, y))
@@ -614,24 +625,30 @@ def _paged_fp8_decode(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, 
             raise ValueError(f"{n} must be [B, Hkv, D] of q's dtype")
     if y is not None and (_dev(y, "y").dtype != q.dtype or y.shape != shape):
         raise ValueError("y must be shaped and typed like q")
+    page_tokens, dtype = _fp8_page_tokens(k_pool, v_pool, D), _dt(q)
     with _launching(device, stream) as s:
         if y is None:
             y = torch.empty_like(q)
-        p = _paged_params(q, k_pool, v_pool, block_table, ctx_len, y, k_new, v_new, scale,
-                          err_word, options)
+
+        def params(ws, nbytes):
+            return _PAGED.pack(
+                q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _addr(k_new), _addr(v_new),
+                block_table.data_ptr(), ctx_len.data_ptr(), y.data_ptr(), dtype, options, B,
+                shape[1], Hkv, D, page_tokens, block_table.shape[1], pool[0], scale,
+                FP8_E4M3_PAGE, _addr(err_word), ws, nbytes)
+
         if workspace is None:
             # the kept scratch is nearly always large enough: ask only when it is not
             ws = _kept_workspace(device, s)
             if ws is not None:
-                p.workspace, p.workspace_bytes = ws.data_ptr(), ws.numel()
-                rc = L.paged_attn_decode(C.byref(p), s)
+                rc = L.paged_attn_decode(params(ws.data_ptr(), ws.numel()), s)
                 if rc != ERR_WORKSPACE:
                     _check("paged_attn_decode", rc)
                     return y
+        p = PagedParams.from_buffer_copy(params(0, 0))
         ws, nb = _stream_workspace(int(L.paged_attn_decode_workspace(C.byref(p))), device, s,
                                    workspace)
-        p.workspace, p.workspace_bytes = _ptr(ws), nb
-        _check("paged_attn_decode", L.paged_attn_decode(C.byref(p), s))
+        _check("paged_attn_decode", L.paged_attn_decode(params(_addr(ws), nb), s))
     return y
 
 
@@ -1059,22 +1076,19 @@ def rotary_embed(q, k, positions, rope, *, q_out=None, k_out=None, stream=None):
         table = _rope_arg(rope)
         if S * B * Hq * D == 0:
             return q_out, k_out
-
-        def strides(st):  # batch, token, head
-            return (0, st[0], st[1]) if dims == 3 else (st[0], st[2], st[1])
-
-        none = (0, 0, 0)
-        p = RotaryParams(
-            q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), positions.data_ptr(), table,
-            dtype, int(i64), B, S, Hq, Hk, D, S if len(ps) == 2 else 0, strides(qst),
-            strides(kst) if Hk else none, strides(q_out.stride()),
-            strides(k_out.stride()) if Hk else none)
-        _check("rotary_embed", L.rotary_embed(C.byref(p), s))
+        token, head = (0, 1) if dims == 3 else (2, 1)
+        strides = []
+        for st in (qst, kst, q_out.stride(), k_out.stride() if Hk else None):
+            strides += (0, 0, 0) if st is None else (st[0] if dims == 4 else 0, st[token], st[head])
+        p = _ROTARY.pack(
+            q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out), positions.data_ptr(), table,
+            dtype, i64, B, S, Hq, Hk, D, S if len(ps) == 2 else 0, *strides)
+        _check("rotary_embed", L.rotary_embed(p, s))
     return q_out, k_out
 
 
 def _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, rope, err_word):
-    """(parameters, device) of a page write or read-back."""
+    """(packed parameters, device) of a page write or read-back; None for no rows."""
     shape, kst = _rows(k, "k")
     vshape, vst = _rows(v, "v", k.dtype)
     if vshape != shape:
@@ -1101,10 +1115,16 @@ def _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, rope
         fmt, page_tokens = 0, pool[2]
     if pool[1] != Hkv:
         raise ValueError("the pools and the rows have different head counts")
-    return KvPagesParams(
+    if seq_start is None and T != B:
+        raise ValueError("without seq_start every sequence has one row")
+    dtype, table = _dt(k), _rope_arg(rope)
+    if T * Hkv * D == 0:
+        return None, device
+    return _KV_PAGES.pack(
         k.data_ptr(), v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
-        ctx_len.data_ptr(), _ptr(seq_start), _rope_arg(rope), _ptr(err_word), _dt(k), fmt, T, B,
-        Hkv, D, page_tokens, block_table.shape[1], pool[0], kst[:2], vst[:2]), device
+        ctx_len.data_ptr(), _addr(seq_start), table or 0, _addr(err_word), dtype, fmt, T, B,
+        Hkv, D, page_tokens, block_table.shape[1], pool[0], kst[0], kst[1], vst[0],
+        vst[1]), device
 
 
 def paged_kv_write(k, v, k_pool, v_pool, block_table, ctx_len, seq_start=None, *, rope=None,
@@ -1118,12 +1138,10 @@ def paged_kv_write(k, v, k_pool, v_pool, block_table, ctx_len, seq_start=None, *
     L = load()
     p, device = _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, rope,
                                  err_word)
-    if seq_start is None and p.T != p.B:
-        raise ValueError("without seq_start every sequence has one row")
-    if p.T * p.Hkv * p.D == 0:
+    if p is None:
         return
     with _launching(device, stream) as s:
-        _check("paged_kv_write", L.paged_kv_write(C.byref(p), s))
+        _check("paged_kv_write", L.paged_kv_write(p, s))
 
 
 def paged_kv_read(k_pool, v_pool, block_table, ctx_len, seq_start, k=None, v=None, *, total=None,
@@ -1147,9 +1165,8 @@ def paged_kv_read(k_pool, v_pool, block_table, ctx_len, seq_start, k=None, v=Non
             raise ValueError("seq_start is required")
         p, _ = _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, None,
                                 err_word)
-        if p.T * p.Hkv * p.D == 0:
-            return k, v
-        _check("paged_kv_read", L.paged_kv_read(C.byref(p), s))
+        if p is not None:
+            _check("paged_kv_read", L.paged_kv_read(p, s))
     return k, v
 
 
@@ -1187,9 +1204,10 @@ def attn_prefill_packed(q, k, v, q_start, k_start=None, *, causal=True, scale=0.
         if Tk == 0:  # no keys anywhere: an empty tensor has no address to give
             k = v = torch.empty((1, Hkv, D), dtype=q.dtype, device=device)
             kst = vst = k.stride()
-        p = PackedParams(
+        yst = y.stride()
+        p = _PACKED.pack(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), q_start.data_ptr(),
-            _ptr(k_start), _ptr(err_word), _dt(q), int(bool(causal)), B, Tq, Tk, Hq, Hkv, D,
-            qst[:2], kst[:2], vst[:2], y.stride()[:2], float(scale), float(softcap))
-        _check("attn_prefill_packed", L.attn_prefill_packed(C.byref(p), s))
+            _addr(k_start), _addr(err_word), _dt(q), bool(causal), B, Tq, Tk, Hq, Hkv, D,
+            qst[0], qst[1], kst[0], kst[1], vst[0], vst[1], yst[0], yst[1], scale, softcap)
+        _check("attn_prefill_packed", L.attn_prefill_packed(p, s))
     return y

@@ -157,3 +157,17 @@ def test_packed_prefill_refusals(host_lib, change, status):  # noqa: F811
 
 def test_packed_prefill_without_queries_launches_nothing(host_lib):  # noqa: F811
     assert host_lib.attn_prefill_packed(C.byref(_set(_packed(), Tq=0)), None) == 0
+
+
+@pytest.mark.parametrize("packed,py", [(sa._ROTARY, sa.RotaryParams), (sa._KV_PAGES, sa.KvPagesParams),
+                                       (sa._PACKED, sa.PackedParams), (sa._PAGED, sa.PagedParams)])
+def test_packed_parameters_are_the_structures(packed, py):
+    """Field for field: every value packed comes out of the structure's field."""
+    def flat(p):
+        for name, _ in py._fields_:
+            x = getattr(p, name)
+            yield from x if isinstance(x, C.Array) else (x,)
+
+    values = list(range(1, 1 + len(list(flat(py())))))
+    p = py.from_buffer_copy(packed.pack(*values))
+    assert packed.size == C.sizeof(py) and list(flat(p)) == values
