@@ -36,15 +36,16 @@
 //    (With a partial per warp the merge of a 131,072-token context, 282 partials
 //    per unit, took longer than the attention.)
 //  * Where a warp goes from one unit to the next, the unit follows by a step (no
-//    search), and its queries were prefetched when its first tile was issued: short
-//    contexts, many units per warp, are bound by these changes.
+//    search), and its queries were prefetched when its first tile was issued; the
+//    partition counts the change as two tiles (unit_place): short contexts, many
+//    units per warp, are bound by these changes.
 //
 // Measured (8 KV heads of 128, pages of 16 or 32; 6.80 TB/s copy): 128 sequences of
-// 1,024 to 32,768 tokens, 4.5 GB, 727 us, 90% of the copy bandwidth; one context of
-// 131,072 among 23 of some hundred, 290 MB, 79 us (54%; about 20 us are launch, tile
-// space, the rings' first fill and the merges, the rest the short contexts' changes
-// of unit on ten CTAs); one sequence of 1,500, 16.4 us, latency.  Twelve warps per CTA
-// with three stages: sixteen with two 800 us and 85 us, ten with four 848 and 95.
+// 1,024 to 32,768 tokens, 4.5 GB, 717 us, 92% of the copy bandwidth; one context of
+// 131,072 among 23 of some hundred, 290 MB, 68 us (63%; about 20 us are launch, tile
+// space, the rings' first fill and the merges); one sequence of 1,500, 16.4 us,
+// latency.  Twelve warps per CTA with three stages; with the earlier partition (727
+// and 90 us) sixteen with two took 800 and 85 us, ten with four 848 and 95.
 #include "gather_common.cuh"
 #include "serving.h"
 #include "tc05.cuh"
