@@ -17,7 +17,7 @@
 //    softmax, PV, buffer free) takes about four times as long as its MMAs: three
 //    tiles on the way at once, two of them in softmax, keep the tensor cores
 //    about half busy.  Measured, 4 x 4,096 tokens, 32 / 8 heads of 128, causal,
-//    bf16: 453 us, 1,214 TFLOP/s (softcap 50: 478 us).  Other orders tried, at
+//    bf16: 434 us, 1,266 TFLOP/s (softcap 50: 460 us).  Other orders tried, at
 //    463 us for this one: two row tiles per item that share K and V, a score
 //    buffer and a warpgroup each, 500 us; the same with two MMA lanes that
 //    interleave, so that both tiles' softmax runs at the same time, 625 us; with
@@ -28,7 +28,9 @@
 //    offset is fixed, below), in a loop over chunks of 32 columns.  Kept in registers they spill, and local memory
 //    shares its path with the MMAs' shared-memory operands; unrolled, the
 //    roles' loops no longer fit the instruction cache together (both measured:
-//    575 us).
+//    575 us).  The first pass's maximum comes with the load (tcgen05.ld.red;
+//    453 -> 434 us), one chunk at a time: with two on their way the plain
+//    variant spills (520 us).
 //  * The two threads of a row agree on its offset tile by tile: a thread posts
 //    the offset after its tile (the old one unless the tile's maximum exceeds it
 //    by more than 2^8), the other one's next tile starts from it.  The raise
@@ -506,6 +508,25 @@ __device__ __forceinline__ uint64_t poly_logit2(uint64_t x, const float (&tq)[N]
   return f2_fma(x, q, add);
 }
 
+// 32 columns of a thread's row and the largest of them (kAbs: of their magnitudes),
+// found by the load itself.  Valid after tmem_ld_wait, m through arrived().
+template <bool kAbs>
+__device__ __forceinline__ void tmem_ld32_max(uint32_t addr, uint32_t (&r)[32], float& m) {
+#define SA_LD32_MAX(op)                                                                         \
+  asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32." op                                      \
+               ".f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20," \
+               "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"                       \
+               : SA_TC05_R32(r), "=f"(m)                                                         \
+               : "r"(addr))
+  if (kAbs) SA_LD32_MAX("max.abs");
+  else SA_LD32_MAX("max");
+#undef SA_LD32_MAX
+}
+__device__ __forceinline__ float arrived(float& m) {
+  asm volatile("" : "+f"(m));
+  return m;
+}
+
 // The largest magnitude of 32 scores.
 __device__ __forceinline__ float largest(const uint32_t (&r)[32]) {
   float ax[2] = {0.f, 0.f};
@@ -608,7 +629,8 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       if (!wait_or_abort_warp(&bars[G::kBarS + buf], (u / kSBufs) & 1, abort_flag, p.err_word)) return;
       tc05::fence_after_sync();
       uint32_t r[2][32];
-      tc05::tmem_ld32(tS, r[0]);
+      float mr[2];
+      tmem_ld32_max<kFixed>(tS + (kFixed ? 0 : 96), r[0], mr[0]);  // (the first pass goes backwards)
       const int tok = it.tok + rt;
       const int lim = rt < p.tpt && tok < it.nq ? last_key(p.causal, it.nq, it.nk, tok) : -1;  // last visible key
       const int rel = lim - j * kTile;  // columns above rel are masked
@@ -631,20 +653,28 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       };
       int mode = kPlain;
       float mx = SA_NEG_INF;
-      if (!kFixed) {
+      if (!kCap && !masked) {  // the loads find the maximum
+        tc05::tmem_ld_wait();
+        mx = arrived(mr[0]);
+#pragma unroll 1
+        for (int c = 2; c >= 0; --c) {
+          tmem_ld32_max<false>(tS + 32 * c, r[0], mr[0]);
+          tc05::tmem_ld_wait();
+          mx = fmaxf(mx, arrived(mr[0]));
+        }
+      } else if (!kFixed) {
         float ax = 0.f;
         auto look = [&](uint32_t (&x)[32], int c) {
           if (kCap) ax = fmaxf(ax, largest(x));
           mx = masked ? max_chunk<true>(x, rel - 32 * c, mx) : max_chunk<false>(x, 0, mx);
         };
+        tc05::tmem_ld_wait();
 #pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {  // the next chunk (at last the first again) is on its way meanwhile
-          tc05::tmem_ld_wait();
-          tc05::tmem_ld32(tS + 32 * (c + 1), r[1]);
+        for (int c = 3;; --c) {
           look(r[0], c);
+          if (c == 0) break;
+          tc05::tmem_ld32(tS + 32 * (c - 1), r[0]);
           tc05::tmem_ld_wait();
-          tc05::tmem_ld32(tS + 32 * ((c + 2) & 3), r[0]);
-          look(r[1], c + 1);
         }
         if (kCap) mode = mode_of(ax);
       }
@@ -678,10 +708,14 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
         }
       }
       const float neg_m = (kFixed || m == SA_NEG_INF) ? 0.0f : -m;
-      auto exps = [&](uint32_t (&x)[32], int c) {
+      auto load = [](uint32_t at, uint32_t (&x)[32], float& most) {
+        if (kFixed) tmem_ld32_max<true>(at, x, most);
+        else tc05::tmem_ld32(at, x);
+      };
+      auto exps = [&](uint32_t (&x)[32], int c, float& most) {
         const int rc = rel - 32 * c;
         uint32_t pk[16];
-        if (kFixed) mode = mode_of(largest(x));
+        if (kFixed) mode = mode_of(arrived(most));
         if (!kCap && masked) exp_chunk<kPlain, true, T>(x, pk, lg, neg_m, rc, ls);
         else if (!kCap) exp_chunk<kPlain, false, T>(x, pk, lg, neg_m, 0, ls);
         else if (mode == kFar) exp_chunk<kFar, true, T>(x, pk, lg, neg_m, masked ? rc : kTile, ls);
@@ -693,11 +727,11 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
 #pragma unroll 1
       for (int c = 0; c < 4; c += 2) {
         tc05::tmem_ld_wait();
-        tc05::tmem_ld32(tS + 32 * (c + 1), r[1]);
-        exps(r[0], c);
+        load(tS + 32 * (c + 1), r[1], mr[1]);
+        exps(r[0], c, mr[0]);
         tc05::tmem_ld_wait();
-        if (c == 0) tc05::tmem_ld32(tS + 64, r[0]);
-        exps(r[1], c + 1);
+        if (c == 0) load(tS + 64, r[0], mr[0]);
+        exps(r[1], c + 1, mr[1]);
         // half of P is there: its PV need not wait for the other half
         tc05::tmem_st_wait();
         tc05::fence_before_sync();
