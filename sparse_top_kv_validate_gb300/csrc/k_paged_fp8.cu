@@ -43,7 +43,7 @@
 // Measured (8 KV heads of 128, pages of 16 or 32; 6.80 TB/s copy): 128 sequences of
 // 1,024 to 32,768 tokens, 4.5 GB, 717 us, 92% of the copy bandwidth; one context of
 // 131,072 among 23 of some hundred, 290 MB, 68 us (63%; about 20 us are launch, tile
-// space, the rings' first fill and the merges); one sequence of 1,500, 16.4 us,
+// space, the rings' first fill and the merges); one sequence of 1,500, 15.3 us,
 // latency.  Twelve warps per CTA with three stages; with the earlier partition (727
 // and 90 us) sixteen with two took 800 and 85 us, ten with four 848 and 95.
 #include "gather_common.cuh"
@@ -55,6 +55,7 @@ namespace sa {
 namespace {
 
 constexpr float kRaiseLog2 = 8.0f;
+constexpr int kMinWarps = 8;  // per CTA, where there are few tiles
 constexpr float kWeightMax = 4096.0f;  // of a value weight before its head's E is raised
 
 template <int D, int NT>
@@ -218,23 +219,29 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
   const int32_t total = unit_place(a, pref[a.B], static_cast<int32_t>(a.B), 0, 0);
   const int64_t gw_total = static_cast<int64_t>(gridDim.x) * NW;
   int64_t R = (total + gw_total - 1) / gw_total;
-  if (R < min_range) R = min_range;
+  int nw = NW;  // warps that get a range
+  if (R < min_range) {
+    // few tiles: more CTAs with fewer warps each (one context of 1,500: 15.3 us, with
+    // all twelve 16.5, with four 15.8)
+    R = min_range;
+    nw = static_cast<int>(min(static_cast<int64_t>(NW), max((total + gridDim.x * R - 1) / (gridDim.x * R), int64_t(kMinWarps))));
+  }
   if (blockIdx.x == 0) {
     // the combine kernel sees the CTAs as its "warps"
     for (int64_t b = threadIdx.x; b <= a.B; b += blockDim.x) a.pref_out[b] = pref[b];
-    if (threadIdx.x == 0) a.meta[0] = R * NW;
+    if (threadIdx.x == 0) a.meta[0] = R * nw;
     // sequences without tiles still need a (zero) output
     for (int b = warp; b < a.B; b += NW)
       if (pref[b + 1] == pref[b])
         for (int64_t e = lane; e < a.Hq * D / 2; e += 32)
           reinterpret_cast<uint32_t*>(a.y)[b * (a.Hq * D / 2) + e] = 0u;
   }
-  const int64_t c_first = static_cast<int64_t>(blockIdx.x) * NW * R;
+  const int64_t c_first = static_cast<int64_t>(blockIdx.x) * nw * R;
   if (c_first >= total) return;  // the whole CTA
-  const int32_t c_place = static_cast<int32_t>(c_first), c_end = c_place + NW * static_cast<int32_t>(R);
+  const int32_t c_place = static_cast<int32_t>(c_first), c_end = c_place + nw * static_cast<int32_t>(R);
   int32_t t_begin, t_end;
   {
-    const int32_t t = tiles_before(a, pref, c_place + (warp + (lane & 1)) * static_cast<int32_t>(R));
+    const int32_t t = tiles_before(a, pref, c_place + min(warp + (lane & 1), nw) * static_cast<int32_t>(R));
     t_begin = __shfl_sync(0xffffffffu, t, 0);
     t_end = __shfl_sync(0xffffffffu, t, 1);
   }
