@@ -186,3 +186,22 @@ def test_pages_past_2_31_bytes(cuda_lib, fp8):
     q = torch.randn(1, 32, 1, D, generator=g).bfloat16().to(DEV)
     assert torch.equal(sa.paged_attn_decode(q, *pools, table, ctx, err_word=err), sa.paged_attn_decode(q, *small, near, ctx))
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("B", [32, 33, 300])
+def test_many_sequences_of_very_different_lengths(cuda_lib, B, causal):
+    """Chunks of 0 to 400 tokens after contexts of up to 1,500: the two ways in which the items
+    are put in order."""
+    g = torch.Generator().manual_seed(B)
+    nq = (2.0 ** (8.7 * torch.rand(B, generator=g)) - 1).int().tolist()
+    past = (2.0 ** (10.6 * torch.rand(B, generator=g)) - 1).int().tolist()
+    nk = [a + b for a, b in zip(nq, past)]
+    nk[3] = 0                                              # queries without a key
+    q, k, v, qs, ks = packed.make("f16", nq, nk, 3, 1, 64, seed=B)
+    y = torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cuda_lib.attn_prefill_packed(q.to(DEV), k.to(DEV), v.to(DEV), packed.starts(qs), packed.starts(ks), causal=causal,
+                                 y=y, err_word=err)
+    assert int(err) == 0 and (y[qs[-1]:] == 9.0).all()
+    packed.check(y, q, k, v, qs, ks, causal=causal)
