@@ -17,7 +17,7 @@
 //    softmax, PV, buffer free) takes about four times as long as its MMAs: three
 //    tiles on the way at once, two of them in softmax, keep the tensor cores
 //    about half busy.  Measured, 4 x 4,096 tokens, 32 / 8 heads of 128, causal,
-//    bf16: 434 us, 1,266 TFLOP/s (softcap 50: 460 us).  Other orders tried, at
+//    bf16: 425 us, 1,295 TFLOP/s (softcap 50: 460 us).  Other orders tried, at
 //    463 us for this one: two row tiles per item that share K and V, a score
 //    buffer and a warpgroup each, 500 us; the same with two MMA lanes that
 //    interleave, so that both tiles' softmax runs at the same time, 625 us; with
@@ -680,6 +680,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
   const uint32_t tS0 = tmem + lanes + G::kColS, tO = tmem + lanes + G::kColO;
   volatile float* xch = reinterpret_cast<volatile float*>(sm + G::kOffXch) + row;
   const int rt = row / p.g;  // token of the tile that this row belongs to
+  const int inv_g = (65536 + p.g - 1) / p.g;
   Logits lg;
   lg.c2 = p.c_log2;
   lg.k1 = p.k1;
@@ -897,14 +898,24 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
     tc05::fence_before_sync();  // these reads precede the next item's first PV
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[G::kBarORead]);
-    T* y = static_cast<T*>(p.y) + e.kvh * p.g * p.ys1 + wg * kOCols + (lane % kPieces) * 8;
+    // four loads before the first store (one by one, 434 -> 425 us at 4 x 4,096 tokens);
+    // one piece of 32 / kPieces rows each
+    T* y = static_cast<T*>(p.y) + (e.q0 + e.tok) * p.ys0 + e.kvh * p.g * p.ys1 + wg * kOCols + (lane % kPieces) * 8;
+    constexpr int kAtOnce = 4;
 #pragma unroll 1
-    for (int i = 0; i < kPieces; ++i) {
-      const int rl = i * (32 / kPieces) + lane / kPieces;  // row of this warp's 32
-      const int rr = (warp & 3) * 32 + rl, r_t = rr / p.g, r_h = rr - r_t * p.g;
-      const uint4 v = stage[rl * kPieces + ((lane % kPieces) ^ (rl & (kPieces - 1)))];
-      if (r_t < p.tpt && e.tok + r_t < e.nq)
-        *reinterpret_cast<uint4*>(y + (e.q0 + e.tok + r_t) * p.ys0 + r_h * p.ys1) = v;
+    for (int i = 0; i < kPieces; i += kAtOnce) {
+      uint4 v[kAtOnce];
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int rl = (i + x) * (32 / kPieces) + lane / kPieces;  // row of this warp's 32
+        v[x] = stage[rl * kPieces + ((lane % kPieces) ^ (rl & (kPieces - 1)))];
+      }
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int rr = (warp & 3) * 32 + (i + x) * (32 / kPieces) + lane / kPieces;
+        const int r_t = (rr * inv_g) >> 16, r_h = rr - r_t * p.g;  // rr / g: exact below 128
+        if (r_t < p.tpt && e.tok + r_t < e.nq) *reinterpret_cast<uint4*>(y + r_t * p.ys0 + r_h * p.ys1) = v[x];
+      }
     }
     fence_proxy_async_smem();  // these reads precede the buffer's next load
     __syncwarp();
