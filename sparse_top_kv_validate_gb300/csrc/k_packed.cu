@@ -34,8 +34,9 @@
 //  * The two threads of a row agree on its offset tile by tile: a thread posts
 //    the offset after its tile (the old one unless the tile's maximum exceeds it
 //    by more than 2^8), the other one's next tile starts from it.  The raise
-//    rescales O in tensor memory, after the previous PV.  With a softcap up to
-//    67 the logits are bounded, the offset is 0 and nothing is posted.
+//    rescales O in tensor memory, after the previous PV.  With a softcap that bounds
+//    2^logit to the normal numbers of P's type (up to 67 in bf16, 9.7 in f16) the
+//    offset is 0 and nothing is posted.
 //  * Warp 0 loads Q (box: 64 dims x g heads x 128 / g tokens; two buffers) and the
 //    K and V tiles through two rings; warp 1's lane issues S = Q K^T and warp 3's
 //    O += P V (P over the first half of its scores), so that a barrier wait or a
@@ -76,7 +77,13 @@ constexpr float kRescaleLog2 = 8.0f;     // lazy-maximum slack (factor 256)
 // absolute error of 1e-7 both
 constexpr int kTanhTerms = 5, kTanhShortTerms = 3;
 constexpr float kTanhBound = 0.625f, kTanhShortBound = 0.25f;
-constexpr float kFixedOffsetMaxLog2 = 97.0f;  // softcap * log2(e) up to which 2^logit needs no offset
+// softcap * log2(e) up to which 2^logit needs no offset: the logits lie within that on
+// either side, and every 2^logit is a normal number of the type that P is held in (the
+// row sums, fp32, hold 2^30 of them).  f16 ends at 2^16 and its normal numbers at 2^-14.
+template <typename T>
+constexpr float fixed_offset_max_log2() {
+  return std::is_same<T, __half>::value ? 14.0f : 97.0f;
+}
 constexpr int kMaxSeqs = 1024;           // sequences per launch
 constexpr int kSmemLimit = 227 * 1024;
 
@@ -1130,7 +1137,7 @@ int launch_t(const PackedArgs& a, cudaStream_t st) {
   if (a.softcap != 0.0f) {
     p.k1 = a.scale / a.softcap;
     p.c_log2 = a.softcap * log2e;
-    variant = p.c_log2 <= kFixedOffsetMaxLog2 ? kVarCapFixed : kVarCapMax;
+    variant = p.c_log2 <= fixed_offset_max_log2<T>() ? kVarCapFixed : kVarCapMax;
     static const TanhFits fits;
     p.tq_bound = score_polynomial(fits.full, kTanhBound, a.softcap, p.k1, p.tq);
     p.ts_bound = score_polynomial(fits.brief, kTanhShortBound, a.softcap, p.k1, p.ts);

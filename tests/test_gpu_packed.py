@@ -190,3 +190,48 @@ def test_refusals(cuda_lib):
     with pytest.raises(sa.SAError):
         x = torch.zeros(10, 2, 258, dtype=torch.float16, device=DEV)
         sa.attn_prefill_packed(x, x, x, s)
+
+
+def leaning(dt, nq, nk, Hq, Hkv, D, lean, seed):
+    """Queries and keys whose scores (scale 1 / sqrt(D)) lie around `lean`, or around both
+    signs of it ("mixed": a sign per key)."""
+    q, k, v, qs, ks = make(dt, nq, nk, Hq, Hkv, D, seed=seed)
+    mean, size = (24.0, 24.0) if lean == "mixed" else (lean, abs(lean))
+    side = math.sqrt(size / math.sqrt(D))
+    sign = torch.where(torch.rand(k.shape[:2], generator=torch.Generator().manual_seed(seed)) < 0.5, -1.0, 1.0)[..., None] \
+        if lean == "mixed" else math.copysign(1.0, mean)
+    return (side + 0.3 * q.float()).to(DT[dt]), (sign * side + 0.3 * k.float()).to(DT[dt]), v, qs, ks
+
+
+def check_tail(y, q, k, v, qs, ks, causal, cap, what, tanh=2.0 ** -20):
+    """check()'s bound (`tanh`: of the softcap's tanh), and for f16 what its subnormal probabilities lose: a probability
+    held against an offset of at most the row's maximum is off by half of 2^-24 at the
+    most, and the row's sum is at least 1."""
+    want, mag, most = orc.prefill_packed(q, k, v, qs, ks, causal, 0.0, cap)
+    y = y.cpu()
+    fi = torch.finfo(y.dtype)
+    D, g = q.shape[2], q.shape[1] // k.shape[1]
+    rel = 2 * (D * 2.0 ** -22 * most + tanh * cap + 2.0 ** -16) + D * 2.0 ** -22 + 2.0 ** -16 + fi.eps / 2
+    lost = torch.zeros_like(want)
+    if y.dtype == torch.float16:
+        for b in range(len(qs) - 1):
+            s = v[ks[b]:ks[b + 1]].double().abs().sum(0) * 2.0 ** -25
+            lost[qs[b]:qs[b + 1]] = s.repeat_interleave(g, 0)[None]
+    own = ~torch.isnan(want)
+    near = rel * mag + lost
+    tol = near + (want.abs() + near) * fi.eps / 2 + fi.smallest_normal * fi.eps
+    assert torch.isfinite(y[own].double()).all(), what
+    off = float(((y.double() - want).abs() - tol)[own].max())
+    assert off <= 0, f"{what}: {off:.3e} over the bound"
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("cap", [9.7, 9.8, 30.0, 50.0, 67.0, 68.0])
+@pytest.mark.parametrize("lean", [24.0, -24.0, 100.0, -100.0, "mixed"])
+def test_scores_that_reach_the_softcap(cuda_lib, dt, cap, lean):
+    """Logits around +-20 and at the cap itself: what 2^logit is without an offset is far
+    outside f16 there, on either side."""
+    for D, Hq, Hkv in ((128, 4, 2), (64, 3, 1)):
+        q, k, v, qs, ks = leaning(dt, [200, 70], [512, 70], Hq, Hkv, D, lean, seed=int(cap))
+        y = cuda_lib.attn_prefill_packed(q.to(DEV), k.to(DEV), v.to(DEV), starts(qs), starts(ks), softcap=cap)
+        check_tail(y, q, k, v, qs, ks, True, cap, f"{dt} cap {cap} lean {lean} D {D}")
