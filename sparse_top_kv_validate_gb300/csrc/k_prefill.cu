@@ -35,9 +35,10 @@
 //    loads its scores, applies scale, softcap and mask, and writes
 //    P = 2^(s - m) as 16-bit pairs over its own score columns; at the end the
 //    groups add their row sums and each normalises and stores half the O
-//    row.  With a softcap the logits are bounded and m is the constant 0
-//    (exact: softmax is shift-invariant, and the bound keeps 2^logit and the
-//    row sums inside fp32's normal range); otherwise m is a running maximum
+//    row.  With a softcap that bounds 2^logit to the normal numbers of P's type
+//    (up to 67 in bf16, 9.7 in f16) m is the constant 0 (exact: softmax is
+//    shift-invariant, and the row sums stay inside fp32's normal range);
+//    otherwise m is a running maximum
 //    shared by the groups and raised only when a tile's maximum exceeds it by
 //    more than 2^8, O then rescaled in TMEM after the previous PV completed.
 //  * The softcap's tanh runs on the FMA pipes as a fitted odd polynomial
@@ -76,9 +77,13 @@ constexpr int kLead = kSBufs - 1;        // S(j + kLead) is issued before PV(j)
 constexpr int kTanhTerms = 5;            // tanh(x) ~= x * sum_k c_k (x^2)^k
 constexpr float kTanhPolyBound = 0.625f; // |x| range of the fit (abs error ~1e-7)
 // Largest softcap * log2(e) for which 2^(logit) needs no offset: logits in
-// [-97, 97] keep every probability a normal fp32 number and row sums over up
-// to 2^30 keys below 2^127.
-constexpr float kFixedOffsetMaxLog2 = 97.0f;
+// [-97, 97] keep every probability a normal number of fp32 and of bf16 and row
+// sums over up to 2^30 keys below 2^127; in f16, whose normal numbers are 2^-14
+// to 2^16, logits in [-14, 14] do.
+template <typename T>
+constexpr float fixed_offset_max_log2() {
+  return std::is_same<T, __half>::value ? 14.0f : 97.0f;
+}
 
 template <int D>
 struct PGeo {
@@ -543,11 +548,10 @@ __device__ __forceinline__ uint64_t exp_pass(const uint32_t (&r)[kGroupKeys], ui
 }
 
 // Score variants: no softcap; softcap with a running maximum; softcap with the
-// constant offset 0.  With |softcap| * log2(e) <= kFixedOffsetMaxLog2 every
-// log2-domain logit lies within +-97, so 2^logit neither overflows nor
-// underflows fp32, nor does a row sum over up to 2^30 keys: the shift-
-// invariant softmax then needs no maximum at all (no cross-group exchange,
-// no O rescale).
+// constant offset 0.  With |softcap| * log2(e) <= fixed_offset_max_log2 every
+// 2^logit is a normal number of the type that P is held in, and a row sum over
+// up to 2^30 keys one of fp32: the shift-invariant softmax then needs no maximum
+// at all (no cross-group exchange, no O rescale).
 enum ScoreVariant { kVarPlain = 0, kVarSoftcapMax = 1, kVarSoftcapFixed = 2 };
 
 template <int D, typename T, int kVariant>
@@ -914,7 +918,7 @@ static int launch_prefill_t(const PrefillTcArgs& a, cudaStream_t st) {
     const float cap = std::fabs(a.softcap);
     p.k1 = a.scale / cap;
     p.c_log2 = cap * log2e;
-    p.softcap_on = p.c_log2 <= kFixedOffsetMaxLog2 ? 2 : 1;
+    p.softcap_on = p.c_log2 <= fixed_offset_max_log2<T>() ? 2 : 1;
     const double* c = tanh_poly();
     for (int k = 0; k < kTanhTerms; ++k)
       p.tq[k] = static_cast<float>(c[k] * static_cast<double>(cap) * 1.4426950408889634);

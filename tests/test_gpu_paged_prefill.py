@@ -199,3 +199,20 @@ def test_full_size_prefill_sampled_rows(cuda_lib):
                          rows=rows)
     got = y.reshape(-1, c.D)[torch.tensor(rows, device=DEV)]
     assert_close(to64(got), ref, y.dtype, "prefill sampled")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("cap", [9.7, 9.8, 30.0, 50.0, 67.0, 68.0])
+@pytest.mark.parametrize("lean", [24.0, -24.0, 100.0, -100.0, "mixed"])
+def test_scores_that_reach_the_softcap(cuda_lib, dt, cap, lean):
+    """Logits around +-20 and at the cap itself: what 2^logit is without an offset is far
+    outside f16 there, on either side.  Bound: test_gpu_packed.check_tail's, whose steps
+    (fp32 scores, tanh, exp2, a 16-bit probability, fp32 sums) are this kernel's too but
+    for the tanh, off by 2^-10.9 of the softcap where the hardware's serves."""
+    from test_gpu_packed import check_tail, leaning
+    for D, Hq, Hkv in ((128, 4, 2), (64, 3, 1)):
+        q, k, v, qs, ks = leaning(dt, [300], [300], Hq, Hkv, D, lean, seed=int(cap))
+        d = [t[:300].transpose(0, 1)[None].contiguous().to(DEV) for t in (q, k, v)]
+        y = cuda_lib.attn_prefill(*d, causal=True, softcap=cap)
+        y = y.reshape(Hq, 300, D).transpose(0, 1)
+        check_tail(y, q[:300], k[:300], v[:300], qs, ks, True, cap, f"{dt} cap {cap} lean {lean} D {D}", tanh=2.0 ** -10.9)
