@@ -24,11 +24,14 @@
 //    element 2^-39 below the row's largest is rounded).  The key's scale and
 //    the head's power of two multiply the fp32 score.
 //  * V: the codes become f16 the same way (exact).  The value's scale is folded
-//    into the probability: w = p 2^(ev - E), E a power of two per head that is
-//    raised when w passes 2^12 (O then follows, exactly), so that f16 holds every
-//    weight to 2^-25 of about the largest; it is split into two f16 (hi + lo, 22
-//    bits), so that its rounding stays far below the output's.  (V as bf16, whose
-//    range needs no E, costs 96 more integer instructions of 620 per tile.)
+//    into the probability: w = p 2^(ev - E), E a power of two per head.  It is raised
+//    when w passes 2^15, to put the tile's largest weight into [2^6, 2^7), and lowered
+//    by d when the running maximum rises by d (rounded up), as everything that set it
+//    has then shrunk by 2^-d; O follows both.  So the largest weight that still
+//    counts is held as 2^6 or more, and f16 holds every weight to 2^-31 of it (half its
+//    smallest step of 2^-24); w is split into two f16 (hi + lo, 22 bits), so that its
+//    rounding stays far below the output's.  (V as bf16, whose range needs no E, costs
+//    96 more integer instructions of 620 per tile.)
 //  * The running maximum is raised only when a score exceeds it by 2^8 (one
 //    vote per tile instead of a reduction and a rescale).
 //  * A unit split across warps is merged in shared memory by its CTA; only one
@@ -56,7 +59,11 @@ namespace {
 
 constexpr float kRaiseLog2 = 8.0f;
 constexpr int kMinWarps = 8;  // per CTA, where there are few tiles
-constexpr float kWeightMax = 4096.0f;  // of a value weight before its head's E is raised
+// Of a held value weight: the largest before its head's E is raised (f16 ends at 2^16),
+// and the exponent that the tile's largest then gets.
+constexpr float kWeightMax = 32768.0f;
+constexpr uint32_t kWeightExp = 6;
+constexpr uint32_t kDownExpMax = 252;  // biased exponent of 2^-E: its inverse is a normal number too
 
 template <int D, int NT>
 struct FGeo {
@@ -542,7 +549,7 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
       if (__any_sync(0xffffffffu, raise) && have) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float al[2];
+          float al[2];  // of O
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // a row of nothing but NaN scores still gets a finite maximum, so that its
@@ -553,12 +560,17 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, sh));
             const float mn = fmaxf(m_run[nt][j], tm + mu);
-            al[j] = mn == SA_NEG_INF ? 1.f : ex2(m_run[nt][j] - mn);
+            const float fall = mn == SA_NEG_INF ? 0.f : m_run[nt][j] - mn;  // (-inf: no maximum before)
+            // E falls with the weights that set it
+            const uint32_t dn = __float_as_uint(down_v[nt][j]);
+            const uint32_t by = dn == 0u ? 0u : min(static_cast<uint32_t>(ceilf(fminf(-fall, 256.f))), kDownExpMax - (dn >> 23));
+            down_v[nt][j] = __uint_as_float(dn + (by << 23));
+            al[j] = ex2(fall + static_cast<float>(by));
             const float d = mn == SA_NEG_INF ? 0.f : mu - mn;
             s[nt][j] += d;
             s[nt][2 + j] += d;
             m_run[nt][j] = mn;
-            l_run[nt][j] *= al[j];
+            l_run[nt][j] *= ex2(fall);
           }
 #pragma unroll
           for (int mt = 0; mt < G::kKs; ++mt) {
@@ -593,12 +605,11 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
             float w = fmaxf(wt[nt][j], wt[nt][2 + j]);
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, sh));
-            // 2^-E with E the exponent of the largest weight, never lowered; weights
-            // of nothing (all zero, or infinite) leave it
+            // 2^-E, raised only here; weights of nothing (all zero, or infinite) leave it
             const uint32_t ex = __float_as_uint(w) >> 23;
             float down = down_v[nt][j];
-            if (ex >= 1 && ex <= 252) {
-              const float want = __uint_as_float((254u - ex) << 23);
+            if (w > 0.f && ex < 255) {
+              const float want = __uint_as_float(min(254u + kWeightExp - ex, kDownExpMax) << 23);
               if (down == 0.f || want < down) down = want;
             }
             al[j] = down_v[nt][j] == 0.f ? 1.f : down * (1.0f / down_v[nt][j]);

@@ -259,3 +259,62 @@ def test_refusals(cuda_lib):
         sa.paged_attn_decode(q, *pools, table, ctx_t, k_new=kn)
     with pytest.raises(sa.SAError):
         sa.paged_attn_decode(q, pools[0], pools[0], table, ctx_t)
+
+
+def bound_check(y, q, k, v, weight, scale, what):
+    """One sequence's heads of one KV head against 64 bits.  Besides check()'s steps a value
+    weight p 2^ev is held to 2^-25 of a unit in which the largest weight that counts (after
+    the maximum's rises) is at least 2^6: 2^-31 of the largest, per token, times its code."""
+    want, mag, most = orc.attend(q, k, v, scale)
+    fi = torch.finfo(y.dtype)
+    rel = 2 * (q.shape[-1] * 2.0 ** -22 * most + 2.0 ** -14) + 2.0 ** -16 + 2.0 ** -18
+    p = torch.softmax(q.double() @ k.T * scale, -1)
+    near = rel * mag + 2.0 ** -31 * (p * weight).amax(-1, keepdim=True) * (v / weight[:, None]).abs().sum(0)
+    tol = near + (want.abs() + near) * fi.eps / 2 + fi.smallest_normal * fi.eps
+    got = y.double().cpu()
+    assert torch.isfinite(got).all(), what
+    off = float(((got - want).abs() - tol).max())
+    assert off <= 0, f"{what}: {off:.3e} over the bound, largest output {float(want.abs().max()):.3e}"
+
+
+def shared_context(n, pt, Hkv, D, k, v, B):
+    """FP8 pools with the rows k, v [n, Hkv, D] (quantised) as one context, and a table in
+    which B sequences share its pages, so that a warp's range holds many tiles."""
+    lay = Layout([n], [n], pt)
+    pools, vals, weight = [], [], None
+    for x in (k, v):
+        codes, scales = orc.quantise_rows(x.reshape(-1, D))
+        codes, scales = codes.view(n, Hkv, D), scales.view(n, Hkv)
+        p = torch.zeros(lay.pages, Hkv, pt * (D + 1), dtype=torch.uint8)
+        for i in range(n):
+            page, slot = lay.place(0, i)
+            for h in range(Hkv):
+                orc.write_row(p, page, h, slot, pt, D, codes[i, h], scales[i, h])
+        pools.append(p.to(DEV))
+        vals.append(orc.dequantise_rows(codes, scales))
+        weight = 2.0 ** (scales.double() - 127)
+    table = lay.table.expand(B, -1).contiguous().to(DEV)
+    return pools, table, torch.full((B,), n, dtype=torch.int32, device=DEV), vals, weight
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("drop,rise,how", [(16, 30, "step"), (20, 30, "step"), (26, 60, "step"), (30, 90, "step"),
+                                           (16, 30, "ramp"), (24, 40, "ramp"), (30, 60, "ramp"), (28, 200, "ramp")])
+def test_value_scales_fall_while_the_scores_rise(cuda_lib, dt, drop, rise, how):
+    """Rows of large values that the running maximum soon scales away: the later rows'
+    weights count in full."""
+    n, Hkv, g, D, B = 192, 4, 4, 128, 240
+    gen = torch.Generator().manual_seed(drop)
+    q = (torch.rand(B, Hkv * g, 1, D, generator=gen) + 0.5).to(DT[dt])
+    t = torch.arange(n).double() / (n - 1)
+    t = (t > 0.2).double() if how == "step" else t
+    scale = 1 / math.sqrt(D)
+    up = rise * math.log(2) / (D * scale)                  # mean q is 1: `rise` log2 units of score
+    k = 0.05 * torch.randn(n, Hkv, D, generator=gen).double() + (t * up)[:, None, None]
+    v = torch.randn(n, Hkv, D, generator=gen).double() * torch.exp2(drop * (0.3 - t).round(decimals=3))[:, None, None]
+    pools, table, ctx, vals, weight = shared_context(n, 16, Hkv, D, k, v, B)
+    y = cuda_lib.paged_attn_decode(q.to(DEV), *pools, table, ctx)
+    for b in (0, 1, 7, 100, 101, 102, 103, 239):
+        for h in range(Hkv):
+            bound_check(y[b, h * g:(h + 1) * g, 0], q[b, h * g:(h + 1) * g, 0].double(), vals[0][:, h], vals[1][:, h],
+                        weight[:, h], scale, f"{dt} drop {drop} rise {rise} {how}: {b} {h}")
