@@ -28,10 +28,10 @@
 //    when w passes 2^15, to put the tile's largest weight into [2^6, 2^7), and lowered
 //    by d when the running maximum rises by d (rounded up), as everything that set it
 //    has then shrunk by 2^-d; O follows both.  So the largest weight that still
-//    counts is held as 2^6 or more, and f16 holds every weight to 2^-31 of it (half its
-//    smallest step of 2^-24); w is split into two f16 (hi + lo, 22 bits), so that its
-//    rounding stays far below the output's.  (V as bf16, whose range needs no E, costs
-//    96 more integer instructions of 620 per tile.)
+//    counts (rows of zeros do not) is held as 2^6 or more, and f16 holds every weight
+//    to 2^-31 of it (half its smallest step of 2^-24); w is split into two f16 (hi + lo,
+//    22 bits), so that its rounding stays far below the output's.  (V as bf16, whose
+//    range needs no E, costs 96 more integer instructions of 620 per tile.)
 //  * The running maximum is raised only when a score exceeds it by 2^8 (one
 //    vote per tile instead of a reduction and a rescale).
 //  * A unit split across warps is merged in shared memory by its CTA; only one
@@ -597,9 +597,24 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
       }
       if (__any_sync(0xffffffffu, raise) && have) {
         fresh = false;
+        // A row whose codes are all zero says nothing about the others, whatever its scale
+        // (1 where paged_kv_write stored it): it has no weight here, but for a NaN scale.
+        uint32_t some[4];  // per token of vx: the lanes that hold a code other than zero
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t any = 0;
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) any |= vx[i][w];
+          some[i] = __ballot_sync(0xffffffffu, (any & 0x7f7f7f7fu) != 0u);
+        }
+        const uint32_t quad = 0x11111111u << (gid >> 1);  // the lanes with token gid, and gid + 8
+        const bool none0 = vb0 != 255u && !((gid & 1 ? some[1] : some[0]) & quad);
+        const bool none1 = vb1 != 255u && !((gid & 1 ? some[3] : some[2]) & quad);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float al[2];
+          if (none0) wt[nt][0] = wt[nt][1] = 0.f;
+          if (none1) wt[nt][2] = wt[nt][3] = 0.f;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float w = fmaxf(wt[nt][j], wt[nt][2 + j]);

@@ -318,3 +318,38 @@ def test_value_scales_fall_while_the_scores_rise(cuda_lib, dt, drop, rise, how):
         for h in range(Hkv):
             bound_check(y[b, h * g:(h + 1) * g, 0], q[b, h * g:(h + 1) * g, 0].double(), vals[0][:, h], vals[1][:, h],
                         weight[:, h], scale, f"{dt} drop {drop} rise {rise} {how}: {b} {h}")
+
+
+@pytest.mark.parametrize("dt,size", [("bf16", 2.0 ** -6), ("f16", 2.0 ** -6), ("bf16", 2.0 ** -26), ("bf16", 2.0 ** -60)])
+@pytest.mark.parametrize("where", [(0,), (5, 700), (1990,), tuple(range(0, 2000, 3))])
+def test_value_rows_of_zeros_say_nothing_about_the_others(cuda_lib, dt, size, where):
+    """A row of zeros is stored with a scale of 1, whatever the size of the rows around it;
+    here the zero rows have nearly all of the probability."""
+    n, Hkv, g, D, B = 2000, 2, 4, 64, 200
+    gen = torch.Generator().manual_seed(len(where))
+    q = (torch.rand(B, Hkv * g, 1, D, generator=gen) + 0.5).to(DT[dt])
+    k = 0.05 * torch.randn(n, Hkv, D, generator=gen).double()
+    v = size * torch.randn(n, Hkv, D, generator=gen).double()
+    k[list(where)] += 16 * math.log(2) / math.sqrt(D)      # 2^16 times the others' probability
+    v[list(where)] = 0
+    pools, table, ctx, vals, weight = shared_context(n, 16, Hkv, D, k, v, B)
+    weight[list(where)] = weight.min()                     # (they hold nothing)
+    y = cuda_lib.paged_attn_decode(q.to(DEV), *pools, table, ctx)
+    for b in (0, 1, 66, 199):
+        for h in range(Hkv):
+            bound_check(y[b, h * g:(h + 1) * g, 0], q[b, h * g:(h + 1) * g, 0].double(), vals[0][:, h], vals[1][:, h],
+                        weight[:, h], 1 / math.sqrt(D), f"{dt} {size} {where[:3]}: {b} {h}")
+
+
+def test_a_nan_row_of_zero_codes_is_still_nan(cuda_lib):
+    """What paged_kv_write stores for a row with a NaN: codes 0, scale byte 255."""
+    n, D = 40, 64
+    k = torch.randn(n, 1, D, generator=torch.Generator().manual_seed(1)).double()
+    for at in (0, 17, 39):
+        pools, table, ctx, _, _ = shared_context(n, 16, 1, D, k, k, 3)
+        lay = Layout([n], [n], 16)
+        page, slot = lay.place(0, at)
+        pools[1][page, 0, slot * D:(slot + 1) * D] = 0
+        pools[1][page, 0, 16 * D + slot] = 255
+        y = cuda_lib.paged_attn_decode(torch.ones(3, 4, 1, D, device=DEV, dtype=torch.bfloat16), *pools, table, ctx)
+        assert torch.isnan(y).all()
