@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads)
       const float mul = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
       uint8_t* page = fp8_page(a, w, p.page, h);
       for (int d = lane; d < a.D / 4; d += 32)
-        *reinterpret_cast<uint32_t*>(page + p.slot * a.D + 4 * d) =
+        *reinterpret_cast<uint32_t*>(page + static_cast<int64_t>(p.slot) * a.D + 4 * d) =
             bad ? 0u
                 : to_e4m3x4(x[4 * d] * mul, x[4 * d + 1] * mul, x[4 * d + 2] * mul,
                             x[4 * d + 3] * mul);

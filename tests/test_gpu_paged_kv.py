@@ -335,3 +335,27 @@ def test_refusals(cuda_lib):
         sa.paged_kv_read(*pools, table, ctx_t, None, total=40, head_dim=128)
     with pytest.raises(sa.SAError):            # one output for both
         sa.paged_kv_read(*pools, table, ctx_t, start, k, k)
+
+
+def test_places_past_2_to_the_31_bytes_of_a_page(cuda_lib):
+    """Rows behind the first 2^31 bytes of one page, through the kernel for any rotary_dim
+    (a rotation by no angle) and through the other one."""
+    D, pt, n = 256, (1 << 23) + 64, 5
+    k, v = rows((n, 1, D), "f32", 1), rows((n, 1, D), "f32", 2)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    ctx = torch.tensor([pt - 3], dtype=torch.int32, device=DEV)
+    start = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    first = pt - 3 - n
+    for rope in (cuda_lib.rope_table(20, inv_freq=[0.0] * 10), None):
+        pools = [cuda_lib.new_fp8_pool(1, 1, pt, D) for _ in range(2)]
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        cuda_lib.paged_kv_write(k.to(DEV), v.to(DEV), *pools, table, ctx, start, rope=rope, err_word=err)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        for x, p in ((k, pools[0]), (v, pools[1])):
+            codes, scales = orc.quantise_rows(x[:, 0])
+            page = p[0, 0]
+            assert torch.equal(page[first * D:(first + n) * D].cpu().view(n, D), codes)
+            assert torch.equal(page[pt * D + first:pt * D + first + n].cpu(), scales)
+            assert int((page[:first * D].view(torch.int64) != 0).sum()) == 0
+        del pools, page, p
