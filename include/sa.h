@@ -669,7 +669,8 @@ int sa_rope_table(const sa_rope_config* c, sa_rope* out);
  * positions for every batch).  q_out / k_out may be the input itself (same
  * pointer and strides); any other overlap is SA_ERR_OVERLAP.  dtype SA_F32,
  * SA_F16 or SA_BF16; angles are reduced exactly, cos and sin and the rotation
- * are fp32, rounded once.  S 0 is a call that does nothing.
+ * are fp32, rounded once.  S 0 is a call that does nothing; B * S of 2^31 - 256 and
+ * more is SA_ERR_UNSUPPORTED.
  */
 typedef struct {
   const void* q;
@@ -715,7 +716,8 @@ int rotary_embed(const sa_rotary_params* p, void* stream);
  * skipped, and no access leaves the tensors.  Two rows written to one slot (a
  * page shared by two sequences) leave bytes of both there, in no order.
  * pool_format 0 (pages [num_pages, Hkv, page_tokens, D] of dtype) serves any D
- * up to 1024; the rope then needs rotary_dim <= D.  No workspace.
+ * up to 1024; the rope then needs rotary_dim <= D.  T below 2^31 - 256.  No
+ * workspace.
  */
 typedef struct {
   void* k;

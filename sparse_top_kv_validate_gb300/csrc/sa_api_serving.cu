@@ -14,6 +14,8 @@
 namespace {
 
 constexpr int64_t kMaxInt = int64_t(1) << 31;
+// Tokens of a call: the kernels' indexes run past the last token by less than a block.
+constexpr int64_t kMaxTokens = kMaxInt - 256;
 
 size_t dtype_bytes(int dt) { return dt == SA_F32 ? 4 : (dt == SA_F16 || dt == SA_BF16) ? 2 : 0; }
 
@@ -200,7 +202,7 @@ int rotary_embed(const sa_rotary_params* p, void* stream) {
   if (p->B <= 0 || p->S < 0 || p->Hq <= 0 || p->D <= 0 || (p->k && p->Hk <= 0) || p->pos_stride < 0)
     return SA_ERR_SHAPE;
   if (!rope_ok(p->rope) || p->rope->rotary_dim > p->D) return SA_ERR_SHAPE;
-  if (p->B >= kMaxInt || p->S >= kMaxInt || p->B * p->S >= kMaxInt || p->Hq >= kMaxInt / 4 ||
+  if (p->B >= kMaxInt || p->S >= kMaxInt || p->B * p->S >= kMaxTokens || p->Hq >= kMaxInt / 4 ||
       p->Hk >= kMaxInt / 4 || p->D - p->rope->rotary_dim / 2 > 256)
     return SA_ERR_UNSUPPORTED;
   auto tensor = [&](const void* ptr, int64_t H, const int64_t (&st)[3]) {
@@ -264,7 +266,7 @@ static int kv_pages_args(const sa_kv_pages_params* p, bool write, sa::KvPagesArg
   if (!p->seq_start && p->T != p->B) return SA_ERR_SHAPE;
   if (p->rope && (!rope_ok(p->rope) || p->rope->rotary_dim > p->D)) return SA_ERR_SHAPE;
   if (p->rope && !write) return SA_ERR_UNSUPPORTED;
-  if (p->D > 1024 || p->T >= kMaxInt || p->B >= kMaxInt || p->Hkv >= (int64_t(1) << 20) ||
+  if (p->D > 1024 || p->T >= kMaxTokens || p->B >= kMaxInt || p->Hkv >= (int64_t(1) << 20) ||
       p->page_tokens >= kMaxInt || p->max_pages >= kMaxInt || p->num_pages >= kMaxInt ||
       p->max_pages * p->page_tokens >= kMaxInt)
     return SA_ERR_UNSUPPORTED;

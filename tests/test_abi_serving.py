@@ -171,3 +171,16 @@ def test_packed_parameters_are_the_structures(packed, py):
     values = list(range(1, 1 + len(list(flat(py())))))
     p = py.from_buffer_copy(packed.pack(*values))
     assert packed.size == C.sizeof(py) and list(flat(p)) == values
+
+
+@pytest.mark.parametrize("T", [(1 << 31) - 8, (1 << 31) - 256])
+def test_token_counts_near_2_to_the_31_are_refused(host_lib, T):  # noqa: F811
+    """The kernels round the tokens up to blocks in 32 bits."""
+    keep = []
+    p = _set(_rotary(keep), S=T, k=None, k_out=None, q_out=1 << 44)
+    assert host_lib.rotary_embed(C.byref(p), None) == -7
+    p = _set(p, S=T // 2 + 1, B=2, q_strides=[T * 1024, 1024, 128], q_out_strides=[T * 1024, 1024, 128])
+    assert host_lib.rotary_embed(C.byref(p), None) == -7
+    p = _set(_pages(), T=T, k=1 << 44, v=1 << 46)
+    for fn in (host_lib.paged_kv_write, host_lib.paged_kv_read):
+        assert fn(C.byref(p), None) == -7
