@@ -851,7 +851,10 @@ static int check_paged(const sa_paged_params* p, int query = 0) {
         (reinterpret_cast<uintptr_t>(p->k_new) | reinterpret_cast<uintptr_t>(p->v_new)) % 2)
       return SA_ERR_ALIGN;
   }
-  if (p->num_pages * p->Hkv * p->page_tokens >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;
+  constexpr int64_t k31 = int64_t(1) << 31;  // (one factor at a time: the product could wrap around)
+  if (p->num_pages >= k31 || p->Hkv >= k31 || p->num_pages * p->Hkv >= k31 || p->page_tokens >= k31 ||
+      p->num_pages * p->Hkv * p->page_tokens >= k31)
+    return SA_ERR_UNSUPPORTED;
   if (!std::isfinite(p->scale)) return SA_ERR_SHAPE;
   const size_t es = dtype_bytes(p->dtype);
   const size_t yb = static_cast<size_t>(p->B * p->Hq * p->D) * es;

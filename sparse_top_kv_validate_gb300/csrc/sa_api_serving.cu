@@ -36,8 +36,8 @@ struct Strided {
     return ok;
   }
   bool strides_ok() const {
-    for (int i = 0; i < axes; ++i)
-      if (n[i] > 1 && (st[i] < 0 || st[i] >= (int64_t(1) << 40))) return false;
+    for (int i = 0; i < axes; ++i)  // (no device holds 2^58 elements: extent() stays in 64 bits)
+      if (n[i] > 1 && (st[i] < 0 || st[i] >= (int64_t(1) << 40) || st[i] > (int64_t(1) << 58) / n[i])) return false;
     return true;
   }
   // No two elements share an address.
@@ -282,7 +282,9 @@ static int kv_pages_args(const sa_kv_pages_params* p, bool write, sa::KvPagesArg
     if (!aligned(x[i].p, es)) return SA_ERR_ALIGN;
   }
   const size_t row = fp8 ? static_cast<size_t>(p->D + 1) : static_cast<size_t>(p->D) * es;
-  const size_t pool = static_cast<size_t>(p->num_pages * p->Hkv * p->page_tokens) * row;
+  const int64_t head_page = p->page_tokens * static_cast<int64_t>(row);  // (below 2^43)
+  if (p->num_pages * p->Hkv > (int64_t(1) << 62) / head_page) return SA_ERR_UNSUPPORTED;
+  const size_t pool = static_cast<size_t>(p->num_pages * p->Hkv * head_page);
   if (ranges_meet(p->k_pool, pool, p->v_pool, pool)) return SA_ERR_OVERLAP;
   if (p->T > 0) {
     for (int i = 0; i < 2; ++i)

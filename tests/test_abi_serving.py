@@ -184,3 +184,19 @@ def test_token_counts_near_2_to_the_31_are_refused(host_lib, T):  # noqa: F811
     p = _set(_pages(), T=T, k=1 << 44, v=1 << 46)
     for fn in (host_lib.paged_kv_write, host_lib.paged_kv_read):
         assert fn(C.byref(p), None) == -7
+
+
+def test_sizes_whose_products_leave_64_bits_are_refused(host_lib):  # noqa: F811
+    big = dict(num_pages=(1 << 31) - 1, Hkv=1 << 19, page_tokens=(1 << 31) - 16, max_pages=1, k_strides=[1 << 26, 128],
+               v_strides=[1 << 26, 128])
+    for fmt in (sa.FP8_E4M3_PAGE, 0):
+        p = _set(_pages(), pool_format=fmt, **big)
+        for fn in (host_lib.paged_kv_write, host_lib.paged_kv_read):
+            assert fn(C.byref(p), None) == -7
+        p = _set(_fp8_decode(), pool_format=fmt, num_pages=1 << 40, Hkv=1 << 20, Hq=1 << 20, page_tokens=16)
+        assert host_lib.paged_attn_decode(C.byref(p), None) == -7
+    keep = []
+    p = _set(_rotary(keep), S=1 << 30, k=None, k_out=None, q_out=1 << 44, q_strides=[0, (1 << 40) - 128, 128])
+    assert host_lib.rotary_embed(C.byref(p), None) == -2
+    p = _set(_packed(), Tq=(1 << 30) - 1, q_strides=[(1 << 40) - 128, 128])
+    assert host_lib.attn_prefill_packed(C.byref(p), None) == -2
