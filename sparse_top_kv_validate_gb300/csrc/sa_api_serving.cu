@@ -77,23 +77,38 @@ bool ranges_meet(const void* a, size_t na, const void* b, size_t nb) {
   return na && nb && x < y + nb && y < x + na;
 }
 
-// Whether two tensors can share a byte.  Tensors whose rows interleave (heads
-// of one projection's output: the same token stride, each token's heads within
-// it) are told apart by their place inside the token stride.
+// Elements that a tensor takes of every `period` (its axes of smaller strides), or -1
+// when it is not a block that repeats with the period.
+int64_t block_of(const Strided& t, int64_t period) {
+  int64_t e = t.D;
+  for (int i = 0; i < t.axes; ++i) {
+    if (t.n[i] <= 1) continue;
+    if (t.st[i] < period) e += (t.n[i] - 1) * t.st[i];
+    else if (t.st[i] % period) return -1;
+  }
+  return e <= period ? e : -1;
+}
+
+// Whether two tensors can share a byte.  Tensors whose rows interleave (heads of one
+// projection's output, token-major or head-major, in any number of batches) are told
+// apart by their places inside a stride that both repeat with.
 bool overlap(const Strided& a, const Strided& b) {
   if (a.empty() || b.empty()) return false;
   if (!ranges_meet(a.p, a.extent(), b.p, b.extent())) return false;
-  const int t = a.axes - 2;  // the token axis; the head axis is the last
-  if (a.axes != b.axes || a.es != b.es || a.st[t] != b.st[t] || a.n[t] <= 1) return true;
-  for (int i = 0; i < t; ++i)  // one row of tokens through all batches
-    if (a.n[i] != b.n[i] || (a.n[i] > 1 && (a.st[i] != a.n[t] * a.st[t] || b.st[i] != a.st[i]))) return true;
-  const int64_t ts = a.st[t] * static_cast<int64_t>(a.es);
-  const int64_t la = ((a.n[t + 1] - 1) * a.st[t + 1] + a.D) * static_cast<int64_t>(a.es);
-  const int64_t lb = ((b.n[t + 1] - 1) * b.st[t + 1] + b.D) * static_cast<int64_t>(b.es);
-  if (ts <= 0 || la > ts || lb > ts) return true;
-  int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % ts;
-  if (d < 0) d += ts;
-  return !(d >= la && d + lb <= ts);
+  if (a.es != b.es) return true;
+  const int64_t es = static_cast<int64_t>(a.es);
+  for (const Strided* t : {&a, &b})
+    for (int i = 0; i < t->axes; ++i) {
+      const int64_t period = t->st[i];
+      if (t->n[i] <= 1 || period <= 0) continue;
+      const int64_t la = block_of(a, period), lb = block_of(b, period);
+      if (la < 0 || lb < 0) continue;
+      int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) %
+                  (period * es);
+      if (d < 0) d += period * es;
+      if (d >= la * es && d + lb * es <= period * es) return false;
+    }
+  return true;
 }
 
 bool same(const Strided& a, const Strided& b) {

@@ -200,3 +200,23 @@ def test_sizes_whose_products_leave_64_bits_are_refused(host_lib):  # noqa: F811
     assert host_lib.rotary_embed(C.byref(p), None) == -2
     p = _set(_packed(), Tq=(1 << 30) - 1, q_strides=[(1 << 40) - 128, 128])
     assert host_lib.attn_prefill_packed(C.byref(p), None) == -2
+
+
+def test_fused_views_of_several_batches_do_not_overlap(host_lib):  # noqa: F811
+    """q and k as heads of one [B, Hq + 2 Hk, S, D] or [B, S, Hq + 2 Hk, D] buffer, rotated in
+    place; without a device the launch itself is what fails."""
+    keep = []
+    B, S, D, heads = 3, 10, 128, 12
+    for token, head in ((D, S * D), (heads * D, D)):
+        st = [heads * S * D, token, head]
+        k = 0x100000 + 8 * head * 2
+        p = _set(_rotary(keep), B=B, S=S, k=k, q_out=0x100000, k_out=k, q_strides=st, k_strides=st, q_out_strides=st,
+                 k_out_strides=st)
+        assert host_lib.rotary_embed(C.byref(p), None) not in (0, -6)
+        for shift in (1, -1):                             # a head into each other, in every batch
+            x = k + shift * head * 2
+            assert host_lib.rotary_embed(C.byref(_set(p, k=x, k_out=x)), None) == (-6 if shift < 0 else -8)
+        # the next batch's queries: a batch stride too short for the heads
+        short = [10 * S * D - 128, token, head]
+        p = _set(p, k=k, k_out=k, q_strides=short, k_strides=short, q_out_strides=short, k_out_strides=short)
+        assert host_lib.rotary_embed(C.byref(p), None) in (-6, -2)

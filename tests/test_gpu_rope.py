@@ -169,3 +169,27 @@ def test_refusals(cuda_lib):
         sa.rotary_embed(q, None, pos, rope, q_out=torch.zeros(1, 4, 64, device=DEV).expand(8, 4, 64))
     with pytest.raises(sa.SAError):
         sa.rotary_embed(q, q[:, :2], pos, rope, q_out=None, k_out=q[:, 2:])
+
+
+@pytest.mark.parametrize("order", ["head-major", "token-major"])
+def test_views_of_one_projection_of_several_batches_in_place(cuda_lib, order):
+    """q and k as heads of one [B, Hq + 2 Hk, S, D] (or [B, S, Hq + 2 Hk, D]) buffer."""
+    sa = cuda_lib
+    B, S, Hq, Hk, D = 3, 50, 8, 2, 128
+    g = torch.Generator().manual_seed(1)
+    if order == "head-major":
+        buf = torch.randn(B, Hq + 2 * Hk, S, D, generator=g).bfloat16().to(DEV)
+        q, k, v = buf[:, :Hq], buf[:, Hq:Hq + Hk], buf[:, Hq + Hk:]
+    else:
+        buf = torch.randn(B, S, Hq + 2 * Hk, D, generator=g).bfloat16().to(DEV)
+        q, k, v = (x.transpose(1, 2) for x in (buf[:, :, :Hq], buf[:, :, Hq:Hq + Hk], buf[:, :, Hq + Hk:]))
+    pos = torch.randint(0, 5000, (B, S), generator=g).to(DEV)
+    rope = sa.rope_table(D)
+    want = sa.rotary_embed(q.contiguous(), k.contiguous(), pos, rope)
+    before = v.clone()
+    a, b = sa.rotary_embed(q, k, pos, rope, q_out=q, k_out=k)
+    assert a.data_ptr() == q.data_ptr() and b.data_ptr() == k.data_ptr()
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, before)
+    with pytest.raises(sa.SAError):                       # keys that begin inside the queries
+        x = (buf[:, Hq - 1:Hq - 1 + Hk] if order == "head-major" else buf[:, :, Hq - 1:Hq - 1 + Hk].transpose(1, 2))
+        sa.rotary_embed(q, x, pos, rope, q_out=q, k_out=x)
