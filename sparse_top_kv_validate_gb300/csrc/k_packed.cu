@@ -17,7 +17,7 @@
 //    softmax, PV, buffer free) takes about four times as long as its MMAs: three
 //    tiles on the way at once, two of them in softmax, keep the tensor cores
 //    about half busy.  Measured, 4 x 4,096 tokens, 32 / 8 heads of 128, causal,
-//    bf16: 425 us, 1,295 TFLOP/s (softcap 50: 460 us).  Other orders tried, at
+//    bf16: 425 us, 1,295 TFLOP/s (softcap 50: 465 us).  Other orders tried, at
 //    463 us for this one: two row tiles per item that share K and V, a score
 //    buffer and a warpgroup each, 500 us; the same with two MMA lanes that
 //    interleave, so that both tiles' softmax runs at the same time, 625 us; with
@@ -25,10 +25,10 @@
 //  * P is passed on in halves: the PV of the first 64 keys runs while the other
 //    64 probabilities are still being formed (463 -> 453 us).
 //  * A thread reads its 128 scores from tensor memory twice (once where the
-//    offset is fixed, below), in a loop over chunks of 32 columns.  Kept in registers they spill, and local memory
-//    shares its path with the MMAs' shared-memory operands; unrolled, the
-//    roles' loops no longer fit the instruction cache together (both measured:
-//    575 us).  The first pass's maximum comes with the load (tcgen05.ld.red;
+//    offset is fixed, below), in a loop over chunks of 32 columns.  Kept in
+//    registers they spill, and local memory shares its path with the MMAs'
+//    shared-memory operands; unrolled, the roles' loops no longer fit the
+//    instruction cache together (both measured: 575 us).  The first pass's maximum comes with the load (tcgen05.ld.red;
 //    453 -> 434 us), one chunk at a time: with two on their way the plain
 //    variant spills (520 us).
 //  * The two threads of a row agree on its offset tile by tile: a thread posts
@@ -562,8 +562,9 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
 }
 
 // How the log2-domain logit of a score s is formed: c_log2 s (no softcap), or
-// c_log2 tanh(k1 s) by the fitted polynomials (kShort, kPoly) or, where a score of
-// the warp lies outside their ranges, from the hardware exponential and reciprocal.
+// c_log2 tanh(k1 s) by the fitted polynomials (kShort, kPoly) or, where a score of the
+// warp lies outside their ranges or is hidden, from the hardware exponential and
+// reciprocal.
 enum ScoreMode { kPlain = 0, kShort = 1, kPoly = 2, kFar = 3 };
 
 // The constants of that: c2 = c_log2, k1 and the polynomials.
@@ -738,6 +739,13 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
                : !__any_sync(0xffffffffu, !(most <= p.tq_bound)) ? kPoly
                                                                  : kFar;
       };
+      // Whether chunk c holds scores that some row of the warp does not see.  They may be anything
+      // and must not choose the form of the others, so such a chunk takes the one that holds for
+      // all, and no form at all where no row sees any of it.  (bf16, softcap 50, 4 x 4,096 tokens
+      // and 256 x 128: 465 and 254 us; the form chosen by the scores that are seen, the others
+      // cleared, 525 and 276: the loops outgrow the instruction cache; kFar for every chunk of a
+      // tile with hidden scores 451 and 290.)
+      auto partial = [&](int c) { return masked && __any_sync(0xffffffffu, rel - 32 * c < 31); };
       int mode = kPlain;
       float mx = SA_NEG_INF;
       if (!kCap && !masked) {  // the loads find the maximum
@@ -752,7 +760,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       } else if (!kFixed) {
         float ax = 0.f;
         auto look = [&](uint32_t (&x)[32], int c) {
-          if (kCap) ax = fmaxf(ax, largest(x));
+          if (kCap && !partial(c)) ax = fmaxf(ax, largest(x));
           mx = masked ? max_chunk<true>(x, rel - 32 * c, mx) : max_chunk<false>(x, 0, mx);
         };
         tc05::tmem_ld_wait();
@@ -768,10 +776,10 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       if (!kFixed) {
         float mt = SA_NEG_INF;
         if (mx != SA_NEG_INF)
-          mt = mode == kPlain   ? mx * lg.c2
-               : mode == kShort ? poly_logit(mx, lg.ts)
-               : mode == kPoly  ? poly_logit(mx, lg.tq)
-                                : tanh_far(mx * lg.k1) * lg.c2;
+          mt = !kCap                        ? mx * lg.c2
+               : masked || mode == kFar     ? tanh_far(mx * lg.k1) * lg.c2  // (mx: of any chunk)
+               : mode == kPoly              ? poly_logit(mx, lg.tq)
+                                            : poly_logit(mx, lg.ts);
         const bool up = mt > m + kRescaleLog2 || (m == SA_NEG_INF && mt > m);
         xch[(2 * wg + ((u >> 1) & 1)) * kTile] = up ? mt : m;
         __syncwarp();
@@ -802,12 +810,15 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       auto exps = [&](uint32_t (&x)[32], int c, float& most) {
         const int rc = rel - 32 * c;
         uint32_t pk[16];
+        const bool part = kCap && partial(c);
         if (kFixed) mode = mode_of(arrived(most));
         if (!kCap && masked) exp_chunk<kPlain, true, T>(x, pk, lg, neg_m, rc, ls);
         else if (!kCap) exp_chunk<kPlain, false, T>(x, pk, lg, neg_m, 0, ls);
-        else if (mode == kFar) exp_chunk<kFar, true, T>(x, pk, lg, neg_m, masked ? rc : kTile, ls);
-        else if (mode == kPoly) exp_chunk<kPoly, true, T>(x, pk, lg, neg_m, masked ? rc : kTile, ls);
-        else if (masked) exp_chunk<kShort, true, T>(x, pk, lg, neg_m, rc, ls);
+        else if (part && !__any_sync(0xffffffffu, rc >= 0)) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = 0u;
+        } else if (part || mode == kFar) exp_chunk<kFar, true, T>(x, pk, lg, neg_m, part ? rc : kTile, ls);
+        else if (mode == kPoly) exp_chunk<kPoly, false, T>(x, pk, lg, neg_m, 0, ls);
         else exp_chunk<kShort, false, T>(x, pk, lg, neg_m, 0, ls);
         tc05::tmem_st16(tS + c * 16, pk);
       };
@@ -976,14 +987,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *found = 0;
     fence_mbar_init();
   }
-  // rows of the query tiles that no head fills (g does not divide 128): zeros once
-  const int used = p.g * p.tpt;
-  for (int e = static_cast<int>(threadIdx.x); e < (kTile - used) * 8 * G::kSlabs * 2; e += kThreads) {
-    const int r = used + e / (16 * G::kSlabs), c = e % (16 * G::kSlabs);
-    *reinterpret_cast<uint4*>(sm + G::kOffQ + (c >> 3) * kSlabBytes + r * 128 + (c & 7) * 16) =
-        make_uint4(0u, 0u, 0u, 0u);
-  }
-  fence_proxy_async_smem();
+  // (Rows of a query tile that no head fills, where g does not divide 128, hold whatever the
+  // shared memory held: their scores are all masked.)
   if (warp == 1) {
     tc05::tmem_alloc(tslot, G::kTmemCols);
     tc05::tmem_relinquish();

@@ -235,3 +235,39 @@ def test_scores_that_reach_the_softcap(cuda_lib, dt, cap, lean):
         q, k, v, qs, ks = leaning(dt, [200, 70], [512, 70], Hq, Hkv, D, lean, seed=int(cap))
         y = cuda_lib.attn_prefill_packed(q.to(DEV), k.to(DEV), v.to(DEV), starts(qs), starts(ks), softcap=cap)
         check_tail(y, q, k, v, qs, ks, True, cap, f"{dt} cap {cap} lean {lean} D {D}")
+
+
+@pytest.mark.parametrize("dt,D,cap", [("bf16", 128, 30.0), ("bf16", 64, 200.0), ("f16", 128, 30.0), ("f16", 64, 9.0)])
+def test_with_a_softcap_too_neighbours_and_hidden_keys_leave_the_bits(cuda_lib, dt, D, cap):
+    """Keys that none of a warp's rows sees and other sequences' queries and keys do not choose
+    the form in which its logits are computed."""
+    q, k, v, qs, ks = make(dt, [70, 70, 64], [100, 70, 64], 4, 2, D)
+    run = lambda *a: cuda_lib.attn_prefill_packed(*(t.to(DEV) for t in a), starts(qs), starts(ks), softcap=cap)  # noqa: E731
+    clean = run(q, k, v)
+    for x in (float("nan"), 300.0):
+        k2, q2 = k.clone(), q.clone()
+        k2[100:170], q2[70:140] = x, x                             # the whole second sequence
+        k2[218:] = x                                               # the third's keys 48 to 63
+        y = run(q2, k2, v)
+        assert torch.equal(y[:70], clean[:70])
+        assert torch.equal(y[140:188], clean[140:188])             # its queries 0 .. 47: three warps
+
+
+@pytest.mark.parametrize("g", [3, 5])
+@pytest.mark.parametrize("cap", [30.0, 200.0])
+def test_rows_of_a_tile_without_a_head_do_not_count(cuda_lib, g, cap):
+    """Heads that do not divide 128, several query tiles per CTA: large outputs of other
+    sequences, which pass through the query tiles' memory, leave a row's bits alone."""
+    n = [50] * 120
+    q, k, v, qs, _ = make("bf16", n, n, 4 * g, 4, 64, seed=g)
+    run = lambda v: cuda_lib.attn_prefill_packed(q.to(DEV), k.to(DEV), v.to(DEV), starts(qs), softcap=cap)  # noqa: E731
+    clean = run(v)
+    for period in (2, 4, 8, 16, 32):                               # whichever items share a CTA's buffer
+        v2 = v.clone()
+        for b in range(120):
+            if b % period < period // 2:
+                v2[qs[b]:qs[b + 1]] *= 1e4
+        y = run(v2)
+        for b in range(120):
+            if b % period >= period // 2:
+                assert torch.equal(y[qs[b]:qs[b + 1]], clean[qs[b]:qs[b + 1]]), (period, b)
