@@ -911,16 +911,27 @@ class _launching:
         return False
 
 
+class _Kept(threading.local):
+    """Scratch kept per host thread, device and stream (a handle).  Per thread, as a call is
+    several launches: two threads' launches on one stream may alternate."""
+
+    def __init__(self):
+        self.of = {}
+
+
+_kept = _Kept()
+
+
 def _kept_workspace(device, stream):
-    """The scratch kept for calls on ``stream`` (a handle), or None: none yet, or a
-    graph is being captured."""
-    ws = _ws_cache.get(("launch", device.index, stream))
+    """The scratch kept for this thread's calls on ``stream`` (a handle), or None: none
+    yet, or a graph is being captured."""
+    ws = _kept.of.get((device.index, stream))
     return None if ws is None or torch.cuda.is_current_stream_capturing() else ws
 
 
 def _stream_workspace(nbytes, device, stream, workspace):
     """Scratch for one call on ``stream`` (a handle): the given tensor, else one
-    kept per (device, stream), so that calls that may overlap never share it.
+    kept per (thread, device, stream), so that calls that may overlap never share it.
     Under graph capture it comes from the graph's own memory instead: a kept
     tensor could be replaced while the graph still names it, or be shared with
     another graph that replays at the same time."""
@@ -931,11 +942,11 @@ def _stream_workspace(nbytes, device, stream, workspace):
         return None, 0
     if torch.cuda.is_current_stream_capturing():
         return new_workspace(nbytes, device), nbytes
-    key = ("launch", device.index, stream)
-    buf = _ws_cache.get(key)
+    key = (device.index, stream)
+    buf = _kept.of.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = new_workspace(max(nbytes, 1 << 20), device)
-        _ws_cache[key] = buf
+        _kept.of[key] = buf
     return buf, buf.numel()
 
 

@@ -220,3 +220,28 @@ def test_fused_views_of_several_batches_do_not_overlap(host_lib):  # noqa: F811
         short = [10 * S * D - 128, token, head]
         p = _set(p, k=k, k_out=k, q_strides=short, k_strides=short, q_out_strides=short, k_out_strides=short)
         assert host_lib.rotary_embed(C.byref(p), None) in (-6, -2)
+
+
+def test_threads_do_not_share_the_kept_scratch(monkeypatch):
+    """A call is several launches; two threads' launches on one stream may alternate."""
+    import threading
+
+    import torch
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(sa, "new_workspace", lambda n, device: torch.empty(n, dtype=torch.uint8))
+    device, got = torch.device("cuda", 0), {}
+
+    def work(name):
+        got[name] = [sa._stream_workspace(n, device, 7, None)[0] for n in (1 << 21, 1 << 10)]
+        got[name].append(sa._kept_workspace(device, 7))
+        barrier.wait()
+
+    barrier = threading.Barrier(2)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for mine in got.values():                            # kept within a thread
+        assert mine[0] is mine[1] and mine[0] is mine[2]
+    assert got[0][0].data_ptr() != got[1][0].data_ptr()

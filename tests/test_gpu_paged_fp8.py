@@ -353,3 +353,28 @@ def test_a_nan_row_of_zero_codes_is_still_nan(cuda_lib):
         pools[1][page, 0, 16 * D + slot] = 255
         y = cuda_lib.paged_attn_decode(torch.ones(3, 4, 1, D, device=DEV, dtype=torch.bfloat16), *pools, table, ctx)
         assert torch.isnan(y).all()
+
+
+def test_two_threads_on_one_stream(cuda_lib):
+    """Their calls' launches may alternate on the stream: each thread has scratch of its own."""
+    import threading
+    sa = cuda_lib
+    lay = Layout([20000, 3000], [1, 1], 16, seed=8)
+    pools = [p.to(DEV) for p in fill(lay, 2, 128, 5)]
+    table, ctx_t, _ = lay.gpu()
+    qs = [torch.randn(2, 8, 1, 128, generator=torch.Generator().manual_seed(i)).bfloat16().to(DEV) for i in range(4)]
+    want = [sa.paged_attn_decode(q, *pools, table, ctx_t) for q in qs]
+    torch.cuda.synchronize()
+    got, barrier = [None] * 4, threading.Barrier(4)
+
+    def work(i):
+        barrier.wait()
+        got[i] = [sa.paged_attn_decode(qs[i], *pools, table, ctx_t) for _ in range(100)]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(4) for y in got[i])
