@@ -896,6 +896,8 @@ class _launching:
 
     def __enter__(self):
         index = self.device.index
+        if self.stream is not None and self.stream.device != self.device:
+            raise ValueError(f"stream is on {self.stream.device}, the tensors are on {self.device}")
         if self.stream is None and index == torch.cuda.current_device():
             return _stream_handle(index)
         self.stack = contextlib.ExitStack()
@@ -936,7 +938,8 @@ def _stream_workspace(nbytes, device, stream, workspace):
     tensor could be replaced while the graph still names it, or be shared with
     another graph that replays at the same time."""
     if workspace is not None:
-        _dev(workspace, "workspace")
+        if _dev(workspace, "workspace").device != device:
+            raise ValueError(f"workspace is on {workspace.device}, not on {device}")
         return workspace, workspace.numel() * workspace.element_size()
     if nbytes == 0:
         return None, 0

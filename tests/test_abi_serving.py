@@ -245,3 +245,20 @@ def test_threads_do_not_share_the_kept_scratch(monkeypatch):
     for mine in got.values():                            # kept within a thread
         assert mine[0] is mine[1] and mine[0] is mine[2]
     assert got[0][0].data_ptr() != got[1][0].data_ptr()
+
+
+def test_a_stream_or_a_workspace_of_another_device_is_refused():
+    """Stand-ins for what a second device would give: the checks read nothing else."""
+    import types
+
+    import torch
+    device, other = torch.device("cuda", 0), torch.device("cuda", 1)
+    with pytest.raises(ValueError):
+        with sa._launching(device, types.SimpleNamespace(device=other, cuda_stream=5)):
+            pass
+
+    class Elsewhere(torch.Tensor):
+        device, is_cuda = other, True
+
+    with pytest.raises(ValueError):
+        sa._stream_workspace(16, device, 5, torch.empty(16, dtype=torch.uint8).as_subclass(Elsewhere))
