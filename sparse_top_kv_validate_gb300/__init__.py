@@ -1088,7 +1088,7 @@ def rotary_embed(q, k, positions, rope, *, q_out=None, k_out=None, stream=None):
         if k is not None and k_out is None:
             k_out = torch.empty(ks, dtype=q.dtype, device=device)
         table = _rope_arg(rope)
-        if S * B * Hq * D == 0:
+        if S * B * D * max(Hq, Hk) == 0:  # (keys without queries go on, and are refused)
             return q_out, k_out
         token, head = (0, 1) if dims == 3 else (2, 1)
         strides = []

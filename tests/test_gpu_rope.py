@@ -193,3 +193,18 @@ def test_views_of_one_projection_of_several_batches_in_place(cuda_lib, order):
     with pytest.raises(sa.SAError):                       # keys that begin inside the queries
         x = (buf[:, Hq - 1:Hq - 1 + Hk] if order == "head-major" else buf[:, :, Hq - 1:Hq - 1 + Hk].transpose(1, 2))
         sa.rotary_embed(q, x, pos, rope, q_out=q, k_out=x)
+
+
+def test_keys_without_queries_are_refused(cuda_lib):
+    """Queries of no heads beside keys of some: not a call that returns keys never written."""
+    sa = cuda_lib
+    rope, pos = sa.rope_table(64), torch.arange(5, device=DEV)
+    k = torch.ones(5, 2, 64, device=DEV, dtype=torch.bfloat16)
+    with pytest.raises(sa.SAError):
+        sa.rotary_embed(k[:, :0], k, pos, rope)
+    with pytest.raises(sa.SAError):
+        sa.rotary_embed(k[None].transpose(1, 2)[:, :0], k[None].transpose(1, 2), pos, rope)
+    q, none = sa.rotary_embed(k[:, :0], None, pos, rope)
+    assert q.shape == (5, 0, 64) and none is None
+    q, x = sa.rotary_embed(k[:0], k[:0], pos[:0], rope)
+    assert q.shape == x.shape == (0, 2, 64)
