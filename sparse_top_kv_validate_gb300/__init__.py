@@ -259,14 +259,19 @@ def load():
         L.sa_graph_kernel_count.argtypes = [_p]
         L.paged_attn_decode_workspace.restype = C.c_size_t
         L.paged_attn_decode_workspace.argtypes = [C.POINTER(PagedParams)]
-        L.paged_attn_decode.restype = C.c_int
-        L.paged_attn_decode.argtypes = [_p, _p]
         L.sa_rope_table.restype = C.c_int
         L.sa_rope_table.argtypes = [C.POINTER(_RopeConfig), C.POINTER(RopeTable)]
-        for name in ("rotary_embed", "paged_kv_write", "paged_kv_read", "attn_prefill_packed"):
+        for name, params in (("paged_attn_decode", PagedParams), ("rotary_embed", RotaryParams),
+                             ("paged_kv_write", KvPagesParams), ("paged_kv_read", KvPagesParams),
+                             ("attn_prefill_packed", PackedParams)):
             fn = getattr(L, name)
             fn.restype = C.c_int
-            fn.argtypes = [_p, _p]
+            fn.argtypes = [C.POINTER(params), _p]
+            # the same entry for the calls below that pack their parameters as bytes
+            raw = L[name]
+            raw.restype = C.c_int
+            raw.argtypes = [C.c_char_p, _p]
+            setattr(L, name + "_bytes", raw)
         _lib = L
         return _lib
 
@@ -641,14 +646,14 @@ def _paged_fp8_decode(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, 
             # the kept scratch is nearly always large enough: ask only when it is not
             ws = _kept_workspace(device, s)
             if ws is not None:
-                rc = L.paged_attn_decode(params(ws.data_ptr(), ws.numel()), s)
+                rc = L.paged_attn_decode_bytes(params(ws.data_ptr(), ws.numel()), s)
                 if rc != ERR_WORKSPACE:
                     _check("paged_attn_decode", rc)
                     return y
         p = PagedParams.from_buffer_copy(params(0, 0))
         ws, nb = _stream_workspace(int(L.paged_attn_decode_workspace(C.byref(p))), device, s,
                                    workspace)
-        _check("paged_attn_decode", L.paged_attn_decode(params(_addr(ws), nb), s))
+        _check("paged_attn_decode", L.paged_attn_decode_bytes(params(_addr(ws), nb), s))
     return y
 
 
@@ -1097,7 +1102,7 @@ def rotary_embed(q, k, positions, rope, *, q_out=None, k_out=None, stream=None):
         p = _ROTARY.pack(
             q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out), positions.data_ptr(), table,
             dtype, i64, B, S, Hq, Hk, D, S if len(ps) == 2 else 0, *strides)
-        _check("rotary_embed", L.rotary_embed(p, s))
+        _check("rotary_embed", L.rotary_embed_bytes(p, s))
     return q_out, k_out
 
 
@@ -1155,7 +1160,7 @@ def paged_kv_write(k, v, k_pool, v_pool, block_table, ctx_len, seq_start=None, *
     if p is None:
         return
     with _launching(device, stream) as s:
-        _check("paged_kv_write", L.paged_kv_write(p, s))
+        _check("paged_kv_write", L.paged_kv_write_bytes(p, s))
 
 
 def paged_kv_read(k_pool, v_pool, block_table, ctx_len, seq_start, k=None, v=None, *, total=None,
@@ -1180,7 +1185,7 @@ def paged_kv_read(k_pool, v_pool, block_table, ctx_len, seq_start, k=None, v=Non
         p, _ = _kv_pages_params(k, v, k_pool, v_pool, block_table, ctx_len, seq_start, None,
                                 err_word)
         if p is not None:
-            _check("paged_kv_read", L.paged_kv_read(p, s))
+            _check("paged_kv_read", L.paged_kv_read_bytes(p, s))
     return k, v
 
 
@@ -1223,5 +1228,5 @@ def attn_prefill_packed(q, k, v, q_start, k_start=None, *, causal=True, scale=0.
             q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), q_start.data_ptr(),
             _addr(k_start), _addr(err_word), _dt(q), bool(causal), B, Tq, Tk, Hq, Hkv, D,
             qst[0], qst[1], kst[0], kst[1], vst[0], vst[1], yst[0], yst[1], scale, softcap)
-        _check("attn_prefill_packed", L.attn_prefill_packed(p, s))
+        _check("attn_prefill_packed", L.attn_prefill_packed_bytes(p, s))
     return y

@@ -262,3 +262,14 @@ def test_a_stream_or_a_workspace_of_another_device_is_refused():
 
     with pytest.raises(ValueError):
         sa._stream_workspace(16, device, 5, torch.empty(16, dtype=torch.uint8).as_subclass(Elsewhere))
+
+
+@pytest.mark.parametrize("name,params", [("paged_attn_decode", sa.PagedParams), ("rotary_embed", sa.RotaryParams),
+                                         ("paged_kv_write", sa.KvPagesParams), ("paged_kv_read", sa.KvPagesParams),
+                                         ("attn_prefill_packed", sa.PackedParams)])
+def test_entries_check_the_structure_they_are_given(lib, name, params):  # noqa: F811
+    fn = getattr(lib, name)
+    assert fn(None, None) == -1
+    for wrong in (C.byref(sa.PrefillParams()), bytes(C.sizeof(params)), 0x1000):
+        with pytest.raises(C.ArgumentError):
+            fn(wrong, None)
