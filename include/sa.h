@@ -85,6 +85,7 @@ extern "C" {
  * 255 is NaN.  D is 64, 128 or 256 and page_tokens a multiple of 16, so that
  * a page of one head is one contiguous, 16-byte aligned piece. */
 #define SA_FP8_E4M3_PAGE 4
+#define SA_MAX_FORMAT 255 /* formats yet to come lie below this */
 
 /* ---- index-row status codes (row_status bytes; OR-ed into err_word) --- */
 #define SA_IDX_BELOW_SENTINEL 1  /* a value below -1                          */
@@ -606,7 +607,9 @@ typedef struct {
   uint32_t options;     /* 0, or SA_OPT_ROW_COPIES (pages fetched row by row) */
   int64_t B, Hq, Hkv, D, page_tokens, max_pages, num_pages;
   float scale;
-  int32_t pool_format;  /* 0: elements of dtype, or SA_FP8_E4M3_PAGE */
+  int32_t pool_format;  /* 0: elements of dtype, or SA_FP8_E4M3_PAGE.  Padding before
+                           version 0.2: what is no format, 1 .. SA_MAX_FORMAT,
+                           counts as 0 */
   uint32_t* err_word;
   void* workspace;
   size_t workspace_bytes;

@@ -465,7 +465,7 @@ const char* sa_status_string(int status) {
   }
 }
 
-int sa_version(void) { return 100; }
+int sa_version(void) { return 200; }
 
 int validate_indices(const void* idx, int idx_is_i64, int64_t B, int64_t I, int64_t Sq,
                      int64_t K, const int64_t* bound_per_batch, int64_t bound,
@@ -839,7 +839,8 @@ static int check_paged(const sa_paged_params* p, int query = 0) {
   if (p->Hq % p->Hkv != 0) return SA_ERR_SHAPE;
   if (dtype_bytes(p->dtype) == 0) return SA_ERR_DTYPE;
   const bool fp8 = p->pool_format == SA_FP8_E4M3_PAGE;
-  if (p->pool_format != 0 && !fp8) return SA_ERR_DTYPE;
+  // (a larger value: the padding that lay here before version 0.2, never set)
+  if (p->pool_format > 0 && p->pool_format <= SA_MAX_FORMAT && !fp8) return SA_ERR_DTYPE;
   if (p->options & ~SA_OPT_ROW_COPIES) return SA_ERR_UNSUPPORTED;
   if (fp8) {
     if (p->dtype == SA_F32) return SA_ERR_DTYPE;

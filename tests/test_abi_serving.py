@@ -273,3 +273,16 @@ def test_entries_check_the_structure_they_are_given(lib, name, params):  # noqa:
     for wrong in (C.byref(sa.PrefillParams()), bytes(C.sizeof(params)), 0x1000):
         with pytest.raises(C.ArgumentError):
             fn(wrong, None)
+
+
+def test_callers_that_never_set_the_field_before_pool_format(host_lib):  # noqa: F811
+    """The field was padding: what an older caller left there changes nothing."""
+    assert host_lib.sa_version() >= 200
+    need = host_lib.paged_attn_decode_workspace(C.byref(_set(_fp8_decode(), pool_format=0)))
+    assert need > 0
+    for rubbish in (0x40490FDB, -1, 256, 0x7FFFFFFF, -(1 << 31)):
+        p = _set(_fp8_decode(), pool_format=rubbish)
+        assert host_lib.paged_attn_decode_workspace(C.byref(p)) == need
+        assert host_lib.paged_attn_decode(C.byref(p), None) == -5
+    for fmt in (1, 2, 3, 5, 255):
+        assert host_lib.paged_attn_decode(C.byref(_set(_fp8_decode(), pool_format=fmt)), None) == -3
