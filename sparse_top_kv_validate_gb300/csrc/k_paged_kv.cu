@@ -447,15 +447,16 @@ __global__ void __launch_bounds__(kThreads)
 // more often), as long as the blocks cover the SMs twice (a decode step's 128 tokens
 // in 128 blocks, 6.2 us).
 int tokens_per_block(const KvPagesArgs& a) {
-  const int most = kThreads / 2 / (a.D / 16);
+  const int most = kThreads / 2 / (a.D / 16), sms = sm_count();
   int tt = 1;
-  while (2 * tt <= kMaxTok && 2 * tt <= most && a.T / (2 * tt) >= 2 * 152) tt *= 2;
+  while (2 * tt <= kMaxTok && 2 * tt <= most && a.T / (2 * tt) >= 2 * sms) tt *= 2;
   return tt;
 }
 
 unsigned row_blocks(const KvPagesArgs& a) {
   const int64_t blocks = (static_cast<int64_t>(a.T) * 2 * a.Hkv + kWarps - 1) / kWarps;
-  return static_cast<unsigned>(blocks < 152 * 16 ? blocks : 152 * 16);
+  const int64_t most = 16 * static_cast<int64_t>(sm_count());
+  return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
 template <typename T>

@@ -161,7 +161,8 @@ int launch_t(const RotaryArgs& a, cudaStream_t st) {
   // Up to 8 tokens per block once the blocks still cover the SMs twice: then
   // four tokens' rows share a warp's loads and the set-up is paid once per 8.
   int tt = 8;
-  while (tt > 1 && ((a.T + tt - 1) / tt < 2 * 152 || lanes * tt > kThreads)) tt /= 2;
+  const int sms = sm_count();
+  while (tt > 1 && ((a.T + tt - 1) / tt < 2 * sms || lanes * tt > kThreads)) tt /= 2;
   const unsigned grid = static_cast<unsigned>((a.T + tt - 1) / tt);
   const size_t smem =
       (a.vec ? RowRing<T>::kBytes : 0) + static_cast<size_t>(tt) * 2 * half * sizeof(float);
