@@ -17,7 +17,7 @@
 //    softmax, PV, buffer free) takes about four times as long as its MMAs: three
 //    tiles on the way at once, two of them in softmax, keep the tensor cores
 //    about half busy.  Measured, 4 x 4,096 tokens, 32 / 8 heads of 128, causal,
-//    bf16: 425 us, 1,295 TFLOP/s (softcap 50: 465 us).  Other orders tried, at
+//    bf16: 425 us, 1,295 TFLOP/s (softcap 50: 475 us).  Other orders tried, at
 //    463 us for this one: two row tiles per item that share K and V, a score
 //    buffer and a warpgroup each, 500 us; the same with two MMA lanes that
 //    interleave, so that both tiles' softmax runs at the same time, 625 us; with
@@ -28,15 +28,21 @@
 //    offset is fixed, below), in a loop over chunks of 32 columns.  Kept in
 //    registers they spill, and local memory shares its path with the MMAs'
 //    shared-memory operands; unrolled, the roles' loops no longer fit the
-//    instruction cache together (both measured: 575 us).  The first pass's maximum comes with the load (tcgen05.ld.red;
-//    453 -> 434 us), one chunk at a time: with two on their way the plain
-//    variant spills (520 us).
+//    instruction cache together (both measured: 575 us).  The first pass's
+//    maximum comes with the load (tcgen05.ld.red; 453 -> 434 us), one chunk at a
+//    time: with two on their way the plain variant spills (520 us).
 //  * The two threads of a row agree on its offset tile by tile: a thread posts
 //    the offset after its tile (the old one unless the tile's maximum exceeds it
 //    by more than 2^8), the other one's next tile starts from it.  The raise
 //    rescales O in tensor memory, after the previous PV.  With a softcap that bounds
 //    2^logit to the normal numbers of P's type (up to 67 in bf16, 9.7 in f16) the
-//    offset is 0 and nothing is posted.
+//    offset is 0 and nothing is posted (softcap 50: bf16 475 us, f16, with an
+//    offset, 626).
+//  * P enters the second product in q's type, as the MMA takes it: each probability
+//    is off by up to half a step of it (2^-8 bf16, 2^-11 f16 of itself; in f16 also
+//    by 2^-25 of the row's largest), while the row's sum adds them in fp32.  Against
+//    64 bits the outputs are 1.2 to 1.4 times as far off as with fp32 probabilities.
+//    (P in two parts would be a second PV per tile.)
 //  * Warp 0 loads Q (box: 64 dims x g heads x 128 / g tokens; two buffers) and the
 //    K and V tiles through two rings; warp 1's lane issues S = Q K^T and warp 3's
 //    O += P V (P over the first half of its scores), so that a barrier wait or a
@@ -720,7 +726,11 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       float mr[2];
       tmem_ld32_max<kFixed>(tS + (kFixed ? 0 : 96), r[0], mr[0]);  // (the first pass goes backwards)
       const int tok = it.tok + rt;
-      const int lim = rt < p.tpt && tok < it.nq ? last_key(p.causal, it.nq, it.nk, tok) : -1;  // last visible key
+      // A row of no query is no reason to mask: nothing of it is kept, and it has no say in what
+      // the warp does.  (As a row that sees nothing it sent every tile of a sequence's last item
+      // the longer way: chunks after 24,000 tokens 175 us, softcap 50 206, now 155 and 175.)
+      const bool live = rt < p.tpt && tok < it.nq;
+      const int lim = live ? last_key(p.causal, it.nq, it.nk, tok) : 0x7fffffff;  // last visible key
       const int rel = lim - j * kTile;  // columns above rel are masked
       const bool masked = __any_sync(0xffffffffu, rel < kTile - 1);
       if (!kFixed && j > 0) {
@@ -735,6 +745,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
         }
       }
       auto mode_of = [&](float most) {  // the cheapest form that holds for the warp's scores
+        most = live ? most : 0.f;
         return !__any_sync(0xffffffffu, !(most <= p.ts_bound))   ? kShort
                : !__any_sync(0xffffffffu, !(most <= p.tq_bound)) ? kPoly
                                                                  : kFar;
@@ -742,9 +753,9 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       // Whether chunk c holds scores that some row of the warp does not see.  They may be anything
       // and must not choose the form of the others, so such a chunk takes the one that holds for
       // all, and no form at all where no row sees any of it.  (bf16, softcap 50, 4 x 4,096 tokens
-      // and 256 x 128: 465 and 254 us; the form chosen by the scores that are seen, the others
+      // and 256 x 128: 475 and 257 us; the form chosen by the scores that are seen, the others
       // cleared, 525 and 276: the loops outgrow the instruction cache; kFar for every chunk of a
-      // tile with hidden scores 451 and 290.)
+      // tile with hidden scores 450 and 292.)
       auto partial = [&](int c) { return masked && __any_sync(0xffffffffu, rel - 32 * c < 31); };
       int mode = kPlain;
       float mx = SA_NEG_INF;
@@ -775,7 +786,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       }
       if (!kFixed) {
         float mt = SA_NEG_INF;
-        if (mx != SA_NEG_INF)
+        if (live && mx != SA_NEG_INF)
           mt = !kCap                        ? mx * lg.c2
                : masked || mode == kFar     ? tanh_far(mx * lg.k1) * lg.c2  // (mx: of any chunk)
                : mode == kPoly              ? poly_logit(mx, lg.tq)
@@ -814,7 +825,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
         if (kFixed) mode = mode_of(arrived(most));
         if (!kCap && masked) exp_chunk<kPlain, true, T>(x, pk, lg, neg_m, rc, ls);
         else if (!kCap) exp_chunk<kPlain, false, T>(x, pk, lg, neg_m, 0, ls);
-        else if (part && !__any_sync(0xffffffffu, rc >= 0)) {
+        else if (part && !__any_sync(0xffffffffu, live && rc >= 0)) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = 0u;
         } else if (part || mode == kFar) exp_chunk<kFar, true, T>(x, pk, lg, neg_m, part ? rc : kTile, ls);
@@ -988,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   // (Rows of a query tile that no head fills, where g does not divide 128, hold whatever the
-  // shared memory held: their scores are all masked.)
+  // shared memory held.)
   if (warp == 1) {
     tc05::tmem_alloc(tslot, G::kTmemCols);
     tc05::tmem_relinquish();
