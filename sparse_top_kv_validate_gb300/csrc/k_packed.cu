@@ -90,6 +90,10 @@ template <typename T>
 constexpr float fixed_offset_max_log2() {
   return std::is_same<T, __half>::value ? 14.0f : 97.0f;
 }
+// scale / softcap up to which a softcap does nothing: c tanh(s k1) = scale s to fp32's last
+// bit for |s| up to 2^-12 / k1 = 2.4e5
+constexpr float kNoCapMax = 1e-9f;
+constexpr float kFarMax = 67.0f;         // softcap up to which 2^-20 of it is a small error of a logit
 constexpr int kMaxSeqs = 1024;           // sequences per launch
 constexpr int kSmemLimit = 227 * 1024;
 
@@ -570,13 +574,16 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
 // How the log2-domain logit of a score s is formed: c_log2 s (no softcap), or
 // c_log2 tanh(k1 s) by the fitted polynomials (kShort, kPoly) or, where a score of the
 // warp lies outside their ranges or is hidden, from the hardware exponential and
-// reciprocal.
-enum ScoreMode { kPlain = 0, kShort = 1, kPoly = 2, kFar = 3 };
+// reciprocal (kFar: off by 2^-20 of the softcap).  Above a softcap of 67 that is too
+// much: there each score in the first polynomial's range takes that one (kEach; for
+// every softcap 257 -> 273 us at 256 prompts of 128 tokens).
+enum ScoreMode { kPlain = 0, kShort = 1, kPoly = 2, kFar = 3, kEach = 4 };
 
 // The constants of that: c2 = c_log2, k1 and the polynomials.
 struct Logits {
   float c2, k1;
   float tq[kTanhTerms], ts[kTanhShortTerms];
+  float ts_bound;
 };
 
 __device__ __forceinline__ float tanh_far(float x) {
@@ -655,11 +662,17 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&r)[32], uint32_t (&pk
     const float x0 = __uint_as_float(r[2 * i]), x1 = __uint_as_float(r[2 * i + 1]);
     uint64_t v;
     if (kMode == kPlain) v = f2_fma(f2_pack(x0, x1), c2x2, nm2);
-    else if (kMode == kFar) v = f2_fma(f2_pack(tanh_far(x0 * lg.k1), tanh_far(x1 * lg.k1)), c2x2, nm2);
+    else if (kMode == kFar || kMode == kEach) v = f2_fma(f2_pack(tanh_far(x0 * lg.k1), tanh_far(x1 * lg.k1)), c2x2, nm2);
     else if (kMode == kPoly) v = poly_logit2(f2_pack(x0, x1), lg.tq, nm2);
     else v = poly_logit2(f2_pack(x0, x1), lg.ts, nm2);
     float a, b;
     f2_unpack(v, a, b);
+    if (kMode == kEach) {
+      float n0, n1;
+      f2_unpack(poly_logit2(f2_pack(x0, x1), lg.ts, nm2), n0, n1);
+      if (fabsf(x0) <= lg.ts_bound) a = n0;
+      if (fabsf(x1) <= lg.ts_bound) b = n1;
+    }
     if (kMask) {
       if (2 * i > rel) a = SA_NEG_INF;
       if (2 * i + 1 > rel) b = SA_NEG_INF;
@@ -671,7 +684,8 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&r)[32], uint32_t (&pk
   }
 }
 
-enum Variant { kVarPlain = 0, kVarCapMax = 1, kVarCapFixed = 2 };
+// Without a softcap; with one and offsets; offset 0; a softcap above kFarMax, with offsets.
+enum Variant { kVarPlain = 0, kVarCapMax = 1, kVarCapFixed = 2, kVarCapLarge = 3 };
 
 // What a thread keeps of an item until its epilogue: the item, and the offset and
 // sum of the row over the warpgroup's own tiles.
@@ -686,6 +700,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
                              volatile int* abort_flag, volatile int* found) {
   using G = Geo<D>;
   constexpr bool kCap = kVariant != kVarPlain, kFixed = kVariant == kVarCapFixed;
+  constexpr int kAnyScore = kVariant == kVarCapLarge ? kEach : kFar;  // the form that holds for all
   constexpr int kOCols = D / 2;  // O columns that this warpgroup stores
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int wg = (warp - 4) >> 2;
@@ -698,6 +713,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
   Logits lg;
   lg.c2 = p.c_log2;
   lg.k1 = p.k1;
+  lg.ts_bound = p.ts_bound;
 #pragma unroll
   for (int i = 0; i < kTanhTerms; ++i) lg.tq[i] = p.tq[i];
 #pragma unroll
@@ -787,10 +803,9 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       if (!kFixed) {
         float mt = SA_NEG_INF;
         if (live && mx != SA_NEG_INF)
-          mt = !kCap                        ? mx * lg.c2
-               : masked || mode == kFar     ? tanh_far(mx * lg.k1) * lg.c2  // (mx: of any chunk)
-               : mode == kPoly              ? poly_logit(mx, lg.tq)
-                                            : poly_logit(mx, lg.ts);
+          mt = !kCap                       ? mx * lg.c2
+               : fabsf(mx) <= lg.ts_bound  ? poly_logit(mx, lg.ts)
+                                           : tanh_far(mx * lg.k1) * lg.c2;
         const bool up = mt > m + kRescaleLog2 || (m == SA_NEG_INF && mt > m);
         xch[(2 * wg + ((u >> 1) & 1)) * kTile] = up ? mt : m;
         __syncwarp();
@@ -828,7 +843,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
         else if (part && !__any_sync(0xffffffffu, live && rc >= 0)) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = 0u;
-        } else if (part || mode == kFar) exp_chunk<kFar, true, T>(x, pk, lg, neg_m, part ? rc : kTile, ls);
+        } else if (part || mode == kFar) exp_chunk<kAnyScore, true, T>(x, pk, lg, neg_m, part ? rc : kTile, ls);
         else if (mode == kPoly) exp_chunk<kPoly, false, T>(x, pk, lg, neg_m, 0, ls);
         else exp_chunk<kShort, false, T>(x, pk, lg, neg_m, 0, ls);
         tc05::tmem_st16(tS + c * 16, pk);
@@ -1098,18 +1113,19 @@ struct TanhFits {
 };
 
 // c_log2 tanh(k1 s) as a polynomial in s: coefficient k is c_log2 c_k k1^(2k + 1).
-// The largest |s| of the fit's range; -1, so that no score is in it, where a
-// coefficient leaves fp32's normal range (a scale very far from the softcap).
+// The largest |s| of the fit's range; less where a coefficient is below fp32's normal
+// range (a softcap far above the scale), as far as its rounding, 2^-149 |s|^(2k + 1),
+// stays below 1e-4; -1, so that no score is in it, where one leaves the range above.
 template <int N>
 float score_polynomial(const double (&c)[N], double bound, double softcap, double k1, float (&out)[N]) {
-  double f = softcap * 1.4426950408889634 * k1;
+  double f = softcap * 1.4426950408889634 * k1, most = bound / k1;
   bool ok = true;
   for (int k = 0; k < N; ++k) {
     out[k] = static_cast<float>(c[k] * f);
-    ok = ok && std::isnormal(out[k]);
+    ok = ok && std::isfinite(out[k]) && (k > 0 || std::isnormal(out[k]));
+    if (!std::isnormal(out[k])) most = std::fmin(most, std::pow(1e-4 * std::ldexp(1.0, 149), 1.0 / (2 * k + 1)));
     f *= k1 * k1;
   }
-  const double most = bound / k1;
   return ok && most < 1e18 ? static_cast<float>(most) : -1.0f;  // (s^2 is a finite fp32)
 }
 
@@ -1150,10 +1166,12 @@ int launch_t(const PackedArgs& a, cudaStream_t st) {
   p.causal = a.causal;
   const float log2e = 1.4426950408889634f;
   int variant = kVarPlain;
-  if (a.softcap != 0.0f) {
-    p.k1 = a.scale / a.softcap;
+  p.k1 = a.softcap != 0.0f ? a.scale / a.softcap : 0.0f;
+  if (p.k1 > kNoCapMax) {
     p.c_log2 = a.softcap * log2e;
-    variant = p.c_log2 <= fixed_offset_max_log2<T>() ? kVarCapFixed : kVarCapMax;
+    variant = p.c_log2 <= fixed_offset_max_log2<T>() ? kVarCapFixed
+              : a.softcap <= kFarMax                 ? kVarCapMax
+                                                     : kVarCapLarge;
     static const TanhFits fits;
     p.tq_bound = score_polynomial(fits.full, kTanhBound, a.softcap, p.k1, p.tq);
     p.ts_bound = score_polynomial(fits.brief, kTanhShortBound, a.softcap, p.k1, p.ts);
@@ -1162,9 +1180,12 @@ int launch_t(const PackedArgs& a, cudaStream_t st) {
   }
   const int sms = sm_count();
   if (sms <= 0) return -1;
-  auto kern = variant == kVarPlain    ? packed_tc05_kernel<D, T, kVarPlain>
-              : variant == kVarCapMax ? packed_tc05_kernel<D, T, kVarCapMax>
-                                      : packed_tc05_kernel<D, T, kVarCapFixed>;
+  // (in bf16 every softcap up to kFarMax has the offset 0)
+  constexpr Variant kSmallCap = std::is_same<T, __half>::value ? kVarCapMax : kVarCapLarge;
+  auto kern = variant == kVarPlain      ? packed_tc05_kernel<D, T, kVarPlain>
+              : variant == kVarCapFixed ? packed_tc05_kernel<D, T, kVarCapFixed>
+              : variant == kVarCapMax   ? packed_tc05_kernel<D, T, kSmallCap>
+                                        : packed_tc05_kernel<D, T, kVarCapLarge>;
   if (!allow_smem(reinterpret_cast<const void*>(kern))) return -1;
   for (int64_t b0 = 0; b0 < a.B; b0 += kMaxSeqs) {
     const int64_t seqs = a.B - b0 < kMaxSeqs ? a.B - b0 : kMaxSeqs;

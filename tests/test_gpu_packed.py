@@ -271,3 +271,14 @@ def test_rows_of_a_tile_without_a_head_do_not_count(cuda_lib, g, cap):
         for b in range(120):
             if b % period >= period // 2:
                 assert torch.equal(y[qs[b]:qs[b + 1]], clean[qs[b]:qs[b + 1]]), (period, b)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("cap", [100.0, 1e3, 1e4, 1e6, 1e8, 1e12])
+def test_a_softcap_far_above_the_scores(cuda_lib, dt, cap):
+    """The logits' error goes by the logits, not by the cap: scores of up to 12 in magnitude,
+    each off by 2^-18 of itself at the most, in tiles with hidden keys and in others."""
+    for D, nq, nk in ((128, [70, 1, 300], [70, 200, 700]), (64, [257], [257])):
+        q, k, v, qs, ks = make(dt, nq, nk, 4, 2, D, seed=int(math.log10(cap)))
+        y = cuda_lib.attn_prefill_packed(q.to(DEV), k.to(DEV), v.to(DEV), starts(qs), starts(ks), softcap=cap)
+        check_tail(y, q, k, v, qs, ks, True, cap, f"{dt} cap {cap} D {D}", tanh=2.0 ** -18 * 12 / cap)
