@@ -90,9 +90,6 @@ template <typename T>
 constexpr float fixed_offset_max_log2() {
   return std::is_same<T, __half>::value ? 14.0f : 97.0f;
 }
-// scale / softcap up to which a softcap does nothing: c tanh(s k1) = scale s to fp32's last
-// bit for |s| up to 2^-12 / k1 = 2.4e5
-constexpr float kNoCapMax = 1e-9f;
 constexpr float kFarMax = 67.0f;         // softcap up to which 2^-20 of it is a small error of a logit
 constexpr int kMaxSeqs = 1024;           // sequences per launch
 constexpr int kSmemLimit = 227 * 1024;

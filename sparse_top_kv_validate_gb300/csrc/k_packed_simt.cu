@@ -173,7 +173,7 @@ int launch_t(const PackedArgs& a, cudaStream_t st) {
   const int64_t tiles = (a.Tq + kRows - 1) / kRows + a.B;  // at least the sequences' own
   const size_t smem = ((kRows + 2 * kKeys) * (a.D + 4) + kRows * (kKeys + 1)) * sizeof(float);
   if (!allow_smem(reinterpret_cast<const void*>(packed_simt_kernel<T>), 96 * 1024)) return -1;
-  const float cap = a.softcap;
+  const float cap = fabsf(a.scale) > kNoCapMax * a.softcap ? a.softcap : 0.f;
   packed_simt_kernel<T><<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.Hq)), kThreads,
                           smem, st>>>(a, a.scale * log2e, cap != 0.f ? a.scale / cap : 0.f,
                                       cap * log2e);

@@ -6,6 +6,11 @@
 
 namespace sa {
 
+// |scale| / softcap up to which a softcap does nothing: with k1 that quotient,
+// softcap tanh(k1 s) = scale s to fp32's last bit for |s| up to 2^-12 / k1 = 2.4e5.
+// (softcap log2(e), which the kernels work with, leaves fp32 at the top of its range.)
+constexpr float kNoCapMax = 1e-9f;
+
 // Rows [first, first + n) of sequence b among `total`; starts that decrease or
 // leave the tensor are clipped (and reported by whoever checks them).
 struct Span {

@@ -282,3 +282,11 @@ def test_a_softcap_far_above_the_scores(cuda_lib, dt, cap):
         q, k, v, qs, ks = make(dt, nq, nk, 4, 2, D, seed=int(math.log10(cap)))
         y = cuda_lib.attn_prefill_packed(q.to(DEV), k.to(DEV), v.to(DEV), starts(qs), starts(ks), softcap=cap)
         check_tail(y, q, k, v, qs, ks, True, cap, f"{dt} cap {cap} D {D}", tanh=2.0 ** -18 * 12 / cap)
+
+
+@pytest.mark.parametrize("dt,scale", [("bf16", 0.1), ("f16", 0.1), ("f32", 0.1), ("f32", -0.1)])
+def test_the_largest_softcap_is_none(cuda_lib, dt, scale):
+    q, k, v, qs, _ = make(dt, [70, 200], [70, 200], 4, 2, 64)
+    run = lambda cap: cuda_lib.attn_prefill_packed(q.to(DEV), k.to(DEV), v.to(DEV), starts(qs), scale=scale, softcap=cap)  # noqa: E731
+    y = run(3.4e38)
+    assert torch.equal(y[:270], run(0.0)[:270]) and torch.isfinite(y[:270].float()).all()
