@@ -591,8 +591,13 @@ int attn_prefill(const sa_prefill_params* p, void* stream);
  * as for sparse_attn_decode.
  * pool_format SA_FP8_E4M3_PAGE: quantised pages (q and y SA_F16 or SA_BF16, D
  * 64 / 128 / 256, page_tokens a multiple of 16, B <= 4096, q, y and pools 16-byte
- * aligned, options 0); k_new / v_new are quantised as paged_kv_write does.  The codes' values
- * enter the products exactly and the scales in fp32.
+ * aligned, options 0); k_new / v_new are quantised as paged_kv_write does.  The codes'
+ * values enter the products exactly and the K scales in fp32; a row's weight, its
+ * probability times its V scale, is held to 2^-22 of itself or 2^-31 of the largest
+ * weight of a row that is not zero, whichever is more (V beyond 2^118 in magnitude
+ * may overflow the fp32 sums).  B * Hkv (times the parts that a
+ * group of more than 16 heads, 8 for D 256, is cut into) * (max_pages * page_tokens /
+ * 16 + 2) has to stay below 2^31 - 2^20.
  */
 typedef struct {
   const void* q;
@@ -635,8 +640,9 @@ int paged_attn_decode(const sa_paged_params* p, void* stream);
  * and (u, v) becomes mscale * (u cos - v sin, u sin + v cos).  The pair is
  * dims (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved; dims from
  * rotary_dim on pass unchanged.  The table keeps f_i as a 64-bit fraction of a
- * turn, so position * f_i modulo one turn is exact integer arithmetic at any
- * position (int32 or int64, negative ones too).
+ * turn, so position times that fraction modulo one turn is exact integer arithmetic
+ * (int32 or int64 positions, negative ones too); the fraction is f_i rounded to a
+ * double, about 2^-53 of itself, an error that grows with the position.
  * rotary_dim: even, 2 .. 256.  mscale 0 means 1.  Returns SA_OK, SA_ERR_NULL,
  * SA_ERR_SHAPE (a size or a parameter out of its range: base <= 0, factor <= 0,
  * ramp_high <= ramp_low, original_len <= 0 where it is used, a frequency that
@@ -671,8 +677,8 @@ int sa_rope_table(const sa_rope_config* c, sa_rope* out);
  * s of batch b at positions[b * pos_stride + s] (pos_stride 0: one row of S
  * positions for every batch).  q_out / k_out may be the input itself (same
  * pointer and strides); any other overlap is SA_ERR_OVERLAP.  dtype SA_F32,
- * SA_F16 or SA_BF16; angles are reduced exactly, cos and sin and the rotation
- * are fp32, rounded once.  S 0 is a call that does nothing; B * S of 2^31 - 256 and
+ * SA_F16 or SA_BF16; the reduced angle is rounded to fp32 (2^-25 of a half turn),
+ * cos and sin and the rotation are fp32, rounded once.  S 0 is a call that does nothing; B * S of 2^31 - 256 and
  * more is SA_ERR_UNSUPPORTED.
  */
 typedef struct {
@@ -750,7 +756,9 @@ int paged_kv_read(const sa_kv_pages_params* p, void* stream);
  * a chunk of a prompt sees the context before it), every key otherwise; a
  * query that sees no key gives 0.  softcap as in attn_prefill, scale 0 means
  * 1/sqrt(D).  Rows of y behind the last sequence stay as they are; rows of q,
- * k and v outside the sequences may hold anything.
+ * k and v outside the sequences may hold anything.  Scores, row sums and outputs are
+ * summed in fp32; SA_F16 and SA_BF16 on the tensor cores round each probability to
+ * that type before its product with v.
  * dtype SA_F16 / SA_BF16 with D 64 or 128, a positive scale, Hq / Hkv <= 128
  * and 16-byte aligned pointers and strides run on the tcgen05 tensor cores;
  * other shapes (SA_F32, D a multiple of 4 up to 256) take a kernel on the fp32

@@ -37,7 +37,7 @@
 //    rescales O in tensor memory, after the previous PV.  With a softcap that bounds
 //    2^logit to the normal numbers of P's type (up to 67 in bf16, 9.7 in f16) the
 //    offset is 0 and nothing is posted (softcap 50: bf16 475 us, f16, with an
-//    offset, 626).
+//    offset, 618).
 //  * P enters the second product in q's type, as the MMA takes it: each probability
 //    is off by up to half a step of it (2^-8 bf16, 2^-11 f16 of itself; in f16 also
 //    by 2^-25 of the row's largest), while the row's sum adds them in fp32.  Against

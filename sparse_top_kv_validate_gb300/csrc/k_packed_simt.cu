@@ -6,8 +6,10 @@
 // the query's sequence.  A block takes 16 queries of one head and walks over
 // the keys in tiles of 32 held in shared memory as fp32; eight lanes share a
 // query: four scores each, then D / 8 output dims each, with a running maximum
-// and sum.  Bound by the fp32 pipes and shared-memory reads: 16,384 tokens of 8
-// prompts, 32 / 8 heads of 128, 34.5 ms (12 TFLOP/s; the tensor-core kernel 0.35 ms).
+// and sum.  Bound by shared-memory reads (five of 16 bytes to 16 FMAs): 8 prompts of
+// 2,048 tokens, 32 / 8 heads of 128, fp32, 22.6 ms (12 TFLOP/s; the tensor-core kernel
+// takes 0.27 ms for the same in 16 bits); bf16, heads of 96 and 80 19.1 and 17.4 ms, of
+// 256 72 ms (8 TFLOP/s).
 #include "packed.cuh"
 #include "serving.h"
 

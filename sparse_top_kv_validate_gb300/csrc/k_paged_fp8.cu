@@ -44,10 +44,12 @@
 //    units per warp, are bound by these changes.
 //
 // Measured (8 KV heads of 128, pages of 16 or 32; 6.80 TB/s copy): 128 sequences of
-// 1,024 to 32,768 tokens, 4.5 GB, 717 us, 92% of the copy bandwidth; one context of
-// 131,072 among 23 of some hundred, 290 MB, 68 us (63%; about 20 us are launch, tile
-// space, the rings' first fill and the merges); one sequence of 1,500, 15.3 us,
-// latency.  Twelve warps per CTA with three stages; with the earlier partition (727
+// 1,024 to 32,768 tokens, 4.5 GB, 724 us, 91% of the copy bandwidth; one context of
+// 131,072 among 23 of some hundred, 290 MB, 70 us (61%; about 20 us are launch, tile
+// space, the rings' first fill and the merges); one sequence of 1,500, 15.6 us,
+// latency.  64 sequences of 8,192 tokens: 8 heads of 128, groups of 4, 190 us, of 16,
+// 275 (two MMA columns to a tile); heads of 64, 138 and 170; 8 heads of 256, groups of 4
+// and 8, 357 and 367; 4 of 256, groups of 16, 364 (cut in two, every page read twice).  Twelve warps per CTA with three stages; with the earlier partition (727
 // and 90 us) sixteen with two took 800 and 85 us, ten with four 848 and 95.
 #include "gather_common.cuh"
 #include "serving.h"
@@ -109,7 +111,7 @@ __device__ __forceinline__ float e8m0_f32(uint32_t byte) {
 // Ranges are cut in a space that gives every unit kFp8UnitCost places before its
 // tiles, for what a warp does at a change of unit: tile i of a unit at `place` lies
 // at place + kFp8UnitCost + i, and a warp takes the tiles of its R places.  (One
-// context of 131,072 among 23 short ones: 68 us, 79 with a cost of 0; 400 contexts of
+// context of 131,072 among 23 short ones: 70 us, 79 with a cost of 0; 400 contexts of
 // 350: 73.4, 72.6 with 0, 75.9 with 8.)
 __device__ __forceinline__ int32_t unit_place(const GatherArgs& a, int32_t seq_tiles_before, int32_t b, int32_t grp,
                                               int32_t tu) {
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
   int64_t R = (total + gw_total - 1) / gw_total;
   int nw = NW;  // warps that get a range
   if (R < min_range) {
-    // few tiles: more CTAs with fewer warps each (one context of 1,500: 15.3 us, with
+    // few tiles: more CTAs with fewer warps each (one context of 1,500: 15.6 us, with
     // all twelve 16.5, with four 15.8)
     R = min_range;
     nw = static_cast<int>(min(static_cast<int64_t>(NW), max((total + gridDim.x * R - 1) / (gridDim.x * R), int64_t(kMinWarps))));

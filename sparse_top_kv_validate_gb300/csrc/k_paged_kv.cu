@@ -19,6 +19,8 @@
 // fractions by ordinary loads, -> 24.7; rows in flight in shared memory instead of
 // registers (four blocks to an SM instead of two), keys and values in loops of
 // their own, packed fp32 pairs, 50 -> 31.  A decode step's 128 rows take 6.2 us.
+// Pages of plain elements, 65,536 rows: write 83 us (bf16, 537 MB, 6.5 TB/s; rotated
+// 84; fp32 223, 4.8 TB/s), read-back, a warp per row, 255 us (2.1 TB/s; fp32 263).
 #include <type_traits>
 
 #include "rope.cuh"

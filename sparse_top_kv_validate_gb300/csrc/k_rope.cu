@@ -15,7 +15,10 @@
 // Measured, 4 x 4,096 tokens, 32 + 8 heads of 128, half of each rotated, fp16,
 // head-major (335 MB): 55 us, 6.1 TB/s, 89% of the copy bandwidth; with four rows
 // loaded to registers and a lane's pieces side by side (half-filled sectors per
-// access) 71 us.  A decode step (128 tokens) takes 6.2 us, a launch's latency.
+// access) 71 us.  fp32, whole heads rotated (671 MB): 147 us, 4.6 TB/s.  Heads of 96,
+// half rotated (252 MB), 54 us; heads of 80, 40 or 20 dims rotated, take the kernel for
+// any size, a pair per lane and 2-byte accesses: 127 and 152 us for 210 MB.  A decode
+// step (128 tokens) takes 6.2 us, a launch's latency.
 #include "rope.cuh"
 #include "serving.h"
 

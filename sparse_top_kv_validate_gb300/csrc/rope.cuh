@@ -1,5 +1,5 @@
-// rope.cuh -- rotary positions: exact angle reduction and the rotation of a
-// 16-element chunk, shared by the rotary and the page-write kernels.
+// rope.cuh -- rotary positions: angle reduction and the rotation of a 16-element
+// chunk, shared by the rotary and the page-write kernels.
 #pragma once
 
 #include "common.cuh"
@@ -7,10 +7,12 @@
 namespace sa {
 
 // cos and sin (times m) of position * f, f given as a 64-bit fraction of a
-// turn: the product modulo 2^64 is the fraction of a turn of the angle, exact
-// at any position; its top 32 bits as a signed number of half turns go through
-// sincospi.  (An fp32 product position * f has lost every fraction bit of the
-// angle by position 2^24; this one keeps 32 of them.)
+// turn: the product modulo 2^64 is the fraction of a turn of the angle, exact for
+// the fraction given; its top 32 bits, as a signed number of half turns rounded to
+// fp32 (24 bits: off by at most 2^-25 of a half turn), go through sincospi.  (An
+// fp32 product position * f has lost every fraction bit of the angle by position
+// 2^24.)  The fraction itself comes from a double: the frequency is off by up to
+// about 2^-53 of itself, and the angle by that many times as far as it turned.
 __device__ __forceinline__ float2 rope_cos_sin(int64_t pos, uint64_t turns, float m) {
   const uint64_t phase = static_cast<uint64_t>(pos) * turns;
   const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
