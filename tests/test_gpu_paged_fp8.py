@@ -378,3 +378,27 @@ def test_two_threads_on_one_stream(cuda_lib):
         t.join()
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[i]) for i in range(4) for y in got[i])
+
+
+@pytest.mark.parametrize("D,g", [(64, 16), (128, 16), (256, 8), (256, 16), (128, 3)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_the_same_for_every_form_of_the_kernel(cuda_lib, D, g, zeros):
+    """Falling value scales under rising scores, or rows of zeros with most of the probability,
+    for both numbers of MMA columns and every head size."""
+    n, Hkv, B, dt = 192, 2, 300, "bf16"
+    gen = torch.Generator().manual_seed(D + g)
+    q = (torch.rand(B, Hkv * g, 1, D, generator=gen) + 0.5).to(DT[dt])
+    t = (torch.arange(n) > n // 5).double()
+    rise, drop = (12, 20) if zeros else (40, 26)
+    k = 0.05 * torch.randn(n, Hkv, D, generator=gen).double() + (t * rise * math.log(2) / math.sqrt(D))[:, None, None]
+    v = torch.randn(n, Hkv, D, generator=gen).double() * (2.0 ** -drop if zeros else torch.exp2(-drop * t)[:, None, None])
+    if zeros:
+        v[n // 2:] = 0
+    pools, table, ctx, vals, weight = shared_context(n, 16, Hkv, D, k, v, B)
+    if zeros:
+        weight[n // 2:] = weight.min()
+    y = cuda_lib.paged_attn_decode(q.to(DEV), *pools, table, ctx)
+    for b in (0, 1, 150, 299):
+        for h in range(Hkv):
+            bound_check(y[b, h * g:(h + 1) * g, 0], q[b, h * g:(h + 1) * g, 0].double(), vals[0][:, h], vals[1][:, h],
+                        weight[:, h], 1 / math.sqrt(D), f"D {D} group {g} zeros {zeros}: {b} {h}")
