@@ -1,7 +1,7 @@
 /*
  * sa.h -- C ABI of the GB300 KV-cache attention library (libsa.so).
  *
- * Twelve operations, all computed on the GPU on the caller's stream:
+ * Sixteen operations, all computed on the GPU on the caller's stream:
  *
  *   validate_indices     index-row validation with a device error word
  *   build_present_kv     present K/V = past ++ current (concat or in-place append)
@@ -12,6 +12,10 @@
  *   paged_kv_write       new tokens' K/V, rotated and quantised, into their pages
  *   paged_kv_read        a context read back from its pages into packed rows
  *   attn_prefill_packed  causal prefill of packed sequences of different lengths
+ *   attn_weights_packed  the attention weight that each key receives from packed queries
+ *   paged_attn_decode_weights  the paged decode, its attention weights accumulated
+ *   paged_kv_select      the tokens that each head keeps of a context over its budget
+ *   paged_kv_compact     the kept rows moved to the front of their pages, in place
  *   sparse_index_select  ratio-4 index scoring + top-k (produces selected indices)
  *   csa_ratio4_attention compressed sparse attention: window store + records + sink
  *   csa_*_compress       the compression stages that produce the CSA records
@@ -781,6 +785,128 @@ typedef struct {
   float softcap;
 } sa_packed_params;
 int attn_prefill_packed(const sa_packed_params* p, void* stream);
+
+/*
+ * Cache eviction -- the operators that keep a paged cache within a budget of tokens
+ * by the attention that its tokens receive.
+ *
+ * A weights pool is float32 [num_pages, Hkv, page_tokens], addressed like the pages of
+ * K and V: the accumulated weight of token t of sequence b and KV head h lies at page
+ * block_table[b * max_pages + t / page_tokens], head h, slot t % page_tokens.  A token's
+ * weight is the sum of the softmax probabilities that the queries of the KV head's
+ * group give it.  Two calls accumulate it.  Both SET the weights of the tokens that
+ * are new with them (so that a page that changes hands needs no clearing) and ADD to
+ * the others'.  A page that two sequences of one call share receives the weights of
+ * both, in no order.  Sums and softmax statistics are fp32.
+ *
+ * After a compaction a token's place in its pages is no longer its position: rotate
+ * with rotary_embed and the true positions, and write with paged_kv_write without a rope.
+ */
+
+/*
+ * attn_weights_packed -- the weights that packed queries give the keys of their
+ * sequences: q [Tq, Hq, D], k [Tk, Hkv, D] (GQA), starts and strides as for
+ * attn_prefill_packed, causal: with nq queries and nk keys, query i sees the keys
+ * j <= i + nk - nq.  For sequence b and KV head h
+ *   w_j = sum over the queries i and the heads of h's group of
+ *         softmax_j(scale q_i . k_j)        (a query that sees no key gives nothing)
+ * and the weight of token j is set to w_j where j >= nk - nq (the queries' own tokens) or
+ * accumulate is 0, else w_j is added to it.  All queries of a prompt, a chunk's, or
+ * the last few of a context may be given.  Sequences without queries or keys, and
+ * slots that hold no token, are left as they are.
+ * scale 0 means 1/sqrt(D).  dtype SA_F16 / SA_BF16 with D 64 or 128, a positive scale,
+ * Hq / Hkv <= 128 and 16-byte aligned pointers and strides run on the tcgen05 tensor
+ * cores; other shapes (SA_F32, D a multiple of 4 up to 256) take a kernel on the fp32
+ * pipes.  Malformed starts set SA_ERRBIT_SEQ (err_word nullable) and nothing is
+ * written; a table entry outside [0, num_pages), or a token past max_pages *
+ * page_tokens, sets SA_ERRBIT_PAGE and that token is skipped.  Workspace:
+ * attn_weights_packed_workspace(p) bytes, 256-byte aligned, contents on entry
+ * irrelevant (the rows' statistics and the partial sums of tiles cut between CTAs).
+ * Deterministic, but for shared pages.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  float* weights;
+  const int32_t* block_table; /* [B, max_pages] */
+  const int32_t* q_start;     /* [B + 1] */
+  const int32_t* k_start;     /* [B + 1]; NULL: q_start */
+  uint32_t* err_word;
+  int32_t dtype;
+  int32_t accumulate;
+  int64_t B, Tq, Tk, Hq, Hkv, D, page_tokens, max_pages, num_pages;
+  int64_t q_strides[2], k_strides[2]; /* token, head */
+  float scale;
+  int32_t reserved_;          /* must be 0 */
+  void* workspace;
+  size_t workspace_bytes;
+} sa_weights_params;
+
+size_t attn_weights_packed_workspace(const sa_weights_params* p);
+int attn_weights_packed(const sa_weights_params* p, void* stream);
+
+/*
+ * paged_attn_decode_weights -- paged_attn_decode (the same y) that also accumulates
+ * the weights of its queries: of token t < ctx_len[b] - 1 added, of the new token,
+ * ctx_len[b] - 1, set.  weights: the pool, with p's num_pages, Hkv and page_tokens; it
+ * must overlap nothing else of the call.  options must be 0.  Workspace:
+ * paged_attn_decode_weights_workspace(p) bytes: paged_attn_decode's, and the scores,
+ * B * Hq * max_pages * page_tokens floats (at most 2^40).
+ */
+size_t paged_attn_decode_weights_workspace(const sa_paged_params* p);
+int paged_attn_decode_weights(const sa_paged_params* p, float* weights, void* stream);
+
+/*
+ * paged_kv_select -- the tokens that each KV head keeps.  For sequence b with
+ * n = ctx_len[b] tokens and KV head h: all of them when n <= budget, else exactly
+ * `budget`: the first `sink`, the last `recent`, and of those between them the
+ * budget - sink - recent with the largest weights (ties: the lower token; NaN counts
+ * as -inf).  keep: int32 [B, Hkv, budget], ascending, -1 behind the last: an index row as
+ * sparse_attn_decode and paged_kv_compact take it.  new_len (nullable int32 [B], not
+ * ctx_len itself): min(n, budget).  A ctx_len outside [0, max_pages * page_tokens] sets
+ * SA_ERRBIT_PAGE (err_word nullable) and counts as 0; the weight behind a table entry
+ * outside [0, num_pages) counts as -inf and sets it too.  sink + recent <= budget;
+ * max_pages * page_tokens below 2^31 - 2^17.  Exact; no workspace.
+ */
+typedef struct {
+  const float* weights;
+  const int32_t* block_table;
+  const int32_t* ctx_len;
+  int32_t* keep;
+  int32_t* new_len;
+  uint32_t* err_word;
+  int64_t B, Hkv, page_tokens, max_pages, num_pages;
+  int64_t budget, sink, recent;
+} sa_select_params;
+int paged_kv_select(const sa_select_params* p, void* stream);
+
+/*
+ * paged_kv_compact -- moves the kept rows to the front of their sequence's pages, in
+ * place: for every sequence b, KV head h and i < m, with m the entries of keep[b, h, :]
+ * before its first -1, token i's row of K, row of V and weight (weights nullable)
+ * become those of token keep[b, h, i].  Bit for bit; FP8 rows move with their scale
+ * bytes.  Tokens from m on keep what they held.  keep: int32 [B, Hkv, width], each row
+ * strictly increasing from 0 on, below ctx_len[b] (the length before), -1 behind;
+ * a row that is not stays as it is and ORs its SA_IDX_* codes into err_word (nullable).
+ * A ctx_len outside [0, max_pages * page_tokens], or a table entry outside
+ * [0, num_pages) that a moved row names, sets SA_ERRBIT_PAGE; such rows stay.  The pages of
+ * a sequence must be its own: a page shared with another sequence of the call, or
+ * named twice, ends up with rows of either.  pool_format and D as for
+ * paged_kv_write.  No workspace.
+ */
+typedef struct {
+  void* k_pool;
+  void* v_pool;
+  float* weights;
+  const int32_t* block_table;
+  const int32_t* ctx_len;
+  const int32_t* keep;
+  uint32_t* err_word;
+  int32_t dtype;              /* of pages of plain elements */
+  int32_t pool_format;
+  int64_t B, Hkv, D, page_tokens, max_pages, num_pages, width;
+} sa_compact_params;
+int paged_kv_compact(const sa_compact_params* p, void* stream);
 
 #ifdef __cplusplus
 }

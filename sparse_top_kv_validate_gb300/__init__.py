@@ -10,7 +10,9 @@ Entry points (same names as the C ABI):
     validate_indices, build_present_kv, sparse_attn_decode, attn_prefill,
     paged_attn_decode, sparse_index_select, csa_ratio4_attention,
     csa_ratio128_compress, csa_ratio4_main_compress, csa_ratio4_index_compress,
-    csa_pool_weight, rotary_embed, paged_kv_write, paged_kv_read, attn_prefill_packed
+    csa_pool_weight, rotary_embed, paged_kv_write, paged_kv_read, attn_prefill_packed,
+    attn_weights_packed, paged_attn_decode_weights (paged_attn_decode with weights),
+    paged_kv_select, paged_kv_compact
 """
 from __future__ import annotations
 
@@ -40,6 +42,8 @@ __all__ = [
     "RopeTable", "rope_table", "RotaryParams", "rotary_embed", "KvPagesParams", "paged_kv_write",
     "paged_kv_read", "new_fp8_pool", "PackedParams", "attn_prefill_packed", "FP8_E4M3_PAGE",
     "ERRBIT_SEQ", "ERRBIT_NONFINITE",
+    "WeightsParams", "attn_weights_packed", "new_weight_pool", "SelectParams", "paged_kv_select",
+    "CompactParams", "paged_kv_compact", "paged_attn_decode_weights_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -182,12 +186,43 @@ class PackedParams(C.Structure):
     ]
 
 
+class WeightsParams(C.Structure):
+    _fields_ = [
+        ("q", _p), ("k", _p), ("weights", _p), ("block_table", _p), ("q_start", _p),
+        ("k_start", _p), ("err_word", _p), ("dtype", _i32), ("accumulate", _i32),
+        ("B", _i64), ("Tq", _i64), ("Tk", _i64), ("Hq", _i64), ("Hkv", _i64), ("D", _i64),
+        ("page_tokens", _i64), ("max_pages", _i64), ("num_pages", _i64),
+        ("q_strides", _i64 * 2), ("k_strides", _i64 * 2), ("scale", C.c_float),
+        ("reserved_", _i32), ("workspace", _p), ("workspace_bytes", C.c_size_t),
+    ]
+
+
+class SelectParams(C.Structure):
+    _fields_ = [
+        ("weights", _p), ("block_table", _p), ("ctx_len", _p), ("keep", _p), ("new_len", _p),
+        ("err_word", _p), ("B", _i64), ("Hkv", _i64), ("page_tokens", _i64), ("max_pages", _i64),
+        ("num_pages", _i64), ("budget", _i64), ("sink", _i64), ("recent", _i64),
+    ]
+
+
+class CompactParams(C.Structure):
+    _fields_ = [
+        ("k_pool", _p), ("v_pool", _p), ("weights", _p), ("block_table", _p), ("ctx_len", _p),
+        ("keep", _p), ("err_word", _p), ("dtype", _i32), ("pool_format", _i32),
+        ("B", _i64), ("Hkv", _i64), ("D", _i64), ("page_tokens", _i64), ("max_pages", _i64),
+        ("num_pages", _i64), ("width", _i64),
+    ]
+
+
 # The serving-step calls pack their parameters as bytes of the structures above (filling
 # a ctypes structure field by field takes as long as the launch).
 _ROTARY = struct.Struct("6P2i18q")
 _KV_PAGES = struct.Struct("9P2i11q")
 _PACKED = struct.Struct("7P2i14q2f")
 _PAGED = struct.Struct("8PiI7qfi2PN")
+_WEIGHTS = struct.Struct("7P2i13qfiPN")
+_SELECT = struct.Struct("6P8q")
+_COMPACT = struct.Struct("7P2i7q")
 
 
 class SAError(RuntimeError):
@@ -263,7 +298,10 @@ def load():
         L.sa_rope_table.argtypes = [C.POINTER(_RopeConfig), C.POINTER(RopeTable)]
         for name, params in (("paged_attn_decode", PagedParams), ("rotary_embed", RotaryParams),
                              ("paged_kv_write", KvPagesParams), ("paged_kv_read", KvPagesParams),
-                             ("attn_prefill_packed", PackedParams)):
+                             ("attn_prefill_packed", PackedParams),
+                             ("attn_weights_packed", WeightsParams),
+                             ("paged_kv_select", SelectParams),
+                             ("paged_kv_compact", CompactParams)):
             fn = getattr(L, name)
             fn.restype = C.c_int
             fn.argtypes = [C.POINTER(params), _p]
@@ -272,6 +310,15 @@ def load():
             raw.restype = C.c_int
             raw.argtypes = [C.c_char_p, _p]
             setattr(L, name + "_bytes", raw)
+        L.paged_attn_decode_weights.restype = C.c_int
+        L.paged_attn_decode_weights.argtypes = [C.POINTER(PagedParams), _p, _p]
+        raw = L["paged_attn_decode_weights"]
+        raw.restype, raw.argtypes = C.c_int, [C.c_char_p, _p, _p]
+        L.paged_attn_decode_weights_bytes = raw
+        L.paged_attn_decode_weights_workspace.restype = C.c_size_t
+        L.paged_attn_decode_weights_workspace.argtypes = [C.POINTER(PagedParams)]
+        L.attn_weights_packed_workspace.restype = C.c_size_t
+        L.attn_weights_packed_workspace.argtypes = [C.POINTER(WeightsParams)]
         _lib = L
         return _lib
 
@@ -587,15 +634,24 @@ def paged_attn_decode_workspace(q, k_pool, v_pool, block_table, ctx_len, scale=0
     return int(load().paged_attn_decode_workspace(C.byref(p)))
 
 
+def paged_attn_decode_weights_workspace(q, k_pool, v_pool, block_table, ctx_len, scale=0.0) -> int:
+    p = _paged_params(q, k_pool, v_pool, block_table, ctx_len, None, None, None, scale, None)
+    return int(load().paged_attn_decode_weights_workspace(C.byref(p)))
+
+
 def paged_attn_decode(q, k_pool, v_pool, block_table, ctx_len, *, k_new=None, v_new=None,
                       scale=0.0, err_word=None, y=None, workspace=None, stream=None,
-                      options=0):
+                      options=0, weights=None):
     """Paged causal decode: ``q [B,Hq,1,D]`` (or ``[B,Hq,D]``), pools
     ``[num_pages,Hkv,page_tokens,D]`` of q's dtype, or FP8 pools (uint8
     ``[num_pages,Hkv,page_tokens*(D+1)]``, see ``new_fp8_pool``; q float16 or
     bfloat16), ``block_table int32 [B,max_pages]``, ``ctx_len int32 [B]``;
     optional ``k_new/v_new [B,Hkv,D]`` written (quantised for FP8 pools) at
-    token ``ctx_len-1`` first.  Returns ``y`` shaped like ``q``."""
+    token ``ctx_len-1`` first.  Returns ``y`` shaped like ``q``.
+
+    ``weights`` (float32 ``[num_pages,Hkv,page_tokens]``, ``new_weight_pool``): the attention
+    weight that each token receives, summed over the heads of its KV head's group, is added to
+    its entry, and set for the new token ``ctx_len-1``."""
     L = load()
     for n, t in (("q", q), ("k_pool", k_pool), ("v_pool", v_pool), ("block_table", block_table),
                  ("ctx_len", ctx_len), ("k_new", k_new), ("v_new", v_new),
@@ -603,6 +659,9 @@ def paged_attn_decode(q, k_pool, v_pool, block_table, ctx_len, *, k_new=None, v_
         _dev(t, n)
     if block_table.dtype != torch.int32 or ctx_len.dtype != torch.int32:
         raise TypeError("block_table and ctx_len must be int32")
+    if weights is not None:
+        return _paged_decode_weights(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new,
+                                     scale, err_word, y, workspace, stream, options, weights)
     if k_pool.dtype == torch.uint8:
         return _paged_fp8_decode(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, scale,
                                  err_word, y, workspace, stream, options)
@@ -617,8 +676,8 @@ def paged_attn_decode(q, k_pool, v_pool, block_table, ctx_len, *, k_new=None, v_
     return y
 
 
-def _paged_fp8_decode(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, scale, err_word,
-                      y, workspace, stream, options):
+def _paged_decode_device(q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, err_word, y):
+    """The device of a paged decode whose shapes fit."""
     shape, pool = q.shape, k_pool.shape
     B, D, Hkv = shape[0], shape[-1], pool[1]
     if not (len(shape) == 3 or (len(shape) == 4 and shape[2] == 1)):
@@ -630,6 +689,61 @@ def _paged_fp8_decode(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, 
             raise ValueError(f"{n} must be [B, Hkv, D] of q's dtype")
     if y is not None and (_dev(y, "y").dtype != q.dtype or y.shape != shape):
         raise ValueError("y must be shaped and typed like q")
+    return device
+
+
+def _paged_decode_weights(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, scale, err_word,
+                          y, workspace, stream, options, weights):
+    device = _paged_decode_device(q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, err_word, y)
+    shape, pool = q.shape, k_pool.shape
+    B, D, Hkv = shape[0], shape[-1], pool[1]
+    if k_pool.dtype == torch.uint8:
+        fmt, page_tokens = FP8_E4M3_PAGE, _fp8_page_tokens(k_pool, v_pool, D)
+    else:
+        if len(pool) != 4 or v_pool.shape != pool or k_pool.dtype != q.dtype or \
+                v_pool.dtype != q.dtype or pool[3] != D:
+            raise ValueError("pools must be [num_pages, Hkv, page_tokens, D] of q's dtype, or FP8 "
+                             "pools")
+        fmt, page_tokens = 0, pool[2]
+    _weight_pool(weights, pool[0], Hkv, page_tokens, device)
+    dtype = _dt(q)
+    with _launching(device, stream) as s:
+        if y is None:
+            y = torch.empty_like(q)
+
+        def params(ws, nbytes):
+            return _PAGED.pack(
+                q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _addr(k_new), _addr(v_new),
+                block_table.data_ptr(), ctx_len.data_ptr(), y.data_ptr(), dtype, options, B,
+                shape[1], Hkv, D, page_tokens, block_table.shape[1], pool[0], scale, fmt,
+                _addr(err_word), ws, nbytes)
+
+        _call_with_workspace(
+            "paged_attn_decode_weights", params, device, s, workspace,
+            lambda p: L.paged_attn_decode_weights_bytes(p, weights.data_ptr(), s),
+            lambda p: L.paged_attn_decode_weights_workspace(C.byref(PagedParams.from_buffer_copy(p))))
+    return y
+
+
+def _call_with_workspace(name, params, device, s, workspace, call, size):
+    """Run ``call`` on parameters with the given workspace, the kept one, or one of ``size``."""
+    if workspace is None:
+        # the kept scratch is nearly always large enough: ask only when it is not
+        ws = _kept_workspace(device, s)
+        if ws is not None:
+            rc = call(params(ws.data_ptr(), ws.numel()))
+            if rc != ERR_WORKSPACE:
+                _check(name, rc)
+                return
+    ws, nb = _stream_workspace(int(size(params(0, 0))), device, s, workspace)
+    _check(name, call(params(_addr(ws), nb)))
+
+
+def _paged_fp8_decode(L, q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, scale, err_word,
+                      y, workspace, stream, options):
+    device = _paged_decode_device(q, k_pool, v_pool, block_table, ctx_len, k_new, v_new, err_word, y)
+    shape, pool = q.shape, k_pool.shape
+    B, D, Hkv = shape[0], shape[-1], pool[1]
     page_tokens, dtype = _fp8_page_tokens(k_pool, v_pool, D), _dt(q)
     with _launching(device, stream) as s:
         if y is None:
@@ -1230,3 +1344,156 @@ def attn_prefill_packed(q, k, v, q_start, k_start=None, *, causal=True, scale=0.
             qst[0], qst[1], kst[0], kst[1], vst[0], vst[1], yst[0], yst[1], scale, softcap)
         _check("attn_prefill_packed", L.attn_prefill_packed_bytes(p, s))
     return y
+
+
+# ---- cache eviction by accumulated attention weight -------------------------------------------
+
+def new_weight_pool(num_pages: int, Hkv: int, page_tokens: int, device="cuda") -> torch.Tensor:
+    """A pool of attention weights, zeroed: float32 ``[num_pages, Hkv, page_tokens]``, addressed
+    like the pages of K and V."""
+    return torch.zeros((num_pages, Hkv, page_tokens), dtype=torch.float32, device=device)
+
+
+def _weight_pool(weights, num_pages, Hkv, page_tokens, device):
+    _dev(weights, "weights")
+    if weights.dtype != torch.float32:
+        raise TypeError("weights must be float32")
+    if tuple(weights.shape) != (num_pages, Hkv, page_tokens):
+        raise ValueError(f"weights must be [{num_pages}, {Hkv}, {page_tokens}]")
+    if weights.device != device:
+        raise ValueError(f"weights are on {weights.device}, not on {device}")
+
+
+def attn_weights_packed(q, k, weights, block_table, q_start, k_start=None, *, scale=0.0,
+                        accumulate=True, err_word=None, workspace=None, stream=None):
+    """The attention weight that each key receives from packed queries, into a weights pool.
+
+    ``q [Tq, Hq, D]``, ``k [Tk, Hkv, D]`` and the starts as for ``attn_prefill_packed`` (causal: a
+    sequence's queries are the last tokens of its keys).  Token j's weight in head h of
+    ``weights`` (float32 ``[num_pages, Hkv, page_tokens]``, through ``block_table`` int32
+    ``[B, max_pages]``) becomes the sum of the probabilities that the queries of the head's group
+    give it: set for the queries' own tokens, added to the others', or set for all with
+    ``accumulate=False``.  Returns ``weights``."""
+    L = load()
+    qs, qst = _rows(q, "q")
+    ks, kst = _rows(k, "k", q.dtype)
+    Tq, Hq, D = qs
+    Tk, Hkv, _ = ks
+    if ks[2] != D:
+        raise ValueError("q and k must have the same head size")
+    _int32(q_start, "q_start")
+    B = q_start.numel() - 1
+    if k_start is not None:
+        _int32(k_start, "k_start", B + 1)
+    elif Tk != Tq:
+        raise ValueError("k_start is required when q and k have different rows")
+    _int32(block_table, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    _dev(err_word, "err_word")
+    device = _same_device(q, (k, block_table, q_start, k_start, err_word))
+    if _dev(weights, "weights").dim() != 3:
+        raise ValueError("weights must be [num_pages, Hkv, page_tokens]")
+    _weight_pool(weights, weights.shape[0], Hkv, weights.shape[2], device)
+    dtype = _dt(q)
+    with _launching(device, stream) as s:
+        if Tq * Tk * Hq * Hkv * D == 0:
+            return weights
+
+        def params(ws, nbytes):
+            return _WEIGHTS.pack(
+                q.data_ptr(), k.data_ptr(), weights.data_ptr(), block_table.data_ptr(),
+                q_start.data_ptr(), _addr(k_start), _addr(err_word), dtype, bool(accumulate), B,
+                Tq, Tk, Hq, Hkv, D, weights.shape[2], block_table.shape[1], weights.shape[0],
+                qst[0], qst[1], kst[0], kst[1], scale, 0, ws, nbytes)
+
+        _call_with_workspace(
+            "attn_weights_packed", params, device, s, workspace,
+            lambda p: L.attn_weights_packed_bytes(p, s),
+            lambda p: L.attn_weights_packed_workspace(C.byref(WeightsParams.from_buffer_copy(p))))
+    return weights
+
+
+def paged_kv_select(weights, block_table, ctx_len, budget, *, sink=0, recent=0, keep=None,
+                    new_len=None, err_word=None, stream=None):
+    """The tokens that each KV head keeps of contexts that have outgrown ``budget`` tokens: the
+    first ``sink``, the last ``recent``, and of those between them the ones with the largest
+    accumulated weights (ties: the lower token; NaN counts as -inf); all of a shorter context.
+
+    ``weights`` float32 ``[num_pages, Hkv, page_tokens]``, ``block_table`` int32 ``[B, max_pages]``,
+    ``ctx_len`` int32 ``[B]``.  Returns ``(keep, new_len)``: int32 ``[B, Hkv, budget]``, ascending,
+    -1 behind the last, and int32 ``[B]``, ``min(ctx_len, budget)``."""
+    L = load()
+    _dev(weights, "weights")
+    if weights.dtype != torch.float32:
+        raise TypeError("weights must be float32")
+    if weights.dim() != 3:
+        raise ValueError("weights must be [num_pages, Hkv, page_tokens]")
+    _int32(block_table, "block_table")
+    _int32(ctx_len, "ctx_len")
+    _dev(err_word, "err_word")
+    B = ctx_len.numel()
+    _paged_shapes(B, block_table, ctx_len)
+    num_pages, Hkv, page_tokens = weights.shape
+    budget = int(budget)
+    device = _same_device(weights, (block_table, ctx_len, keep, new_len, err_word))
+    if keep is not None:
+        _int32(keep, "keep", B * Hkv * budget)
+    if new_len is not None:
+        _int32(new_len, "new_len", B)
+    with _launching(device, stream) as s:
+        if keep is None:
+            keep = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=device)
+        if new_len is None:
+            new_len = torch.empty(B, dtype=torch.int32, device=device)
+        p = _SELECT.pack(weights.data_ptr(), block_table.data_ptr(), ctx_len.data_ptr(),
+                         keep.data_ptr(), new_len.data_ptr(), _addr(err_word), B, Hkv, page_tokens,
+                         block_table.shape[1], num_pages, budget, int(sink), int(recent))
+        _check("paged_kv_select", L.paged_kv_select_bytes(p, s))
+    return keep, new_len
+
+
+def paged_kv_compact(k_pool, v_pool, block_table, ctx_len, keep, *, weights=None, head_dim=None,
+                     err_word=None, stream=None):
+    """Move the kept rows to the front of their sequences' pages, in place: token i of sequence b
+    and KV head h becomes token ``keep[b, h, i]`` (its rows of K and V and its weight).
+
+    ``keep`` int32 ``[B, Hkv, width]``, ascending, -1 behind the last, as ``paged_kv_select`` returns
+    it; ``ctx_len`` int32 ``[B]``, the lengths before.  FP8 pools need ``weights`` or ``head_dim``
+    to tell their rows' size.  A sequence's pages must be its own."""
+    L = load()
+    for n, t in (("k_pool", k_pool), ("v_pool", v_pool), ("err_word", err_word)):
+        _dev(t, n)
+    _int32(block_table, "block_table")
+    _int32(ctx_len, "ctx_len")
+    _int32(keep, "keep")
+    B, pool = ctx_len.numel(), k_pool.shape
+    _paged_shapes(B, block_table, ctx_len)
+    device = _same_device(k_pool, (v_pool, block_table, ctx_len, keep, weights, err_word))
+    if k_pool.dtype == torch.uint8:
+        D = head_dim
+        if D is None:
+            if weights is None or weights.dim() != 3 or len(pool) != 3 or weights.shape[2] == 0:
+                raise ValueError("give head_dim, or weights [num_pages, Hkv, page_tokens]")
+            D = max(pool[2] // weights.shape[2] - 1, 0)
+        fmt, page_tokens, dtype = FP8_E4M3_PAGE, _fp8_page_tokens(k_pool, v_pool, D), BF16
+    else:
+        if len(pool) != 4 or v_pool.shape != pool or v_pool.dtype != k_pool.dtype:
+            raise ValueError("pools must be two of [num_pages, Hkv, page_tokens, D], or FP8 pools")
+        fmt, page_tokens, D, dtype = 0, pool[2], pool[3], _dt(k_pool)
+        if head_dim is not None and head_dim != D:
+            raise ValueError(f"the pools' rows have {D} elements")
+    if keep.dim() != 3 or keep.shape[0] != B or keep.shape[1] != pool[1]:
+        raise ValueError("keep must be [B, Hkv, width]")
+    if weights is not None:
+        _weight_pool(weights, pool[0], pool[1], page_tokens, device)
+    if k_pool.shape != v_pool.shape:
+        raise ValueError("k_pool and v_pool must have the same shape")
+    if keep.numel() == 0:
+        return
+    with _launching(device, stream) as s:
+        p = _COMPACT.pack(k_pool.data_ptr(), v_pool.data_ptr(), _addr(weights),
+                          block_table.data_ptr(), ctx_len.data_ptr(), keep.data_ptr(),
+                          _addr(err_word), dtype, fmt, B, pool[1], D, page_tokens,
+                          block_table.shape[1], pool[0], keep.shape[2])
+        _check("paged_kv_compact", L.paged_kv_compact_bytes(p, s))

@@ -63,6 +63,12 @@ __device__ __forceinline__ bool dense_visible(const GatherArgs& a, int64_t b, in
   return !(a.causal && c > off + i);
 }
 
+// What the weights of a decode row need of it: its maximum and the inverse of its
+// sum (0 where it saw nothing; NaN where it saw a NaN).
+__device__ __forceinline__ float2 row_stat(float m, float l) {
+  return make_float2(m, l != l ? l : (m == SA_NEG_INF || l == 0.f) ? 0.f : 1.0f / l);
+}
+
 // Per-batch write position of the fused current-token append.
 __device__ __forceinline__ int64_t write_pos_of(const GatherArgs& a, int64_t b) {
   return a.write_pos ? a.write_pos[b] : a.T - a.C;

@@ -147,7 +147,12 @@ __global__ void __launch_bounds__(128) gather_simt_kernel(GatherArgs a) {
 #pragma unroll
     for (int t = 0; t < kU; ++t) {
       const int32_t row = rows[t];
-      if (row < 0) continue;
+      // (paged: the scores that the tokens' weights are formed from, -inf for a bad page)
+      float* score = a.scores && cb + 4 * t < c1 ? a.scores + (u.b * a.Hq + h) * a.score_stride + cb + 4 * t : nullptr;
+      if (row < 0) {
+        if (score && lane == 0) *score = SA_NEG_INF;
+        continue;
+      }
       float dot = 0.f;
 #pragma unroll
       for (int k = 0; k < DPL; ++k) {
@@ -164,6 +169,7 @@ __global__ void __launch_bounds__(128) gather_simt_kernel(GatherArgs a) {
         x += kLog2e * bias_term(a, u.b, h, u.i, j);
         if (x == SA_NEG_INF) continue;  // a -inf term masks the key
       }
+      if (score && lane == 0) *score = x;
       const float mn = fmaxf(m, x);
       const float al = exp2f(m - mn);  // m == -inf -> 0
       const float p = exp2f(x - mn);

@@ -177,7 +177,9 @@ struct Part {
   int32_t where;               // float offset of o from the shared-memory base (-1: none)
 };
 
-template <typename T, int D, int NT>
+// kScores: the scores and the rows' statistics are kept for the tokens' weights (a form
+// of its own, so that the plain decode keeps its registers).
+template <typename T, int D, int NT, bool kScores>
 __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
     fp8_pages_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                      const GatherArgs a, int64_t pool_heads, int64_t min_range) {
@@ -429,6 +431,7 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
           if (hh >= hpu) continue;
           const float up_v = down_v[nt][j] == 0.f ? 1.0f : 1.0f / down_v[nt][j];  // 2^E
           if (whole) {
+            if (kScores && gid == 0) a.stats[head0 + hh] = row_stat(m_run[nt][j], l);
             const float inv = (m_run[nt][j] == SA_NEG_INF || l == 0.f) ? 0.f : up_v / l;
             T* yp = static_cast<T*>(a.y) + static_cast<int64_t>(head0 + hh) * D;
 #pragma unroll
@@ -536,6 +539,19 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
       // scores in log2 units less the running maximum; probabilities
       const float ks0 = e8m0_f32(kb0), ks1 = e8m0_f32(kb1);
       const float vs0 = lo_ok ? e8m0_f32(vb0) : 0.f, vs1 = hi_ok ? e8m0_f32(vb1) : 0.f;
+      if (kScores) {
+        // (a token's scores of 8 heads: sectors of 32 bytes, 8 tokens each)
+        float* sp = a.scores + (cur.b * a.Hq + cur.grp * a.hpu + 2 * tig) * a.score_stride + (cur.ctx - left + gid);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (nt * 8 + 2 * tig + j >= hpu) continue;
+            float* at = sp + (nt * 8 + j) * a.score_stride;
+            if (lo_ok) at[0] = s[nt][j] * (ks0 * mult[nt][j]);
+            if (hi_ok) at[8] = s[nt][2 + j] * (ks1 * mult[nt][j]);
+          }
+      }
       bool raise = fresh;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -738,6 +754,7 @@ __global__ void __launch_bounds__(FGeo<D, NT>::kThreads, 1)
         acc.w = fmaf(v.w, c, acc.w);
       }
       if (whole) {
+        if (kScores && d == 0) a.stats[head0 + hh] = row_stat(M, L);
         const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
         *reinterpret_cast<uint2*>(static_cast<T*>(a.y) + (head0 + hh) * D + d) =
             make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
@@ -806,6 +823,7 @@ __global__ void __launch_bounds__(128) fp8_combine_kernel(const GatherArgs a) {
       acc.w = fmaf(v[i].w, f, acc.w);
     }
   }
+  if (a.stats && d == 0) a.stats[b * a.Hq + grp * a.hpu + hh] = row_stat(M, L);
   const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
   *reinterpret_cast<uint2*>(static_cast<T*>(a.y) + (b * a.Hq + grp * a.hpu + hh) * a.D + d) =
       make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
@@ -828,17 +846,17 @@ bool pool_map(CUtensorMap* m, const void* base, const GatherArgs& a, int64_t poo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, int NT>
-int launch_t(const GatherArgs& a, int64_t pool_heads, int sms, cudaStream_t st) {
+template <typename T, int D, int NT, bool kScores>
+int launch_s(const GatherArgs& a, int64_t pool_heads, int sms, cudaStream_t st) {
   using G = FGeo<D, NT>;
   CUtensorMap tk, tv;
   if (!pool_map<D, NT>(&tk, a.k, a, pool_heads) || !pool_map<D, NT>(&tv, a.v, a, pool_heads)) return -1;
   const size_t smem = 1024 + G::kOffPref + static_cast<size_t>(a.B + 1) * sizeof(int32_t);
-  if (!allow_smem(reinterpret_cast<const void*>(fp8_pages_kernel<T, D, NT>))) return -1;
+  if (!allow_smem(reinterpret_cast<const void*>(fp8_pages_kernel<T, D, NT, kScores>))) return -1;
   mark_event(a.ev_before, st);
   // Ranges of at least two tiles: below that a warp's set-up and the merge of its
   // partial cost more than the tiles.
-  fp8_pages_kernel<T, D, NT><<<static_cast<unsigned>(sms), G::kThreads, smem, st>>>(tk, tv, a, pool_heads, 2);
+  fp8_pages_kernel<T, D, NT, kScores><<<static_cast<unsigned>(sms), G::kThreads, smem, st>>>(tk, tv, a, pool_heads, 2);
   if (cudaGetLastError() != cudaSuccess) return -1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.units * a.hpu * (D / 4) + 127) / 128));
@@ -851,6 +869,11 @@ int launch_t(const GatherArgs& a, int64_t pool_heads, int sms, cudaStream_t st) 
   cfg.numAttrs = 1;
   mark_event(a.ev_after, st);
   return cudaLaunchKernelEx(&cfg, fp8_combine_kernel<T>, a) == cudaSuccess ? 0 : -1;
+}
+
+template <typename T, int D, int NT>
+int launch_t(const GatherArgs& a, int64_t pool_heads, int sms, cudaStream_t st) {
+  return a.scores ? launch_s<T, D, NT, true>(a, pool_heads, sms, st) : launch_s<T, D, NT, false>(a, pool_heads, sms, st);
 }
 
 template <typename T>

@@ -189,9 +189,10 @@ __device__ __forceinline__ int64_t key_row(const GatherArgs& a, const KeyRef& k)
   return static_cast<int64_t>(k.raw) * a.Hkv * a.page_tokens + k.base;
 }
 
-// kBias: the request carries an additive bias (a separate instance, so that
-// the common bias-free kernel keeps its registers).
-template <typename T, int D, int NT, bool kTma, bool kBias>
+// kBias: the request carries an additive bias; kScores: a paged request whose scores
+// and row statistics are kept for the tokens' weights (separate instances, so that the
+// common kernel keeps its registers).
+template <typename T, int D, int NT, bool kTma, bool kBias, bool kScores>
 __global__ void __launch_bounds__(SGeo<D, kTma>::kThreads, 1)
     gather_stream_kernel(const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, GatherArgs a) {
@@ -423,6 +424,7 @@ __global__ void __launch_bounds__(SGeo<D, kTma>::kThreads, 1)
           const int64_t h = cur.ui.h0 + hh;
           const float M = m_run[nt][j];
           float L = lsum[nt][j];
+          if (kScores && gid == 0) a.stats[cur.ui.b * a.Hq + h] = row_stat(M, L);
           if (a.sink && M != SA_NEG_INF) L += ex2(a.sink[h] * kLog2e - M);
           const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
           T* yp = static_cast<T*>(a.y) + ((cur.ui.b * a.Hq + h) * a.Sq + cur.ui.i) * D;
@@ -524,6 +526,11 @@ __global__ void __launch_bounds__(SGeo<D, kTma>::kThreads, 1)
             x += kLog2e * bias_term(a, cur.ui.b, cur.ui.h0 + hh, cur.ui.i, j);
         }
         s[nt][e] = ((e < 2) ? v_lo : v_hi) ? x : SA_NEG_INF;
+        if (kScores) {
+          const int hh = nt * 8 + 2 * tig + (e & 1);
+          if (((e < 2) ? v_lo : v_hi) && hh < a.hpu)
+            a.scores[(cur.ui.b * a.Hq + cur.ui.h0 + hh) * a.score_stride + (t - cur.tu.off) * 16 + gid + (e < 2 ? 0 : 8)] = x;
+        }
       }
       float tm0 = fmaxf(s[nt][0], s[nt][2]);
       float tm1 = fmaxf(s[nt][1], s[nt][3]);
@@ -624,10 +631,11 @@ __global__ void __launch_bounds__(128) stream_combine_kernel(GatherArgs a) {
       for (int wi = 0; wi < kRegW; ++wi)
         if (wi < nw) M = fmaxf(M, ml[wi].x);
       const float Mu = (M == SA_NEG_INF) ? 0.f : M;
-      float L = 0.f;
+      float L = 0.f, lost = 0.f;  // lost: NaN when a partial of nothing but NaN scores is left out
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int wi = 0; wi < kRegW; ++wi) {
+        if (wi < nw && ml[wi].x == SA_NEG_INF) lost += ml[wi].y;
         if (wi < nw && ml[wi].x != SA_NEG_INF) {
           const float f = ex2(ml[wi].x - Mu);
           L += ml[wi].y * f;
@@ -637,6 +645,7 @@ __global__ void __launch_bounds__(128) stream_combine_kernel(GatherArgs a) {
           acc.w = fmaf(v[wi].w, f, acc.w);
         }
       }
+      if (a.stats && d == 0) a.stats[ui.b * a.Hq + ui.h0 + hh] = row_stat(M, L + lost);
       if (a.sink && M != SA_NEG_INF) L += ex2(a.sink[ui.h0 + hh] * kLog2e - M);
       const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
       T* yp = static_cast<T*>(a.y) + ((ui.b * a.Hq + ui.h0 + hh) * a.Sq + ui.i) * D + d;
@@ -725,6 +734,7 @@ __global__ void __launch_bounds__(128) stream_combine_kernel(GatherArgs a) {
     const int hh = (e * 4) / D, d = (e * 4) % D;
     const float M = sM[hh];
     float L = sL[hh];
+    if (a.stats && d == 0) a.stats[ui.b * a.Hq + ui.h0 + hh] = row_stat(M, L);
     if (a.sink && M != SA_NEG_INF) L += ex2(a.sink[ui.h0 + hh] * kLog2e - M);
     const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
     T* yp = static_cast<T*>(a.y) + ((ui.b * a.Hq + ui.h0 + hh) * a.Sq + ui.i) * D + d;
@@ -789,26 +799,26 @@ static bool kv_maps(const GatherArgs& a, int dtype, CUtensorMap* tk, CUtensorMap
   return true;
 }
 
-template <typename T, int D, int NT, bool kBias>
+template <typename T, int D, int NT, bool kBias, bool kScores = false>
 static int launch_stream_b(const GatherArgs& a, int dtype, int grid, cudaStream_t st) {
   CUtensorMap tk, tv;
   std::memset(&tk, 0, sizeof(tk));
   std::memset(&tv, 0, sizeof(tv));
   if (kv_maps(a, dtype, &tk, &tv)) {
     const size_t smem = smem_bytes_t<D, true>(a.source, a.B);
-    if (cudaFuncSetAttribute(gather_stream_kernel<T, D, NT, true, kBias>,
+    if (cudaFuncSetAttribute(gather_stream_kernel<T, D, NT, true, kBias, kScores>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
       return -1;
-    return launch_pdl(gather_stream_kernel<T, D, NT, true, kBias>, dim3(grid),
+    return launch_pdl(gather_stream_kernel<T, D, NT, true, kBias, kScores>, dim3(grid),
                       dim3(SGeo<D, true>::kThreads), smem, st, tk, tv, a);
   }
   const size_t smem = smem_bytes_t<D, false>(a.source, a.B);
-  if (cudaFuncSetAttribute(gather_stream_kernel<T, D, NT, false, kBias>,
+  if (cudaFuncSetAttribute(gather_stream_kernel<T, D, NT, false, kBias, kScores>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return -1;
-  return launch_pdl(gather_stream_kernel<T, D, NT, false, kBias>, dim3(grid),
+  return launch_pdl(gather_stream_kernel<T, D, NT, false, kBias, kScores>, dim3(grid),
                     dim3(SGeo<D, false>::kThreads), smem, st, tk, tv, a);
 }
 
@@ -816,6 +826,7 @@ template <typename T, int D, int NT>
 static int launch_stream_t(const GatherArgs& a, int dtype, int grid, cudaStream_t st) {
   // an additive bias (selected tokens) or attention mask (dense prefill)
   if (a.bias && a.source != kPaged) return launch_stream_b<T, D, NT, true>(a, dtype, grid, st);
+  if (a.scores) return launch_stream_b<T, D, NT, false, true>(a, dtype, grid, st);
   return launch_stream_b<T, D, NT, false>(a, dtype, grid, st);
 }
 

@@ -127,6 +127,10 @@ struct GatherArgs {
   int fp8_warp_mma;           // FP8 records: the warp-level MMA kernel only
   void* ev_before;            // nullable cudaEvent_t pair recorded around the dominant kernel
   void* ev_after;
+  // weights of a paged decode (paged source; scores nullable)
+  float* scores;              // [B, Hq, score_stride]: every token's score, log2 units
+  float2* stats;              // [B, Hq]: a row's maximum and the inverse of its sum
+  int64_t score_stride;
   // math
   float scale_log2;           // scale * log2(e)
   float softcap;              // 0 = off

@@ -14,6 +14,7 @@
 #include "../../include/sa.h"
 #include "kernels.h"
 #include "serving.h"
+#include "weights.h"
 
 namespace {
 
@@ -923,10 +924,43 @@ static bool plan_fp8_pages(const sa_paged_params* p, Plan& pl) {
   return true;
 }
 
-static int paged_fp8_decode(const sa_paged_params* p, cudaStream_t st) {
+// The workspace of a decode that keeps the weights, behind the decode's own: row
+// statistics, the tile space of a decode that has none, the scores.
+struct WeightsPlan {
+  size_t off_stats = 0, off_pref = 0, off_scores = 0, bytes = 0;
+  int64_t stride = 0;
+};
+
+static WeightsPlan plan_decode_weights(const sa_paged_params* p, size_t used) {
+  WeightsPlan w;
+  w.stride = (p->max_pages * p->page_tokens + 15) / 16 * 16;
+  w.off_stats = align_up(used);
+  w.off_pref = w.off_stats + align_up(static_cast<size_t>(p->B * p->Hq) * sizeof(float2));
+  w.off_scores = w.off_pref + align_up(static_cast<size_t>(p->B + 1) * sizeof(int32_t));
+  w.bytes = w.off_scores + align_up(static_cast<size_t>(p->B * p->Hq) * static_cast<size_t>(w.stride) * sizeof(float));
+  return w;
+}
+
+// Fills what a decode with weights needs of the workspace; `pref` where it has no tile space.
+static void carve_weights(const sa_paged_params* p, const WeightsPlan& w, sa::GatherArgs& g) {
+  char* ws = static_cast<char*>(p->workspace);
+  g.stats = reinterpret_cast<float2*>(ws + w.off_stats);
+  g.scores = reinterpret_cast<float*>(ws + w.off_scores);
+  g.score_stride = w.stride;
+  if (!g.pref_out) g.pref_out = reinterpret_cast<int32_t*>(ws + w.off_pref);
+}
+
+// weights: nullable.
+static int paged_fp8_decode(const sa_paged_params* p, float* weights, cudaStream_t st) {
   Plan pl;
   paged_args(p, pl.g);
   if (!plan_fp8_pages(p, pl)) return SA_ERR_UNSUPPORTED;
+  WeightsPlan wp;
+  const size_t own = pl.bytes;
+  if (weights) {
+    wp = plan_decode_weights(p, own);
+    pl.bytes = wp.bytes;
+  }
   const int rc = check_workspace(pl, p->workspace, p->workspace_bytes);
   if (rc != SA_OK) return rc;
   if (p->k_new) {
@@ -961,7 +995,10 @@ static int paged_fp8_decode(const sa_paged_params* p, cudaStream_t st) {
   g.part_ml = reinterpret_cast<float*>(ws + pl.off_part_ml);
   g.ev_before = t_ev_before;
   g.ev_after = t_ev_after;
-  return sa::launch_fp8_pages(g, p->Hkv, p->dtype, sa::sm_count(), st) == 0 ? SA_OK : SA_ERR_LAUNCH;
+  if (weights) carve_weights(p, wp, g);
+  if (sa::launch_fp8_pages(g, p->Hkv, p->dtype, sa::sm_count(), st) != 0) return SA_ERR_LAUNCH;
+  if (weights && sa::launch_decode_weights(g, weights, p->Hkv, st) != 0) return SA_ERR_LAUNCH;
+  return SA_OK;
 }
 
 size_t paged_attn_decode_workspace(const sa_paged_params* p) {
@@ -976,15 +1013,45 @@ size_t paged_attn_decode_workspace(const sa_paged_params* p) {
   return pl.bytes;
 }
 
-int paged_attn_decode(const sa_paged_params* p, void* stream) {
+// What a decode that keeps the weights asks for besides (weights NULL: its sizes alone).
+static int check_decode_weights(const sa_paged_params* p, const float* weights) {
+  constexpr int64_t k31 = int64_t(1) << 31;
+  if (p->options != 0) return SA_ERR_UNSUPPORTED;
+  if (p->B >= k31 || p->Hq >= k31 || p->B * p->Hq >= k31 || p->max_pages >= k31 ||
+      p->max_pages * p->page_tokens >= k31 - 64 ||
+      p->B * p->Hq > (int64_t(1) << 40) / (p->max_pages * p->page_tokens))
+    return SA_ERR_UNSUPPORTED;
+  if (!weights) return SA_OK;
+  if (reinterpret_cast<uintptr_t>(weights) % 4) return SA_ERR_ALIGN;
+  const size_t es = dtype_bytes(p->dtype), pool = static_cast<size_t>(p->num_pages * p->Hkv * p->page_tokens);
+  const size_t kv = p->pool_format == SA_FP8_E4M3_PAGE ? pool * static_cast<size_t>(p->D + 1) : pool * static_cast<size_t>(p->D) * es;
+  const size_t rows = static_cast<size_t>(p->B * p->Hq * p->D) * es, one = static_cast<size_t>(p->B * p->Hkv * p->D) * es;
+  if (overlaps(weights, pool * 4, p->k_pool, kv) || overlaps(weights, pool * 4, p->v_pool, kv) ||
+      overlaps(weights, pool * 4, p->q, rows) || overlaps(weights, pool * 4, p->y, rows) ||
+      (p->k_new && overlaps(weights, pool * 4, p->k_new, one)) || (p->v_new && overlaps(weights, pool * 4, p->v_new, one)) ||
+      overlaps(weights, pool * 4, p->block_table, static_cast<size_t>(p->B * p->max_pages) * 4) ||
+      overlaps(weights, pool * 4, p->ctx_len, static_cast<size_t>(p->B) * 4) ||
+      overlaps(weights, pool * 4, p->workspace, p->workspace_bytes))
+    return SA_ERR_OVERLAP;
+  return SA_OK;
+}
+
+static int paged_decode(const sa_paged_params* p, float* weights, cudaStream_t st) {
   int rc = check_paged(p);
   if (rc != SA_OK) return rc;
-  cudaStream_t st = as_stream(stream);
-  if (p->pool_format == SA_FP8_E4M3_PAGE) return paged_fp8_decode(p, st);
+  if (weights) rc = check_decode_weights(p, weights);
+  if (rc != SA_OK) return rc;
+  if (p->pool_format == SA_FP8_E4M3_PAGE) return paged_fp8_decode(p, weights, st);
   Plan pl;
   paged_args(p, pl.g);
   rc = plan_gather(pl, p->dtype);
   if (rc != SA_OK) return rc;
+  const size_t own = pl.bytes;
+  WeightsPlan wp;
+  if (weights) {
+    wp = plan_decode_weights(p, own);
+    pl.bytes = wp.bytes;
+  }
   if (pl.stream && !(aligned16(p->k_pool) && aligned16(p->v_pool))) return SA_ERR_ALIGN;
   rc = check_workspace(pl, p->workspace, p->workspace_bytes);
   if (rc != SA_OK) return rc;
@@ -1007,8 +1074,29 @@ int paged_attn_decode(const sa_paged_params* p, void* stream) {
     if (sa::launch_paged_append(a, st) != 0) return SA_ERR_LAUNCH;
   }
   carve(pl, p->workspace);
-  return run_plan(pl, p->dtype, st);
+  if (!weights) return run_plan(pl, p->dtype, st);
+  carve_weights(p, wp, pl.g);
+  rc = run_plan(pl, p->dtype, st);
+  if (rc != SA_OK) return rc;
+  if (!pl.stream && sa::launch_row_stats(pl.g, st) != 0) return SA_ERR_LAUNCH;
+  return sa::launch_decode_weights(pl.g, weights, p->Hkv, st) == 0 ? SA_OK : SA_ERR_LAUNCH;
 }
+
+int paged_attn_decode(const sa_paged_params* p, void* stream) { return paged_decode(p, nullptr, as_stream(stream)); }
+
+size_t paged_attn_decode_weights_workspace(const sa_paged_params* p) {
+  if (check_paged(p, 1) != SA_OK || check_decode_weights(p, nullptr) != SA_OK) return 0;
+  Plan pl;
+  paged_args(p, pl.g);
+  if (p->pool_format == SA_FP8_E4M3_PAGE ? !plan_fp8_pages(p, pl) : plan_gather(pl, p->dtype) != SA_OK) return 0;
+  return plan_decode_weights(p, pl.bytes).bytes;
+}
+
+int paged_attn_decode_weights(const sa_paged_params* p, float* weights, void* stream) {
+  if (!weights) return SA_ERR_NULL;
+  return paged_decode(p, weights, as_stream(stream));
+}
+
 
 // ---- ratio-4 index selection -------------------------------------------------------
 
