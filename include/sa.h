@@ -866,7 +866,7 @@ int paged_attn_decode_weights(const sa_paged_params* p, float* weights, void* st
  * ctx_len itself): min(n, budget).  A ctx_len outside [0, max_pages * page_tokens] sets
  * SA_ERRBIT_PAGE (err_word nullable) and counts as 0; the weight behind a table entry
  * outside [0, num_pages) counts as -inf and sets it too.  sink + recent <= budget;
- * max_pages * page_tokens below 2^31 - 2^17.  Exact; no workspace.
+ * max_pages * page_tokens up to 2^22.  Exact; no workspace.
  */
 typedef struct {
   const float* weights;

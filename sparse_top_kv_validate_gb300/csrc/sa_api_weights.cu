@@ -30,6 +30,13 @@ size_t pool_bytes(int64_t Hkv, int64_t page_tokens, int64_t num_pages, int64_t r
   return static_cast<size_t>(num_pages * Hkv * head);
 }
 
+// log2(n), or -1 where n is no power of two.
+int log2_of(int64_t n) {
+  for (int s = 0; s < 31; ++s)
+    if (n == int64_t(1) << s) return s;
+  return -1;
+}
+
 // Checks; fills the kernel's arguments, whether it runs on the tensor cores and its workspace.
 int weights_args(const sa_weights_params* p, bool query, sa::WeightsArgs& a, bool& tc, size_t& need) {
   if (!p || !p->q || !p->k || !p->block_table || !p->q_start || (!query && !p->weights)) return SA_ERR_NULL;
@@ -131,7 +138,8 @@ int paged_kv_select(const sa_select_params* p, void* stream) {
   const int rc = pages_status(p->B, p->Hkv, p->page_tokens, p->max_pages, p->num_pages);
   if (rc != SA_OK) return rc;
   if (p->budget <= 0 || p->sink < 0 || p->recent < 0) return SA_ERR_SHAPE;
-  if (p->budget >= kMaxInt - (int64_t(1) << 17)) return SA_ERR_UNSUPPORTED;
+  if (p->budget >= kMaxInt - (int64_t(1) << 17) || p->max_pages * p->page_tokens > sa::kSelectMost)
+    return SA_ERR_UNSUPPORTED;
   if (p->sink > p->budget || p->recent > p->budget || p->sink + p->recent > p->budget) return SA_ERR_SHAPE;
   const size_t pool = pool_bytes(p->Hkv, p->page_tokens, p->num_pages, 4);
   if (pool == 0) return SA_ERR_UNSUPPORTED;
@@ -162,6 +170,7 @@ int paged_kv_select(const sa_select_params* p, void* stream) {
   a.sink = static_cast<int>(p->sink);
   a.recent = static_cast<int>(p->recent);
   a.page_tokens = static_cast<int>(p->page_tokens);
+  a.shift = log2_of(p->page_tokens);
   a.max_pages = p->max_pages;
   a.num_pages = p->num_pages;
   a.vec = p->page_tokens % 4 == 0 && aligned(p->weights, 16);

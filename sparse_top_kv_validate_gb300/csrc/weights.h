@@ -47,10 +47,12 @@ struct SelectArgs {
   int32_t* new_len;           // nullable [B]
   uint32_t* err_word;
   int B, Hkv, budget, sink, recent;
-  int page_tokens;
+  int page_tokens, shift;     // shift: log2(page_tokens), or -1
   int64_t max_pages, num_pages;
   int vec;                    // four tokens at a time: 16-byte loads stay inside a page
 };
+constexpr int64_t kSelectTokens = int64_t(1) << 19;  // tokens that a CTA can mark
+constexpr int64_t kSelectMost = 8 * kSelectTokens;   // of a context: what a cluster can mark
 int launch_kv_select(const SelectArgs& a, cudaStream_t st);
 
 // ---- compaction ------------------------------------------------------------------------
