@@ -9,9 +9,14 @@
 // before they are written, by all that share it (one barrier), while the reads of the
 // chunk after it may already be on their way.
 //
-// A CTA takes one plane of a (sequence, KV head): the rows of K, those of V, or the
-// small ones (scale bytes and weights) one after the other.  Where that makes too few
-// CTAs for the device, a cluster of up to 8 shares a plane, each chunk cut in as many pieces.
+// A CTA takes the rows of K, or of V, of a (sequence, KV head).  A chunk's rows are found
+// once, a thread to a row (list entry, then page, then place, each a chunk ahead of the
+// next), and their places put into shared memory; the rows themselves pass through a ring there,
+// each thread storing the pieces of 16 bytes that it has loaded.  (With the places worked
+// out for every piece, 160 instructions of it, that was the bound: 128 contexts to 2,048
+// tokens, FP8 pages, 289 us.)  Scale bytes and weights are moved by the threads that find the
+// rows, as soon as they have.  Where there are too few (sequence, KV head)s for the device, a
+// cluster of up to 8 larger CTAs shares one, each chunk cut in as many pieces.
 #include "cluster.cuh"
 #include "weights.h"
 
@@ -19,119 +24,214 @@ namespace sa {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxCluster = 8;
+
+// Where a row comes from (-1: there is none) and goes to, in bytes from the start of its plane,
+// and where its scale byte and its weight go (an element of theirs).
+struct __align__(16) Place {
+  int64_t from, to, scale, weight;
+};
+
+// A thread moves up to two rows of a chunk, two pieces of each at a time; chunks in the ring; the
+// chunks whose places are kept: those in the ring and the one behind them.
+constexpr int kRows = 2, kPieces = 2, kStages = 4, kPlaces = kStages + 1;
+template <bool kCluster>
+constexpr int kThreadsOf = kCluster ? 256 : 128;
+
+// Threads to a row of `pieces` pieces (at most kPieces * threads), rows of a CTA's part of a chunk.
+__host__ __device__ constexpr int lanes_of(int pieces) { return (pieces + kPieces - 1) / kPieces; }
+__host__ __device__ constexpr int chunk_of(int threads, int pieces) {
+  return lanes_of(pieces) == 1 ? threads : kRows * (threads / lanes_of(pieces));
+}
 
 // The loads whose words were folded into x have returned once this has executed.
 __device__ __forceinline__ void arrived(uint32_t x) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %0, 0x5bd1e995;\n\t@p nanosleep.u32 0;\n\t}" ::"r"(x) : "memory");
 }
-__device__ __forceinline__ uint32_t word_of(uint4 v) { return v.x; }
-__device__ __forceinline__ uint32_t word_of(uint32_t v) { return v; }
-__device__ __forceinline__ uint32_t word_of(uint16_t v) { return v; }
-__device__ __forceinline__ uint32_t word_of(uint8_t v) { return v; }
+// Every thread of the cluster passes wait() after every one has passed arrive().  No memory is
+// ordered by it: what it stands for are reads whose values have come back.  (An arrival that
+// releases waits for the stores of the chunk before to reach L2.)
+template <bool kCluster>
+__device__ __forceinline__ void arrive() {
+  __syncthreads();  // (and what this CTA wrote to shared memory is seen)
+  if (kCluster) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+template <bool kCluster>
+__device__ __forceinline__ void wait() {
+  if (kCluster) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
-struct Pages {
-  const int32_t* table;  // of the sequence
-  uint32_t pt;
-  int shift;             // log2(pt), or -1
-  int64_t num_pages, heads, head;
-  __device__ __forceinline__ void find(uint32_t t, int32_t& page, uint32_t& slot) const {
-    const uint32_t pi = shift >= 0 ? t >> shift : t / pt;
-    slot = t - pi * pt;
-    page = __ldg(table + pi);
-  }
-  __device__ __forceinline__ bool good(int32_t page) const { return page >= 0 && page < num_pages; }
+template <typename V>
+__device__ __forceinline__ void copy_async(V* dst, const V* src) {
+  if constexpr (sizeof(V) == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else if constexpr (sizeof(V) == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else *dst = *src;
+}
+
+// The planes of a (sequence, KV head): rows, and beside them scale bytes and weights
+// (nullable).  Row `slot` of unit (page * heads + head) lies at rows + unit * head_stride +
+// slot * row_bytes, its scale at scales + unit * head_stride + slot.
+struct Planes {
+  char* rows;
+  uint8_t* scales;
+  float* weights;
+  int64_t head_stride;
 };
 
-// `pieces` pieces of type V per row of one plane: token t's at
-// base + (page * heads + head) * head_stride + slot * row_stride (bytes).
-template <typename V, int U, bool kCluster>
-__device__ void move_plane(char* base, int64_t head_stride, int64_t row_stride, int pieces, const Pages& pg,
-                           const int32_t* keep, int m, int rank, int ctas, bool& bad) {
+// V: the pieces that a row is moved in.
+template <typename V, bool kCluster>
+__device__ void move_rows(const CompactArgs& a, const Planes& pl, const int32_t* table, const int32_t* keep, int head,
+                          int m, int rank, int ctas, uint8_t* smem, bool& bad) {
+  constexpr int S = kStages, R = kPlaces, kThreads = kThreadsOf<kCluster>;
   const int tid = static_cast<int>(threadIdx.x);
+  const uint32_t pt = static_cast<uint32_t>(a.page_tokens);
+  const int all = a.row_bytes / static_cast<int>(sizeof(V));
+  V* ring = reinterpret_cast<V*>(smem) + tid;  // piece q of row u of stage s: ring[((s * kRows + u) * kPieces + q) * kThreads]
+  Place* places = reinterpret_cast<Place*>(smem + S * kRows * kPieces * kThreads * 16);
 #pragma unroll 1
-  for (int col0 = 0; col0 < pieces; col0 += kThreads) {  // (columns are independent of one another)
-    const int cols = min(pieces - col0, kThreads);
-    const int rows = kThreads / cols;                     // of a step
-    const int r = tid / cols, c = col0 + tid - r * cols;
-    const bool mine = r < rows;
-    const int chunk = rows * U;                           // rows of this CTA's piece of a chunk
-    char* col = base + static_cast<int64_t>(c) * sizeof(V);
-    auto at = [&](int32_t page, uint32_t slot) {
-      return reinterpret_cast<V*>(col + (page * pg.heads + pg.head) * head_stride + slot * row_stride);
+  for (int col0 = 0; col0 < all; col0 += kPieces * kThreads) {  // (columns are independent of one another)
+    const int pieces = min(all - col0, kPieces * kThreads), lanes = lanes_of(pieces);
+    const int rows = kThreads / lanes, chunk = chunk_of(kThreads, pieces);
+    const int r = tid / lanes, c = tid - r * lanes;  // this thread's first row of a chunk, and piece of it
+    const int64_t step = static_cast<int64_t>(chunk) * ctas, own = static_cast<int64_t>(rank) * chunk;
+    char* col = pl.rows + static_cast<int64_t>(col0 + c) * sizeof(V);
+
+    // ---- finding a chunk's rows, one to a thread
+    auto list = [&](int64_t first) {
+      const int64_t i = first + own + tid;
+      const int32_t j = tid < chunk && i < m ? __ldg(keep + i) : -1;
+      return j == i ? -1 : j;  // (-1: it is where it belongs)
     };
-    // the rows of a chunk, on their way; bit u: there is one to move
-    auto load = [&](int64_t first, V (&v)[U]) {
-      uint32_t live = 0;
-      int32_t src[U], page[U];
-      uint32_t slot[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t i = first + u * rows + r;
-        src[u] = -1;
-        if (mine && i < m) {
-          src[u] = __ldg(keep + i);
-          if (src[u] == i) src[u] = -1;  // where it belongs
+    struct Found {
+      int32_t from, to;  // pages
+      uint32_t from_slot, to_slot;
+      bool moving;
+    };
+    auto pages = [&](int64_t first, int32_t src) {
+      Found f{0, 0, 0, 0, src >= 0};
+      if (!f.moving) return f;
+      const uint32_t x = static_cast<uint32_t>(src), y = static_cast<uint32_t>(first + own) + tid;
+      const uint32_t px = a.shift >= 0 ? x >> a.shift : x / pt, py = a.shift >= 0 ? y >> a.shift : y / pt;
+      f.from = __ldg(table + px);
+      f.to = __ldg(table + py);
+      f.from_slot = x - px * pt;
+      f.to_slot = y - py * pt;
+      return f;
+    };
+    // Writes the places down; the row's scale byte and weight are on their way.
+    auto place = [&](const Found& f, int at, uint32_t& scale, uint32_t& weight) {
+      Place now{-1, -1, -1, -1};
+      scale = weight = 0;
+      const bool good = f.from >= 0 && f.from < a.num_pages && f.to >= 0 && f.to < a.num_pages;
+      if (f.moving && good) {
+        const int64_t from = f.from * a.Hkv + head, to = f.to * a.Hkv + head;
+        now.from = from * pl.head_stride + f.from_slot * static_cast<int64_t>(a.row_bytes);
+        now.to = to * pl.head_stride + f.to_slot * static_cast<int64_t>(a.row_bytes);
+        if (pl.scales && col0 == 0) {
+          now.scale = to * pl.head_stride + f.to_slot;
+          scale = pl.scales[from * pl.head_stride + f.from_slot];
+        }
+        if (pl.weights && col0 == 0) {
+          now.weight = to * static_cast<int64_t>(pt) + f.to_slot;
+          weight = reinterpret_cast<const uint32_t*>(pl.weights)[from * static_cast<int64_t>(pt) + f.from_slot];
         }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        page[u] = -1;
-        if (src[u] >= 0) pg.find(static_cast<uint32_t>(src[u]), page[u], slot[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (src[u] < 0) continue;
-        if (pg.good(page[u])) {
-          v[u] = *at(page[u], slot[u]);
-          live |= 1u << u;
-        } else {
-          bad = true;
-        }
-      }
-      return live;
+      bad = bad || (f.moving && !good);
+      if (tid < chunk) places[at * chunk + tid] = now;
     };
-    const int64_t step = static_cast<int64_t>(chunk) * ctas;
-    V v[U], w[U];
+
+    // ---- moving them
+    uint32_t live = 0;  // a bit per stage and row of this thread: it is to be stored
+    auto copy = [&](int stage, int at) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = w[u] = V{};
-    uint32_t live = load(static_cast<int64_t>(rank) * chunk, v);
-#pragma unroll 1
-    for (int64_t first = 0; first < m; first += step) {
-      const int64_t own = first + static_cast<int64_t>(rank) * chunk;
-      const uint32_t next = load(own + step, w);
-      uint32_t x = 0;
+      for (int u = 0; u < kRows; ++u) {
+        const uint32_t bit = 1u << (stage * kRows + u);
+        live &= ~bit;
+        const int x = u * rows + r;
+        if (r >= rows || x >= chunk) continue;
+        const int64_t from = places[at * chunk + x].from;
+        if (from < 0) continue;
+        live |= bit;
 #pragma unroll
-      for (int u = 0; u < U; ++u) x ^= word_of(v[u]);
-      arrived(x);
-      if (kCluster) cluster_sync();
-      else __syncthreads();
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (!((live >> u) & 1u)) continue;
-        int32_t page;
-        uint32_t slot;
-        pg.find(static_cast<uint32_t>(own + u * rows + r), page, slot);
-        if (pg.good(page)) *at(page, slot) = v[u];
-        else bad = true;
+        for (int q = 0; q < kPieces; ++q)
+          if (c + q * lanes < pieces)
+            copy_async(ring + ((stage * kRows + u) * kPieces + q) * kThreads,
+                       reinterpret_cast<const V*>(col + from + q * lanes * static_cast<int>(sizeof(V))));
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto store = [&](int stage, int at, uint32_t scale, uint32_t weight) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = w[u];
-      live = next;
+      for (int u = 0; u < kRows; ++u) {
+        if (!(live >> (stage * kRows + u) & 1u)) continue;
+        const int64_t to = places[at * chunk + u * rows + r].to;
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q)
+          if (c + q * lanes < pieces)
+            *reinterpret_cast<V*>(col + to + q * lanes * static_cast<int>(sizeof(V))) =
+                ring[((stage * kRows + u) * kPieces + q) * kThreads];
+      }
+      if (tid < chunk) {
+        const Place& p = places[at * chunk + tid];
+        if (p.scale >= 0) pl.scales[p.scale] = static_cast<uint8_t>(scale);
+        if (p.weight >= 0) reinterpret_cast<uint32_t*>(pl.weights)[p.weight] = weight;
+      }
+    };
+
+    // Chunk k: stage k % S of the ring, places k % R; its small values in scale / weight[k % S].
+    // (The loop goes S chunks at a time, so that a value on its way stays in its register.)
+    uint32_t scale[S], weight[S];
+    int32_t src[2];
+    Found found[2];
+#pragma unroll
+    for (int s = 0; s < S; ++s) place(pages(s * step, list(s * step)), s, scale[s], weight[s]);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      found[x] = pages((S + x) * step, list((S + x) * step));
+      src[x] = list((S + 2 + x) * step);
     }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) copy(s, s);
+    int at = 0;
+    static_assert(S % 2 == 0, "the pages and entries ahead alternate");
+#pragma unroll 1
+    for (int64_t first = 0; first < m; first += S * step) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const int64_t now = first + s * step;
+        if (now >= m) break;
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");  // this chunk's are there
+        const uint32_t now_scale = scale[s], now_weight = weight[s];
+        arrived(now_scale ^ now_weight);
+        arrive<kCluster>();
+        copy((s + S - 1) % S, at + S - 1 < R ? at + S - 1 : at + S - 1 - R);
+        place(found[s & 1], at + S < R ? at + S : at + S - R, scale[s], weight[s]);
+        found[s & 1] = pages(now + (S + 2) * step, src[s & 1]);
+        src[s & 1] = list(now + (S + 4) * step);
+        wait<kCluster>();
+        store(s, at, now_scale, now_weight);
+        if (++at == R) at = 0;
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the places have been read
   }
 }
 
 template <bool kCluster>
-__global__ void __launch_bounds__(kThreads)
-    kv_compact_kernel(const __grid_constant__ CompactArgs a, int planes, int ctas, int shift) {
+__global__ void __launch_bounds__(kThreadsOf<kCluster>)
+    kv_compact_kernel(const __grid_constant__ CompactArgs a, int ctas) {
+  constexpr int kThreads = kThreadsOf<kCluster>;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ int s_end, s_code;
   const int tid = static_cast<int>(threadIdx.x);
   const uint32_t item = blockIdx.x / static_cast<uint32_t>(ctas);
   const int rank = kCluster ? static_cast<int>(cluster_rank()) : 0;
-  const uint32_t row = item / static_cast<uint32_t>(planes);
-  const int plane = static_cast<int>(item - row * static_cast<uint32_t>(planes));
+  const uint32_t row = item >> 1;
+  const int plane = static_cast<int>(item & 1u);  // K or V
   const int b = static_cast<int>(row / static_cast<uint32_t>(a.Hkv)), h = static_cast<int>(row) - b * a.Hkv;
   const int32_t* keep = a.keep + static_cast<int64_t>(row) * a.width;
   const int64_t n = __ldg(a.ctx_len + b);
@@ -171,46 +271,39 @@ __global__ void __launch_bounds__(kThreads)
     if (tells && tid == 0) atomicOr(a.err_word, static_cast<uint32_t>(code));
     return;
   }
-  const Pages pg{a.block_table + static_cast<int64_t>(b) * a.max_pages, static_cast<uint32_t>(a.page_tokens), shift,
-                 a.num_pages, a.Hkv, h};
   bool bad = false;
-  const int64_t head = static_cast<int64_t>(a.page_tokens) * (a.row_bytes + (a.fp8 ? 1 : 0));
-  if (plane < 2) {
-    char* base = static_cast<char*>(a.pool[plane]);
-    if (a.align == 16)
-      move_plane<uint4, 8, kCluster>(base, head, a.row_bytes, a.row_bytes / 16, pg, keep, m, rank, ctas, bad);
-    else if (a.align == 4)
-      move_plane<uint32_t, 8, kCluster>(base, head, a.row_bytes, a.row_bytes / 4, pg, keep, m, rank, ctas, bad);
-    else
-      move_plane<uint16_t, 8, kCluster>(base, head, a.row_bytes, a.row_bytes / 2, pg, keep, m, rank, ctas, bad);
-  } else {
-    if (a.fp8)
-      for (int t = 0; t < 2; ++t)
-        move_plane<uint8_t, 8, kCluster>(static_cast<char*>(a.pool[t]) + static_cast<int64_t>(a.page_tokens) * a.row_bytes,
-                                         head, 1, 1, pg, keep, m, rank, ctas, bad);
-    if (a.weights)
-      move_plane<uint32_t, 8, kCluster>(reinterpret_cast<char*>(a.weights), static_cast<int64_t>(a.page_tokens) * 4, 4, 1,
-                                        pg, keep, m, rank, ctas, bad);
-  }
+  Planes pl;
+  pl.rows = static_cast<char*>(a.pool[plane]);
+  pl.head_stride = static_cast<int64_t>(a.page_tokens) * (a.row_bytes + (a.fp8 ? 1 : 0));
+  pl.scales = a.fp8 ? reinterpret_cast<uint8_t*>(pl.rows) + static_cast<int64_t>(a.page_tokens) * a.row_bytes : nullptr;
+  pl.weights = plane == 0 ? a.weights : nullptr;
+  const int32_t* table = a.block_table + static_cast<int64_t>(b) * a.max_pages;
+  if (a.align == 16) move_rows<uint4, kCluster>(a, pl, table, keep, h, m, rank, ctas, ring, bad);
+  else if (a.align == 4) move_rows<uint32_t, kCluster>(a, pl, table, keep, h, m, rank, ctas, ring, bad);
+  else move_rows<uint16_t, kCluster>(a, pl, table, keep, h, m, rank, ctas, ring, bad);
   if (bad && a.err_word) atomicOr(a.err_word, static_cast<uint32_t>(SA_ERRBIT_PAGE));
 }
 
 }  // namespace
 
 int launch_kv_compact(const CompactArgs& a, cudaStream_t st) {
-  const int planes = a.fp8 || a.weights ? 3 : 2;
-  const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * planes;
-  // about two CTAs to a multiprocessor, each with a few chunks to move
-  const int64_t pieces = a.row_bytes / a.align, rows = pieces >= kThreads ? 1 : kThreads / pieces;
+  const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * 2;
+  // clusters where a CTA per item would leave half of the multiprocessors idle and there is more
+  // than one chunk to move
+  const int pieces = a.row_bytes / a.align;
   int ctas = 1;
-  while (ctas < kMaxCluster && items * ctas < 2 * sm_count() && rows * 8 * ctas * 2 < a.width) ctas *= 2;
+  while (ctas < kMaxCluster && items * ctas * 2 <= sm_count() && chunk_of(kThreadsOf<true>, pieces) * ctas / 2 < a.width) ctas *= 2;
   if (items * ctas > INT32_MAX) return -1;
-  int shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if (a.page_tokens == 1 << s) shift = s;
+  const int threads = ctas > 1 ? kThreadsOf<true> : kThreadsOf<false>;
+  const void* kernel = ctas > 1 ? reinterpret_cast<const void*>(kv_compact_kernel<true>)
+                                : reinterpret_cast<const void*>(kv_compact_kernel<false>);
+  if (!allow_smem(kernel, kStages * kRows * kPieces * threads * 16 + kPlaces * threads * static_cast<int>(sizeof(Place)))) return -1;
+  // (a row of more pieces than two passes' worth takes several, the last of fewer: room for any chunk)
+  const int chunk = pieces > kPieces * threads ? threads : chunk_of(threads, pieces);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items * ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(kStages * kRows * kPieces * threads * 16 + kPlaces * chunk * static_cast<int>(sizeof(Place)));
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -218,8 +311,8 @@ int launch_kv_compact(const CompactArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return (ctas > 1 ? cudaLaunchKernelEx(&cfg, kv_compact_kernel<true>, a, planes, ctas, shift)
-                   : cudaLaunchKernelEx(&cfg, kv_compact_kernel<false>, a, planes, ctas, shift)) == cudaSuccess
+  return (ctas > 1 ? cudaLaunchKernelEx(&cfg, kv_compact_kernel<true>, a, ctas)
+                   : cudaLaunchKernelEx(&cfg, kv_compact_kernel<false>, a, ctas)) == cudaSuccess
              ? 0 : -1;
 }
 

@@ -189,7 +189,7 @@ int paged_kv_compact(const sa_compact_params* p, void* stream) {
   const int rc = pages_status(p->B, p->Hkv, p->page_tokens, p->max_pages, p->num_pages);
   if (rc != SA_OK) return rc;
   if (p->D <= 0 || p->width <= 0) return SA_ERR_SHAPE;
-  if (p->D > 1024 || p->width >= kMaxInt - (int64_t(1) << 17)) return SA_ERR_UNSUPPORTED;
+  if (p->D > 1024 || p->width >= kMaxInt - (int64_t(1) << 17) || p->num_pages * p->Hkv >= kMaxInt) return SA_ERR_UNSUPPORTED;
   if (fp8 && (!(p->D == 64 || p->D == 128 || p->D == 256) || p->page_tokens % 16 != 0)) return SA_ERR_UNSUPPORTED;
   const int64_t row = p->D * static_cast<int64_t>(es);
   const size_t pool = pool_bytes(p->Hkv, p->page_tokens, p->num_pages, row + (fp8 ? 1 : 0));
@@ -230,6 +230,7 @@ int paged_kv_compact(const sa_compact_params* p, void* stream) {
   for (int n : {4, 16})
     if (row % n == 0 && aligned(p->k_pool, n) && aligned(p->v_pool, n)) a.align = n;
   a.page_tokens = static_cast<int>(p->page_tokens);
+  a.shift = log2_of(p->page_tokens);
   a.max_pages = p->max_pages;
   a.num_pages = p->num_pages;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

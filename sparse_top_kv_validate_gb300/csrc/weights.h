@@ -67,7 +67,7 @@ struct CompactArgs {
   int B, Hkv, width;
   int row_bytes;              // of a row of K or V (codes only, for FP8 pages)
   int align;                  // bytes that every row of K and V is aligned to: 16, 4, 2
-  int page_tokens;
+  int page_tokens, shift;     // shift: log2(page_tokens), or -1
   int64_t max_pages, num_pages;
 };
 int launch_kv_compact(const CompactArgs& a, cudaStream_t st);

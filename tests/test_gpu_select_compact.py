@@ -224,6 +224,7 @@ def test_compaction_reports_bad_contexts_and_pages(cuda_lib):
     sa, lay = cuda_lib, Layout([100] * 3, [0] * 3, 16, seed=8)
     pools = wt.elements(lay, 1, 64, "bf16", 8)
     lay.table[0, 3] = -1
+    lay.table[0, 0] = 0                                     # (the page that the rows go to)
     keep = torch.tensor([[[40, 50, 60]], [[1, 2, 3]], [[1, 2, 3]]], dtype=torch.int32)
     ctx = torch.tensor([100, -5, 1 << 29], dtype=torch.int32, device=DEV)
     got, err = [p.to(DEV) for p in pools], torch.zeros(1, dtype=torch.int32, device=DEV)
@@ -232,8 +233,7 @@ def test_compaction_reports_bad_contexts_and_pages(cuda_lib):
     for x, p in zip(got, pools):  # token 50 lies on the page that does not exist: its row stays
         want = p.clone()
         page = lay.table[0].long()
-        want[page[0], 0, 0] = p[page[2], 0, 8]
-        want[page[0], 0, 2] = p[page[60 // 16], 0, 60 % 16] if page[3] >= 0 else want[page[0], 0, 2]
+        want[0, 0, 0] = p[page[2], 0, 8]
         assert torch.equal(x.cpu(), want)
 
 
