@@ -32,17 +32,30 @@ struct __align__(16) Place {
   int64_t from, to, scale, weight;
 };
 
-// A thread moves up to two rows of a chunk, two pieces of each at a time; chunks in the ring; the
-// chunks whose places are kept: those in the ring and the one behind them.
-constexpr int kRows = 2, kPieces = 2, kStages = 4, kPlaces = kStages + 1;
+// A thread moves up to kRows rows of a chunk, two pieces of each at a time; chunks in the ring; the
+// chunks whose places are kept: those in the ring and the one behind them.  A cluster's chunks
+// are larger, as its barrier costs more.
+constexpr int kPieces = 2;
 template <bool kCluster>
-constexpr int kThreadsOf = kCluster ? 256 : 128;
+struct Shape {
+  static constexpr int kThreads = kCluster ? 256 : 128;
+  static constexpr int kRows = kCluster ? 4 : 2;
+  static constexpr int kStages = kCluster ? 3 : 4;
+  static constexpr int kPlaces = kStages + 1;
+  static constexpr int kRing = kStages * kRows * kPieces * kThreads * 16;
 
-// Threads to a row of `pieces` pieces (at most kPieces * threads), rows of a CTA's part of a chunk.
-__host__ __device__ constexpr int lanes_of(int pieces) { return (pieces + kPieces - 1) / kPieces; }
-__host__ __device__ constexpr int chunk_of(int threads, int pieces) {
-  return lanes_of(pieces) == 1 ? threads : kRows * (threads / lanes_of(pieces));
-}
+  // Rows of a CTA's part of a chunk, for rows of `pieces` pieces (at most kPieces * kThreads).
+  static __host__ __device__ constexpr int chunk(int pieces) {
+    const int n = kRows * (kThreads / ((pieces + kPieces - 1) / kPieces));
+    return n < kThreads ? n : kThreads;  // (a thread finds one row)
+  }
+  static int bytes(int pieces) {  // of shared memory
+    // (a row of more pieces takes several passes, the last of fewer: room for any chunk)
+    const int rows = pieces > kPieces * kThreads ? kThreads : chunk(pieces);
+    return kRing + kPlaces * rows * static_cast<int>(sizeof(Place));
+  }
+  static constexpr int kMost = kRing + kPlaces * kThreads * static_cast<int>(sizeof(Place));
+};
 
 // The loads whose words were folded into x have returned once this has executed.
 __device__ __forceinline__ void arrived(uint32_t x) {
@@ -84,16 +97,17 @@ struct Planes {
 template <typename V, bool kCluster>
 __device__ void move_rows(const CompactArgs& a, const Planes& pl, const int32_t* table, const int32_t* keep, int head,
                           int m, int rank, int ctas, uint8_t* smem, bool& bad) {
-  constexpr int S = kStages, R = kPlaces, kThreads = kThreadsOf<kCluster>;
+  using H = Shape<kCluster>;
+  constexpr int S = H::kStages, R = H::kPlaces, kThreads = H::kThreads, kRows = H::kRows;
   const int tid = static_cast<int>(threadIdx.x);
   const uint32_t pt = static_cast<uint32_t>(a.page_tokens);
   const int all = a.row_bytes / static_cast<int>(sizeof(V));
   V* ring = reinterpret_cast<V*>(smem) + tid;  // piece q of row u of stage s: ring[((s * kRows + u) * kPieces + q) * kThreads]
-  Place* places = reinterpret_cast<Place*>(smem + S * kRows * kPieces * kThreads * 16);
+  Place* places = reinterpret_cast<Place*>(smem + H::kRing);
 #pragma unroll 1
   for (int col0 = 0; col0 < all; col0 += kPieces * kThreads) {  // (columns are independent of one another)
-    const int pieces = min(all - col0, kPieces * kThreads), lanes = lanes_of(pieces);
-    const int rows = kThreads / lanes, chunk = chunk_of(kThreads, pieces);
+    const int pieces = min(all - col0, kPieces * kThreads), lanes = (pieces + kPieces - 1) / kPieces;
+    const int rows = kThreads / lanes, chunk = H::chunk(pieces);
     const int r = tid / lanes, c = tid - r * lanes;  // this thread's first row of a chunk, and piece of it
     const int64_t step = static_cast<int64_t>(chunk) * ctas, own = static_cast<int64_t>(rank) * chunk;
     char* col = pl.rows + static_cast<int64_t>(col0 + c) * sizeof(V);
@@ -101,8 +115,7 @@ __device__ void move_rows(const CompactArgs& a, const Planes& pl, const int32_t*
     // ---- finding a chunk's rows, one to a thread
     auto list = [&](int64_t first) {
       const int64_t i = first + own + tid;
-      const int32_t j = tid < chunk && i < m ? __ldg(keep + i) : -1;
-      return j == i ? -1 : j;  // (-1: it is where it belongs)
+      return tid < chunk && i < m ? __ldg(keep + i) : -1;  // (looked at by pages(), a chunk on)
     };
     struct Found {
       int32_t from, to;  // pages
@@ -110,9 +123,9 @@ __device__ void move_rows(const CompactArgs& a, const Planes& pl, const int32_t*
       bool moving;
     };
     auto pages = [&](int64_t first, int32_t src) {
-      Found f{0, 0, 0, 0, src >= 0};
-      if (!f.moving) return f;
       const uint32_t x = static_cast<uint32_t>(src), y = static_cast<uint32_t>(first + own) + tid;
+      Found f{0, 0, 0, 0, src >= 0 && x != y};
+      if (!f.moving) return f;
       const uint32_t px = a.shift >= 0 ? x >> a.shift : x / pt, py = a.shift >= 0 ? y >> a.shift : y / pt;
       f.from = __ldg(table + px);
       f.to = __ldg(table + py);
@@ -183,20 +196,17 @@ __device__ void move_rows(const CompactArgs& a, const Planes& pl, const int32_t*
     // Chunk k: stage k % S of the ring, places k % R; its small values in scale / weight[k % S].
     // (The loop goes S chunks at a time, so that a value on its way stays in its register.)
     uint32_t scale[S], weight[S];
-    int32_t src[2];
-    Found found[2];
+    Found found[S];
 #pragma unroll
-    for (int s = 0; s < S; ++s) place(pages(s * step, list(s * step)), s, scale[s], weight[s]);
+    for (int s = 0; s < S; ++s) found[s] = pages(s * step, list(s * step));
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      found[x] = pages((S + x) * step, list((S + x) * step));
-      src[x] = list((S + 2 + x) * step);
-    }
+    for (int s = 0; s < S; ++s) place(found[s], s, scale[s], weight[s]);
+    Found ahead = pages(S * step, list(S * step));
+    int32_t src = list((S + 1) * step);
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) copy(s, s);
     int at = 0;
-    static_assert(S % 2 == 0, "the pages and entries ahead alternate");
 #pragma unroll 1
     for (int64_t first = 0; first < m; first += S * step) {
 #pragma unroll
@@ -208,9 +218,9 @@ __device__ void move_rows(const CompactArgs& a, const Planes& pl, const int32_t*
         arrived(now_scale ^ now_weight);
         arrive<kCluster>();
         copy((s + S - 1) % S, at + S - 1 < R ? at + S - 1 : at + S - 1 - R);
-        place(found[s & 1], at + S < R ? at + S : at + S - R, scale[s], weight[s]);
-        found[s & 1] = pages(now + (S + 2) * step, src[s & 1]);
-        src[s & 1] = list(now + (S + 4) * step);
+        place(ahead, at + S < R ? at + S : at + S - R, scale[s], weight[s]);
+        ahead = pages(now + (S + 1) * step, src);
+        src = list(now + (S + 2) * step);
         wait<kCluster>();
         store(s, at, now_scale, now_weight);
         if (++at == R) at = 0;
@@ -222,9 +232,9 @@ __device__ void move_rows(const CompactArgs& a, const Planes& pl, const int32_t*
 }
 
 template <bool kCluster>
-__global__ void __launch_bounds__(kThreadsOf<kCluster>)
+__global__ void __launch_bounds__(Shape<kCluster>::kThreads)
     kv_compact_kernel(const __grid_constant__ CompactArgs a, int ctas) {
-  constexpr int kThreads = kThreadsOf<kCluster>;
+  constexpr int kThreads = Shape<kCluster>::kThreads;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ int s_end, s_code;
   const int tid = static_cast<int>(threadIdx.x);
@@ -292,18 +302,16 @@ int launch_kv_compact(const CompactArgs& a, cudaStream_t st) {
   // than one chunk to move
   const int pieces = a.row_bytes / a.align;
   int ctas = 1;
-  while (ctas < kMaxCluster && items * ctas * 2 <= sm_count() && chunk_of(kThreadsOf<true>, pieces) * ctas / 2 < a.width) ctas *= 2;
+  const int64_t chunk = pieces > kPieces * Shape<true>::kThreads ? 1 : Shape<true>::chunk(pieces);
+  while (ctas < kMaxCluster && items * ctas * 2 <= sm_count() && chunk * ctas / 2 < a.width) ctas *= 2;
   if (items * ctas > INT32_MAX) return -1;
-  const int threads = ctas > 1 ? kThreadsOf<true> : kThreadsOf<false>;
   const void* kernel = ctas > 1 ? reinterpret_cast<const void*>(kv_compact_kernel<true>)
                                 : reinterpret_cast<const void*>(kv_compact_kernel<false>);
-  if (!allow_smem(kernel, kStages * kRows * kPieces * threads * 16 + kPlaces * threads * static_cast<int>(sizeof(Place)))) return -1;
-  // (a row of more pieces than two passes' worth takes several, the last of fewer: room for any chunk)
-  const int chunk = pieces > kPieces * threads ? threads : chunk_of(threads, pieces);
+  if (!allow_smem(kernel, ctas > 1 ? Shape<true>::kMost : Shape<false>::kMost)) return -1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items * ctas));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(kStages * kRows * kPieces * threads * 16 + kPlaces * chunk * static_cast<int>(sizeof(Place)));
+  cfg.blockDim = dim3(static_cast<unsigned>(ctas > 1 ? Shape<true>::kThreads : Shape<false>::kThreads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(ctas > 1 ? Shape<true>::bytes(pieces) : Shape<false>::bytes(pieces));
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
