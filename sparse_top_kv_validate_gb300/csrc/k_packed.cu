@@ -605,25 +605,6 @@ __device__ __forceinline__ uint64_t poly_logit2(uint64_t x, const float (&tq)[N]
   return f2_fma(x, q, add);
 }
 
-// 32 columns of a thread's row and the largest of them (kAbs: of their magnitudes),
-// found by the load itself.  Valid after tmem_ld_wait, m through arrived().
-template <bool kAbs>
-__device__ __forceinline__ void tmem_ld32_max(uint32_t addr, uint32_t (&r)[32], float& m) {
-#define SA_LD32_MAX(op)                                                                         \
-  asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32." op                                      \
-               ".f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20," \
-               "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"                       \
-               : SA_TC05_R32(r), "=f"(m)                                                         \
-               : "r"(addr))
-  if (kAbs) SA_LD32_MAX("max.abs");
-  else SA_LD32_MAX("max");
-#undef SA_LD32_MAX
-}
-__device__ __forceinline__ float arrived(float& m) {
-  asm volatile("" : "+f"(m));
-  return m;
-}
-
 // The largest magnitude of 32 scores.
 __device__ __forceinline__ float largest(const uint32_t (&r)[32]) {
   float ax[2] = {0.f, 0.f};
@@ -737,7 +718,7 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       tc05::fence_after_sync();
       uint32_t r[2][32];
       float mr[2];
-      tmem_ld32_max<kFixed>(tS + (kFixed ? 0 : 96), r[0], mr[0]);  // (the first pass goes backwards)
+      tc05::tmem_ld32_max<kFixed>(tS + (kFixed ? 0 : 96), r[0], mr[0]);  // (the first pass goes backwards)
       const int tok = it.tok + rt;
       // A row of no query is no reason to mask: nothing of it is kept, and it has no say in what
       // the warp does.  (As a row that sees nothing it sent every tile of a sequence's last item
@@ -774,12 +755,12 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       float mx = SA_NEG_INF;
       if (!kCap && !masked) {  // the loads find the maximum
         tc05::tmem_ld_wait();
-        mx = arrived(mr[0]);
+        mx = tc05::arrived(mr[0]);
 #pragma unroll 1
         for (int c = 2; c >= 0; --c) {
-          tmem_ld32_max<false>(tS + 32 * c, r[0], mr[0]);
+          tc05::tmem_ld32_max<false>(tS + 32 * c, r[0], mr[0]);
           tc05::tmem_ld_wait();
-          mx = fmaxf(mx, arrived(mr[0]));
+          mx = fmaxf(mx, tc05::arrived(mr[0]));
         }
       } else if (!kFixed) {
         float ax = 0.f;
@@ -827,14 +808,14 @@ __device__ void softmax_rows(const Params& p, const Work& work, uint8_t* sm, uin
       }
       const float neg_m = (kFixed || m == SA_NEG_INF) ? 0.0f : -m;
       auto load = [](uint32_t at, uint32_t (&x)[32], float& most) {
-        if (kFixed) tmem_ld32_max<true>(at, x, most);
+        if (kFixed) tc05::tmem_ld32_max<true>(at, x, most);
         else tc05::tmem_ld32(at, x);
       };
       auto exps = [&](uint32_t (&x)[32], int c, float& most) {
         const int rc = rel - 32 * c;
         uint32_t pk[16];
         const bool part = kCap && partial(c);
-        if (kFixed) mode = mode_of(arrived(most));
+        if (kFixed) mode = mode_of(tc05::arrived(most));
         if (!kCap && masked) exp_chunk<kPlain, true, T>(x, pk, lg, neg_m, rc, ls);
         else if (!kCap) exp_chunk<kPlain, false, T>(x, pk, lg, neg_m, 0, ls);
         else if (part && !__any_sync(0xffffffffu, live && rc >= 0)) {

@@ -24,8 +24,11 @@
 // leaves partial sums, merged in order by merge_kernel.
 //
 // Warps: 0 loads (outer tiles through two buffers, inner ones through a ring), 1 issues
-// the MMAs, 4-7 and 8-11 take the scores of one outer tile each, from two buffers of
-// tensor memory.  Every mbarrier wait is bounded; a stalled pipeline sets
+// the MMAs, 4-11 and 12-19 take the scores of one outer tile each, from two buffers of
+// tensor memory, a warpgroup half of the columns: a thread reads 64 scores at once, gives the
+// buffer back and then works on them, four warps to a scheduler (with two, and whole rows to a
+// thread, 432 us for 8 prompts of 2,048 tokens, 32 / 8 heads of 128).  A row's two halves
+// meet in the item's own outer tile, which its MMAs have read.  Every mbarrier wait is bounded; a stalled pipeline sets
 // SA_ERRBIT_TIMEOUT, stops every role, and still frees the tensor memory.
 #include <cuda.h>
 
@@ -41,10 +44,11 @@ namespace sa {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;           // 4 service warps, 4 warpgroups
 constexpr int kTile = 128;               // rows of a tile
 constexpr int kSlabBytes = kTile * 128;  // 128 rows x 64 sixteen-bit columns
 constexpr int kMaxSeqs = 1024;           // sequences per launch
+constexpr int kItems = 3;                // items worked out ahead
 constexpr int kLStages = 3;              // slots of the ring of row statistics
 constexpr float kRaiseLog2 = 8.0f;       // the offset of a row's sum is raised beyond 2^8
 
@@ -59,10 +63,12 @@ struct Geo {
   static constexpr int kOffBar = kOffL + kLStages * kTile * 4;
   static constexpr int kBarOFull = 0, kBarOEmpty = 2, kBarIFull = 4, kBarIEmpty = kBarIFull + kStages,
                        kBarLFull = kBarIEmpty + kStages, kBarLEmpty = kBarLFull + kLStages,
-                       kBarSFull = kBarLEmpty + kLStages, kBarSEmpty = kBarSFull + 4,  // [warpgroup][buffer]
-                       kBarDone = kBarSEmpty + 4, kNumBars = kBarDone + 1;
+                       kBarSFull = kBarLEmpty + kLStages, kBarSEmpty = kBarSFull + 4,  // [outer tile][buffer]
+                       kBarXFull = kBarSEmpty + 4, kBarXEmpty = kBarXFull + 2, kBarWFull = kBarXEmpty + 2,
+                       kBarWEmpty = kBarWFull + kItems, kBarDone = kBarWEmpty + kItems, kNumBars = kBarDone + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tensor memory, abort flag
-  static constexpr int kBytes = 1024 + kOffMisc + 8;
+  static constexpr int kOffItems = (kOffMisc + 8 + 15) / 16 * 16;
+  static constexpr int kBytes = 1024 + kOffItems + kItems * 64;
   static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
   static_assert(kStages * kTileBytes >= (kMaxSeqs + 1) * 8 + 64, "the ring serves as scratch");
 };
@@ -162,7 +168,7 @@ struct Items {
   }
 };
 
-// Where a walk over items stands; every role walks on its own from the same start.
+// Where the walk over this CTA's items stands.
 template <bool kSums>
 struct Walk {
   int b, h, o;
@@ -200,9 +206,55 @@ struct Walk {
   }
 };
 
-// A query tile's place among the rows' statistics, of Hkv (Tq / tpt + B + 1): each tile's own.
-__device__ __forceinline__ int64_t tile_id(const Params& p, int b, int q0, int tile, int h) {
-  return (q0 / p.tpt + p.b0 + b + tile) * static_cast<int64_t>(p.Hkv) + h;
+// An item as the roles take it: inner tiles [t0, t1), and those that its tile w has a visible
+// score in, [from[w], to[w]).
+struct __align__(16) Item {
+  int b, h, o;               // sequence (-1: no more items), KV head, item
+  int q0, nq, k0, nk;
+  int t0, t1, from[2], to[2];
+  int cut;                   // 0: whole; 1: begun by another CTA; 2: begun here, ended by another
+  int id;                    // the sequence's first query tile among the rows' statistics
+  int spare;
+};
+static_assert(sizeof(Item) == 64, "");
+
+// A query tile's place among the rows' statistics: of Hkv (Tq / tpt + B + 1), each tile's own.
+__device__ __forceinline__ int64_t tile_id(const Params& p, const Item& it, int tile) {
+  return (it.id + tile) * static_cast<int64_t>(p.Hkv) + it.h;
+}
+
+template <bool kSums>
+__device__ __forceinline__ Item item_of(const Params& p, const Walk<kSums>& wk, int64_t begin, int64_t end) {
+  Item it;
+  it.b = wk.b;
+  it.h = wk.h;
+  it.o = wk.o;
+  it.q0 = wk.s.q0;
+  it.nq = wk.s.nq;
+  it.k0 = wk.s.k0;
+  it.nk = wk.s.nk;
+  const int lo = static_cast<int>(max(begin - wk.off, int64_t(0)));
+  const int hi = static_cast<int>(min(end - wk.off, static_cast<int64_t>(wk.size)));
+  it.t0 = wk.first + lo;
+  it.t1 = wk.first + hi;
+  it.cut = lo > 0 ? 1 : hi < wk.size ? 2 : 0;
+  it.id = wk.s.q0 / p.tpt + p.b0 + wk.b;
+  it.spare = 0;
+  const int off = it.nk - it.nq;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    if (kSums) {
+      const int j = (it.o * 2 + w) * kTile, i = j - off;  // its first key; the first token that sees it
+      it.from[w] = max(it.t0, i > 0 ? i / p.tpt : 0);
+      it.to[w] = j < it.nk ? it.t1 : it.t0;
+    } else {
+      const int i = (it.o * 2 + w) * p.tpt;               // its first token; the last key that its last sees
+      const int last = min(i + p.tpt, it.nq) - 1 + off;
+      it.from[w] = it.t0;
+      it.to[w] = i < it.nq && last >= 0 ? min(it.t1, last / kTile + 1) : it.t0;
+    }
+  }
+  return it;
 }
 
 // ---- what a row ends with ------------------------------------------------------------------
@@ -210,28 +262,27 @@ __device__ __forceinline__ int64_t tile_id(const Params& p, int b, int q0, int t
 // kSums 0: -L of query row `row` of the item's tile w, from the row's offset and sum.
 // -inf, so that its keys get nothing, for a row that sees nothing but -inf and for one
 // that holds no query.
-__device__ __forceinline__ void put_row(const Params& p, const Walk<false>& wk, int w, int row, float m, float l) {
-  const int tile = 2 * wk.o + w, rt = row / p.g;
-  if (tile * p.tpt >= wk.s.nq) return;
-  const bool live = rt < p.tpt && tile * p.tpt + rt < wk.s.nq;
-  p.nlse[tile_id(p, wk.b, wk.s.q0, tile, wk.h) * kTile + row] =
-      !live || m == SA_NEG_INF ? SA_NEG_INF : -(m + log2f(l));
+__device__ __forceinline__ void put_row(const Params& p, const Item& it, int w, int row, float m, float l) {
+  const int tile = 2 * it.o + w, rt = row / p.g;
+  if (tile * p.tpt >= it.nq) return;
+  const bool live = rt < p.tpt && tile * p.tpt + rt < it.nq;
+  p.nlse[tile_id(p, it, tile) * kTile + row] = !live || m == SA_NEG_INF ? SA_NEG_INF : -(m + log2f(l));
 }
 
 // kSums 1: the weight of the item's key `row` of tile w.
-__device__ __forceinline__ void put_key(const Params& p, const Walk<true>& wk, int w, int row, float sum) {
-  const int j = wk.o * 2 * kTile + w * kTile + row;
-  if (j >= wk.s.nk) return;
+__device__ __forceinline__ void put_key(const Params& p, const Item& it, int w, int row, float sum) {
+  const int j = it.o * 2 * kTile + w * kTile + row;
+  if (j >= it.nk) return;
   const uint32_t pi = static_cast<uint32_t>(j) / static_cast<uint32_t>(p.page_tokens);
   int32_t page = -1;
-  if (pi < p.max_pages) page = __ldg(p.block_table + wk.b * p.max_pages + pi);
+  if (pi < p.max_pages) page = __ldg(p.block_table + it.b * p.max_pages + pi);
   if (page < 0 || page >= p.num_pages) {
     if (p.err_word) atomicOr(p.err_word, static_cast<uint32_t>(SA_ERRBIT_PAGE));
     return;
   }
   const int64_t slot = j - static_cast<int64_t>(pi) * p.page_tokens;
-  pool_put(p.weights + (page * static_cast<int64_t>(p.Hkv) + wk.h) * p.page_tokens + slot, sum,
-           p.accumulate && j < wk.s.nk - wk.s.nq);
+  pool_put(p.weights + (page * static_cast<int64_t>(p.Hkv) + it.h) * p.page_tokens + slot, sum,
+           p.accumulate && j < it.nk - it.nq);
 }
 
 // ---- roles -----------------------------------------------------------------------------------
@@ -241,57 +292,74 @@ struct Range {
   int64_t begin, end;
 };
 
+// Works the items out ahead of the other roles (a walk's divisions between two items would
+// hold up the lanes that issue the copies and the MMAs).
 template <int D, bool kSums>
-__device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const Params& p, Walk<kSums> wk, Range rg,
-                         uint8_t* sm, uint64_t* bars, volatile int* abort_flag) {
+__device__ void walker(const Params& p, Walk<kSums> wk, Range rg, uint8_t* sm, uint64_t* bars, volatile int* abort_flag) {
+  using G = Geo<D>;
+  int4 cut = make_int4(-1, 0, 0, 0);  // the item that this range begins and does not end, for merge_kernel
+  for (uint32_t n = 0;; ++n) {
+    const uint32_t slot = n % kItems, use = n / kItems;
+    const bool more = wk.b < p.B && wk.off < rg.end;
+    Item it;
+    if (more) it = item_of(p, wk, rg.begin, rg.end);
+    else it.b = -1;
+    if (more && it.cut == 2)
+      cut = make_int4(it.b, it.h, it.o, static_cast<int>((wk.off + wk.size - 1) / (rg.end - rg.begin)));
+    if (use > 0 && !wait_or_abort(&bars[G::kBarWEmpty + slot], (use - 1) & 1, abort_flag, p.err_word)) break;
+    *reinterpret_cast<Item*>(sm + G::kOffItems + slot * 64) = it;
+    mbar_arrive(&bars[G::kBarWFull + slot]);
+    if (!more) break;
+    wk.next(p);
+  }
+  p.cut[blockIdx.x] = cut;
+}
+
+template <int D, bool kSums>
+__device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const Params& p, uint8_t* sm, uint64_t* bars,
+                         volatile int* abort_flag) {
   using G = Geo<D>;
   const uint32_t q_bytes = static_cast<uint32_t>(G::kSlabs * p.g * p.tpt * 128);
-  uint32_t items = 0, inner = 0;
-  bool ok = true;
+  uint32_t items = 0, inner = 0, slot = 0, use = 0, ls = 0, lu = 0;
   auto load = [&](uint8_t* dst, bool query, int h, int token, uint64_t* bar) {
 #pragma unroll
     for (int s = 0; s < G::kSlabs; ++s)
       if (query) tc05::tma_load3(dst + s * kSlabBytes, tq, s * 64, h * p.g, token, bar);
       else tc05::tma_load3(dst + s * kSlabBytes, tk, s * 64, h, token, bar);
   };
-  for (; ok && wk.b < p.B && wk.off < rg.end; wk.next(p), ++items) {
+  bool ok = true;
+  for (uint32_t n = 0; ok; ++n) {
+    if (!wait_or_abort(&bars[G::kBarWFull + n % kItems], (n / kItems) & 1, abort_flag, p.err_word)) break;
+    const Item it = *reinterpret_cast<const Item*>(sm + G::kOffItems + (n % kItems) * 64);
+    mbar_arrive(&bars[G::kBarWEmpty + n % kItems]);
+    if (it.b < 0) break;
     const uint32_t ob = items & 1;
     if (items >= 2 && !wait_or_abort(&bars[G::kBarOEmpty + ob], ((items >> 1) - 1) & 1, abort_flag, p.err_word)) break;
     uint8_t* outer = sm + G::kOffOuter + ob * 2 * G::kTileBytes;
-    if (kSums) {
-      const int j = wk.o * 2 * kTile;
-      const bool two = j + kTile < wk.s.nk;
-      mbar_arrive_expect_tx(&bars[G::kBarOFull + ob], (two ? 2 : 1) * G::kTileBytes);
-      load(outer, false, wk.h, wk.s.k0 + j, &bars[G::kBarOFull + ob]);
-      if (two) load(outer + G::kTileBytes, false, wk.h, wk.s.k0 + j + kTile, &bars[G::kBarOFull + ob]);
-    } else {
-      const int i = wk.o * 2 * p.tpt;
-      const bool two = i + p.tpt < wk.s.nq;
-      mbar_arrive_expect_tx(&bars[G::kBarOFull + ob], (two ? 2 : 1) * q_bytes);
-      load(outer, true, wk.h, wk.s.q0 + i, &bars[G::kBarOFull + ob]);
-      if (two) load(outer + G::kTileBytes, true, wk.h, wk.s.q0 + i + p.tpt, &bars[G::kBarOFull + ob]);
-    }
-    const int lo = static_cast<int>(max(rg.begin - wk.off, int64_t(0)));
-    const int hi = static_cast<int>(min(rg.end - wk.off, static_cast<int64_t>(wk.size)));
-    for (int x = lo; ok && x < hi; ++x, ++inner) {
-      const int t = wk.first + x;
-      const uint32_t slot = inner % G::kStages, use = inner / G::kStages;
+    const int first = kSums ? it.o * 2 * kTile : it.o * 2 * p.tpt, next = kSums ? kTile : p.tpt;
+    const bool two = first + next < (kSums ? it.nk : it.nq);
+    const int row0 = (kSums ? it.k0 : it.q0) + first;
+    mbar_arrive_expect_tx(&bars[G::kBarOFull + ob], (two ? 2 : 1) * (kSums ? G::kTileBytes : q_bytes));
+    load(outer, !kSums, it.h, row0, &bars[G::kBarOFull + ob]);
+    if (two) load(outer + G::kTileBytes, !kSums, it.h, row0 + next, &bars[G::kBarOFull + ob]);
+    ++items;
+    const float* nlse = p.nlse + tile_id(p, it, it.t0) * kTile;
+    int token = kSums ? it.q0 + it.t0 * p.tpt : it.k0 + it.t0 * kTile;
+    for (int t = it.t0; t < it.t1; ++t) {
       ok = use == 0 || wait_or_abort(&bars[G::kBarIEmpty + slot], (use - 1) & 1, abort_flag, p.err_word);
+      if (ok && kSums) ok = lu == 0 || wait_or_abort(&bars[G::kBarLEmpty + ls], (lu - 1) & 1, abort_flag, p.err_word);
       if (!ok) break;
-      uint8_t* dst = sm + G::kOffInner + slot * G::kTileBytes;
+      mbar_arrive_expect_tx(&bars[G::kBarIFull + slot], kSums ? q_bytes : G::kTileBytes);
+      load(sm + G::kOffInner + slot * G::kTileBytes, kSums, it.h, token, &bars[G::kBarIFull + slot]);
       if (kSums) {
-        const uint32_t ls = inner % kLStages, lu = inner / kLStages;
-        ok = lu == 0 || wait_or_abort(&bars[G::kBarLEmpty + ls], (lu - 1) & 1, abort_flag, p.err_word);
-        if (!ok) break;
         mbar_arrive_expect_tx(&bars[G::kBarLFull + ls], kTile * 4);
-        bulk_g2s(sm + G::kOffL + ls * kTile * 4, p.nlse + tile_id(p, wk.b, wk.s.q0, t, wk.h) * kTile, kTile * 4,
-                 &bars[G::kBarLFull + ls]);
-        mbar_arrive_expect_tx(&bars[G::kBarIFull + slot], q_bytes);
-        load(dst, true, wk.h, wk.s.q0 + t * p.tpt, &bars[G::kBarIFull + slot]);
-      } else {
-        mbar_arrive_expect_tx(&bars[G::kBarIFull + slot], G::kTileBytes);
-        load(dst, false, wk.h, wk.s.k0 + t * kTile, &bars[G::kBarIFull + slot]);
+        bulk_g2s(sm + G::kOffL + ls * kTile * 4, nlse, kTile * 4, &bars[G::kBarLFull + ls]);
+        nlse += static_cast<int64_t>(p.Hkv) * kTile;
+        if (++ls == kLStages) ls = 0, ++lu;
       }
+      token += kSums ? p.tpt : kTile;
+      ++inner;
+      if (++slot == G::kStages) slot = 0, ++use;
     }
   }
   if (*abort_flag) {
@@ -305,54 +373,43 @@ __device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const Par
   }
 }
 
-// Whether the item's tile w has a visible score in inner tile t (the MMA lane and the
-// warpgroups decide alike).
-template <bool kSums>
-__device__ __forceinline__ bool wanted(const Params& p, const Walk<kSums>& wk, int w, int t) {
-  const int off = wk.s.nk - wk.s.nq;
-  if (kSums) {
-    const int j = (wk.o * 2 + w) * kTile;  // its first key
-    return j < wk.s.nk && j <= min((t + 1) * p.tpt, wk.s.nq) - 1 + off;
-  }
-  const int i = (wk.o * 2 + w) * p.tpt;    // its first token
-  return i < wk.s.nq && t * kTile <= min(i + p.tpt, wk.s.nq) - 1 + off;
-}
-
-template <int D, bool kBf16, bool kSums>
-__device__ void mma_lane(const Params& p, Walk<kSums> wk, Range rg, uint8_t* sm, uint64_t* bars, uint32_t tmem,
-                         volatile int* abort_flag) {
+template <int D, bool kBf16>
+__device__ void mma_lane(const Params& p, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
   using G = Geo<D>;
   constexpr uint32_t id = tc05::idesc_f16(kTile, kTile, kBf16, false, false);
   const uint64_t dO = tc05::sw128_desc(smem_u32(sm + G::kOffOuter), 16, 1024);
   const uint64_t dI = tc05::sw128_desc(smem_u32(sm + G::kOffInner), 16, 1024);
-  uint32_t items = 0, inner = 0, cnt[2] = {0, 0};
+  uint32_t items = 0, slot = 0, parity = 0, cnt[2] = {0, 0};
   bool ok = true;
-  for (; ok && wk.b < p.B && wk.off < rg.end; wk.next(p), ++items) {
+  for (uint32_t n = 0; ok; ++n, ++items) {
+    if (!wait_or_abort(&bars[G::kBarWFull + n % kItems], (n / kItems) & 1, abort_flag, p.err_word)) break;
+    const Item it = *reinterpret_cast<const Item*>(sm + G::kOffItems + (n % kItems) * 64);
+    mbar_arrive(&bars[G::kBarWEmpty + n % kItems]);
+    if (it.b < 0) break;
     const uint32_t ob = items & 1;
     ok = wait_or_abort(&bars[G::kBarOFull + ob], (items >> 1) & 1, abort_flag, p.err_word);
-    const int lo = static_cast<int>(max(rg.begin - wk.off, int64_t(0)));
-    const int hi = static_cast<int>(min(rg.end - wk.off, static_cast<int64_t>(wk.size)));
-    for (int x = lo; ok && x < hi; ++x, ++inner) {
-      const uint32_t slot = inner % G::kStages;
-      ok = wait_or_abort(&bars[G::kBarIFull + slot], (inner / G::kStages) & 1, abort_flag, p.err_word);
+    const uint64_t a0 = dO + ((ob * 2 * G::kTileBytes) >> 4);
+    for (int t = it.t0; ok && t < it.t1; ++t) {
+      ok = wait_or_abort(&bars[G::kBarIFull + slot], parity, abort_flag, p.err_word);
       if (!ok) break;
+      const uint64_t b0 = dI + ((slot * G::kTileBytes) >> 4);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        if (!ok || !wanted<kSums>(p, wk, w, wk.first + x)) continue;
+        if (t < it.from[w] || t >= it.to[w]) continue;
         const uint32_t buf = cnt[w] & 1, use = cnt[w] >> 1;
-        ok = use == 0 || wait_or_abort(&bars[G::kBarSEmpty + 2 * w + buf], (use - 1) & 1, abort_flag, p.err_word);
-        if (!ok) continue;
+        ok = ok && (use == 0 || wait_or_abort(&bars[G::kBarSEmpty + 2 * w + buf], (use - 1) & 1, abort_flag, p.err_word));
+        if (!ok) break;
         tc05::fence_after_sync();
-        const uint64_t a0 = dO + (((ob * 2 + w) * G::kTileBytes) >> 4), b0 = dI + ((slot * G::kTileBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t o = ((kk / 4) * kSlabBytes + (kk % 4) * 32) >> 4;
-          tc05::mma_ss(tmem + (2 * w + buf) * kTile, a0 + o, b0 + o, id, kk > 0 ? 1u : 0u);
+          tc05::mma_ss(tmem + (2 * w + buf) * kTile, a0 + ((w * G::kTileBytes) >> 4) + o, b0 + o, id, kk > 0 ? 1u : 0u);
         }
         tc05::commit(&bars[G::kBarSFull + 2 * w + buf]);
         ++cnt[w];
       }
       tc05::commit(&bars[G::kBarIEmpty + slot]);
+      if (++slot == G::kStages) slot = 0, parity ^= 1;
     }
     tc05::commit(&bars[G::kBarOEmpty + ob]);
   }
@@ -390,99 +447,97 @@ __device__ __forceinline__ void add_columns(const uint32_t (&r)[32], uint64_t c2
 }
 
 template <int D, bool kSums>
-__device__ void rows(const Params& p, Walk<kSums> wk, Range rg, uint8_t* sm, uint64_t* bars, uint32_t tmem,
-                     volatile int* abort_flag) {
+__device__ void rows(const Params& p, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
   using G = Geo<D>;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const int w = (warp - 4) >> 2;
-  const int row = ((warp & 3) << 5) | lane;
-  const uint32_t tS0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * w * kTile;
-  const uint32_t nl0 = smem_u32(sm + G::kOffL);
+  const int w = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
+  const int row = ((warp & 3) << 5) | lane, col0 = half * 64;
+  const uint32_t tS0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * w * kTile + col0;
+  const uint32_t nl0 = smem_u32(sm + G::kOffL) + col0 * 4;
   const float c = p.c_log2;
   const uint64_t c2 = f2_pack(c, c);
   const int rt = row / p.g;  // token of its tile that a query row belongs to
-  uint32_t inner = 0, cnt = 0;
-  if (w == 0 && row == 0) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  for (; wk.b < p.B && wk.off < rg.end; wk.next(p)) {
-    const int lo = static_cast<int>(max(rg.begin - wk.off, int64_t(0)));
-    const int hi = static_cast<int>(min(rg.end - wk.off, static_cast<int64_t>(wk.size)));
-    const int off = wk.s.nk - wk.s.nq;
+  uint32_t cnt = 0, ls = 0, lp = 0;
+  for (uint32_t items = 0;; ++items) {
+    const uint32_t ws = items % kItems;
+    if (!wait_or_abort_warp(&bars[G::kBarWFull + ws], (items / kItems) & 1, abort_flag, p.err_word)) return;
+    const Item& it = *reinterpret_cast<const Item*>(sm + G::kOffItems + ws * 64);  // (ours until the item's end)
+    if (it.b < 0) return;
+    const int nq = it.nq, nk = it.nk, off = nk - nq, t1 = it.t1, from_t = it.from[w], to_t = it.to[w];
+    const int tile = 2 * it.o + w;
     float m = SA_NEG_INF, total = 0.f;  // a query row's offset; the sum
-    for (int x = lo; x < hi; ++x, ++inner) {
-      const int t = wk.first + x;
-      const uint32_t ls = inner % kLStages;
+    for (int t = it.t0; t < t1; ++t) {
       // (for a tile that is not wanted too: its slot is passed on once, in its turn)
-      if (kSums && !wait_or_abort_warp(&bars[G::kBarLFull + ls], (inner / kLStages) & 1, abort_flag, p.err_word)) return;
-      if (wanted<kSums>(p, wk, w, t)) {
+      if (kSums && !wait_or_abort_warp(&bars[G::kBarLFull + ls], lp, abort_flag, p.err_word)) return;
+      if (t >= from_t && t < to_t) {
         const uint32_t buf = cnt & 1, tS = tS0 + buf * kTile;
         if (!wait_or_abort_warp(&bars[G::kBarSFull + 2 * w + buf], (cnt >> 1) & 1, abort_flag, p.err_word)) return;
         ++cnt;
         tc05::fence_after_sync();
         uint32_t r[2][32];
-        tc05::tmem_ld32(tS, r[0]);
+        float mx[2];
+        if (kSums) {
+          tc05::tmem_ld32(tS, r[0]);
+          tc05::tmem_ld32(tS + 32, r[1]);
+        } else {
+          tc05::tmem_ld32_max<false>(tS, r[0], mx[0]);
+          tc05::tmem_ld32_max<false>(tS + 32, r[1], mx[1]);
+        }
+        tc05::tmem_ld_wait();
+        tc05::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[G::kBarSEmpty + 2 * w + buf]);
         uint64_t s2[2] = {0, 0};
         if (kSums) {
           // visible columns: queries that see this key, of this sequence
           const int tok = t * p.tpt;
-          const int end = min(p.tpt, wk.s.nq - tok) * p.g;
-          const int key = (wk.o * 2 + w) * kTile + row;
-          const int from = max(key - off - tok, 0) * p.g;
+          const int end = min(p.tpt, nq - tok) * p.g - col0;
+          const int key = tile * kTile + row;
+          const int from = max(key - off - tok, 0) * p.g - col0;
           // (rows that no query fills hold zeros, and -inf for -L)
-          const bool plain = tok + p.tpt <= wk.s.nq && __all_sync(0xffffffffu, from == 0);
+          const bool plain = tok + p.tpt <= nq && __all_sync(0xffffffffu, from <= 0);
           const uint32_t nl = nl0 + ls * kTile * 4;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tc05::tmem_ld_wait();
-            if (q < 3) tc05::tmem_ld32(tS + 32 * (q + 1), r[(q + 1) & 1]);
-            if (plain) add_columns<false>(r[q & 1], c2, nl + q * 128, 0, 0, s2);
-            else if (32 * q < end) add_columns<true>(r[q & 1], c2, nl + q * 128, from - 32 * q, end - 32 * q, s2);
+          for (int q = 0; q < 2; ++q) {
+            if (plain) add_columns<false>(r[q], c2, nl + q * 128, 0, 0, s2);
+            else if (32 * q < end) add_columns<true>(r[q], c2, nl + q * 128, from - 32 * q, end - 32 * q, s2);
           }
         } else {
-          const int tok = (wk.o * 2 + w) * p.tpt + rt;
-          const bool live = rt < p.tpt && tok < wk.s.nq;
+          const int tok = tile * p.tpt + rt;
+          const bool live = rt < p.tpt && tok < nq;
           // the last visible column (rows that hold no query do not mask)
-          const int last = live ? min(wk.s.nk - 1, tok + off) - t * kTile : kTile;
-          const bool plain = __all_sync(0xffffffffu, last >= kTile - 1);
+          const int last = live ? min(nk - 1, tok + off) - t * kTile - col0 : kTile;
+          float top;
+          if (__all_sync(0xffffffffu, last >= 63)) {
+            top = fmaxf(tc05::arrived(mx[0]), tc05::arrived(mx[1])) * c;
+          } else {
+            top = SA_NEG_INF;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t(&v)[32] = r[q & 1];
-            tc05::tmem_ld_wait();
-            if (q < 3) tc05::tmem_ld32(tS + 32 * (q + 1), r[(q + 1) & 1]);
-            float mx[2] = {SA_NEG_INF, SA_NEG_INF};
-            if (!plain) {
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (32 * q + i > last) v[i] = __float_as_uint(SA_NEG_INF);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              mx[i & 1] = max3(mx[i & 1], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            const float top = fmaxf(mx[0], mx[1]) * c;
-            const bool up = live && (top > m + kRaiseLog2 || (m == SA_NEG_INF && top > m));
-            if (__any_sync(0xffffffffu, up)) {
-              if (up) {
-                const float f = ex2(m - top);
-                const uint64_t f2 = f2_pack(f, f);
-                total *= f;
-                s2[0] = f2_mul(s2[0], f2);
-                s2[1] = f2_mul(s2[1], f2);
-                m = top;
+              for (int i = 0; i < 32; ++i) {
+                if (32 * q + i > last) r[q][i] = __float_as_uint(SA_NEG_INF);
+                top = fmaxf(top, __uint_as_float(r[q][i]));
               }
-            }
-            // a row of nothing but NaN scores keeps the offset -inf, and 0 in its place
-            const float n = m == SA_NEG_INF ? 0.f : -m;
-            const uint64_t n2 = f2_pack(n, n);
+            top *= c;
+          }
+          const bool up = live && (top > m + kRaiseLog2 || (m == SA_NEG_INF && top > m));
+          if (up) {
+            total *= ex2(m - top);
+            m = top;
+          }
+          // a row of nothing but NaN scores keeps the offset -inf, and 0 in its place
+          const float n = m == SA_NEG_INF ? 0.f : -m;
+          const uint64_t n2 = f2_pack(n, n);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float a, b;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), c2, n2), a, b);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(r[q][2 * i]), __uint_as_float(r[q][2 * i + 1])), c2, n2), a, b);
               s2[i & 1] = f2_add(s2[i & 1], f2_pack(ex2(a), ex2(b)));
             }
-          }
         }
-        tc05::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[G::kBarSEmpty + 2 * w + buf]);
         float a, b;
         f2_unpack(f2_add(s2[0], s2[1]), a, b);
         total += a + b;
@@ -490,18 +545,48 @@ __device__ void rows(const Params& p, Walk<kSums> wk, Range rg, uint8_t* sm, uin
       if (kSums) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[G::kBarLEmpty + ls]);
+        if (++ls == kLStages) ls = 0, lp ^= 1;
       }
     }
     if (!kSums && m == SA_NEG_INF && total != total) m = 0.f;  // NaN scores alone
-    if (lo == 0 && hi == wk.size) {
-      if constexpr (kSums) put_key(p, wk, w, row, total);
-      else put_row(p, wk, w, row, m, total);
-    } else {
-      p.part[(static_cast<int64_t>(blockIdx.x) * 2 + (lo > 0 ? 0 : 1)) * 256 + w * kTile + row] = make_float2(total, m);
-      // begun here and ended by another CTA: for merge_kernel
-      if (lo == 0 && w == 0 && row == 0)
-        p.cut[blockIdx.x] = make_int4(wk.b, wk.h, wk.o, static_cast<int>((wk.off + wk.size - 1) / (rg.end - rg.begin)));
+
+    // the two halves, in the item's outer tile: its copy has landed and its MMAs have read it
+    const uint32_t ob = items & 1;
+    float2* meet = reinterpret_cast<float2*>(sm + G::kOffOuter + (ob * 2 + w) * G::kTileBytes) + row;
+    if (half == 1) {
+      if (!wait_or_abort_warp(&bars[G::kBarOFull + ob], (items >> 1) & 1, abort_flag, p.err_word)) return;
+      if (items > 0 && !wait_or_abort_warp(&bars[G::kBarXEmpty + w], (items - 1) & 1, abort_flag, p.err_word)) return;
+      *meet = make_float2(total, m);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars[G::kBarXFull + w]);
+        mbar_arrive(&bars[G::kBarWEmpty + ws]);
+      }
+      continue;
     }
+    if (!wait_or_abort_warp(&bars[G::kBarXFull + w], items & 1, abort_flag, p.err_word)) return;
+    const float2 other = *meet;
+    fence_proxy_async_smem();  // the tile becomes a target of TMA again
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&bars[G::kBarXEmpty + w]);
+      mbar_arrive(&bars[G::kBarOEmpty + ob]);
+    }
+    if (kSums) {
+      total += other.x;
+    } else {
+      const float top = fmaxf(m, other.y);
+      total = top == SA_NEG_INF ? total + other.x : total * ex2(m - top) + other.x * ex2(other.y - top);
+      m = top;
+    }
+    if (it.cut == 0) {
+      if constexpr (kSums) put_key(p, it, w, row, total);
+      else put_row(p, it, w, row, m, total);
+    } else {
+      p.part[(static_cast<int64_t>(blockIdx.x) * 2 + it.cut - 1) * 256 + w * kTile + row] = make_float2(total, m);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[G::kBarWEmpty + ws]);
   }
 }
 
@@ -524,7 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[G::kBarOFull + i], 1);
-      mbar_init(&bars[G::kBarOEmpty + i], 1);
+      mbar_init(&bars[G::kBarOEmpty + i], 9);  // the MMAs, and the warps that read the halves
+      mbar_init(&bars[G::kBarXFull + i], 4);
+      mbar_init(&bars[G::kBarXEmpty + i], 4);
     }
     for (int s = 0; s < G::kStages; ++s) {
       mbar_init(&bars[G::kBarIFull + s], 1);
@@ -532,11 +619,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kLStages; ++s) {
       mbar_init(&bars[G::kBarLFull + s], 1);
-      mbar_init(&bars[G::kBarLEmpty + s], 8);  // both warpgroups
+      mbar_init(&bars[G::kBarLEmpty + s], 16);  // all warpgroups
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars[G::kBarSFull + i], 1);
-      mbar_init(&bars[G::kBarSEmpty + i], 4);
+      mbar_init(&bars[G::kBarSEmpty + i], 8);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bars[G::kBarWFull + i], 1);
+      mbar_init(&bars[G::kBarWEmpty + i], 18);  // the producer, the MMA lane, 16 warps
     }
     mbar_init(&bars[G::kBarDone], 1);
     *abort_flag = 0;
@@ -581,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   rg.end = min(rg.begin + R, pairs);
   Walk<kSums> wk{};
   wk.b = p.B;
-  if (rg.begin < rg.end) {  // (every warp alike)
+  if (warp == 2 && rg.begin < rg.end) {  // (the walker's)
     // the last of n ascending places, the first of them 0, that is not past x
     auto find = [&](int n, int64_t x, auto&& place) {
       int lo = 0, hi = n;
@@ -620,11 +711,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) producer<D, kSums>(&tq, &tk, p, wk, rg, sm, bars, abort_flag);
+    if (lane == 0) producer<D, kSums>(&tq, &tk, p, sm, bars, abort_flag);
   } else if (warp == 1) {
-    if (lane == 0) mma_lane<D, kBf16, kSums>(p, wk, rg, sm, bars, tmem, abort_flag);
+    if (lane == 0) mma_lane<D, kBf16>(p, sm, bars, tmem, abort_flag);
+  } else if (warp == 2) {
+    if (lane == 0) walker<D, kSums>(p, wk, rg, sm, bars, abort_flag);
   } else if (warp >= 4) {
-    rows<D, kSums>(p, wk, rg, sm, bars, tmem, abort_flag);
+    rows<D, kSums>(p, sm, bars, tmem, abort_flag);
   }
   __syncwarp();
   tc05::fence_before_sync();
@@ -643,17 +736,20 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Para
   pdl_launch_dependents();
   const int4 c = p.cut[blockIdx.x];
   if (c.x < 0) return;
-  Walk<kSums> wk{};
-  wk.b = c.x;
-  wk.h = c.y;
-  wk.o = c.z;
-  wk.s = seq_of(p, c.x);
+  const Seq q = seq_of(p, c.x);
+  Item it;
+  it.b = c.x;
+  it.h = c.y;
+  it.o = c.z;
+  it.nq = q.nq;
+  it.nk = q.nk;
+  it.id = q.q0 / p.tpt + p.b0 + c.x;
   const int x = static_cast<int>(threadIdx.x);
   auto part = [&](int cta) { return __ldg(p.part + (static_cast<int64_t>(cta) * 2 + (cta == static_cast<int>(blockIdx.x) ? 1 : 0)) * 256 + x); };
   if constexpr (kSums) {
     float sum = 0.f;
     for (int i = blockIdx.x; i <= c.w; ++i) sum += part(i).x;
-    put_key(p, wk, x / kTile, x % kTile, sum);
+    put_key(p, it, x / kTile, x % kTile, sum);
   } else {
     float m = SA_NEG_INF, l = 0.f;
     for (int i = blockIdx.x; i <= c.w; ++i) {
@@ -663,7 +759,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Para
       l = l * ex2(m - up) + e.x * ex2(e.y - up);
       m = up;
     }
-    put_row(p, wk, x / kTile, x % kTile, m, l);
+    put_row(p, it, x / kTile, x % kTile, m, l);
   }
 }
 

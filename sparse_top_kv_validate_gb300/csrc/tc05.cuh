@@ -144,6 +144,25 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// 32 columns of a thread's row and the largest of them (kAbs: of their magnitudes),
+// found by the load itself.  Valid after tmem_ld_wait, m through arrived().
+template <bool kAbs>
+__device__ __forceinline__ void tmem_ld32_max(uint32_t addr, uint32_t (&r)[32], float& m) {
+#define SA_LD32_MAX(op)                                                                         \
+  asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32." op                                      \
+               ".f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20," \
+               "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"                       \
+               : SA_TC05_R32(r), "=f"(m)                                                         \
+               : "r"(addr))
+  if (kAbs) SA_LD32_MAX("max.abs");
+  else SA_LD32_MAX("max");
+#undef SA_LD32_MAX
+}
+__device__ __forceinline__ float arrived(float& m) {
+  asm volatile("" : "+f"(m));
+  return m;
+}
+
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
