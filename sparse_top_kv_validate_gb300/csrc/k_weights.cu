@@ -24,7 +24,7 @@
 // leaves partial sums, merged in order by merge_kernel.
 //
 // Warps: 0 loads (outer tiles through two buffers, inner ones through a ring), 1 issues
-// the MMAs, 4-11 and 12-19 take the scores of one outer tile each, from two buffers of
+// and 3 issue the MMAs of one outer tile each, 2 works out the items, 4-11 and 12-19 take the scores of one outer tile each, from two buffers of
 // tensor memory, a warpgroup half of the columns: a thread reads 64 scores at once, gives the
 // buffer back and then works on them, four warps to a scheduler (with two, and whole rows to a
 // thread, 432 us for 8 prompts of 2,048 tokens, 32 / 8 heads of 128).  A row's two halves
@@ -65,7 +65,7 @@ struct Geo {
                        kBarLFull = kBarIEmpty + kStages, kBarLEmpty = kBarLFull + kLStages,
                        kBarSFull = kBarLEmpty + kLStages, kBarSEmpty = kBarSFull + 4,  // [outer tile][buffer]
                        kBarXFull = kBarSEmpty + 4, kBarXEmpty = kBarXFull + 2, kBarWFull = kBarXEmpty + 2,
-                       kBarWEmpty = kBarWFull + kItems, kBarDone = kBarWEmpty + kItems, kNumBars = kBarDone + 1;
+                       kBarWEmpty = kBarWFull + kItems, kBarDone = kBarWEmpty + kItems, kNumBars = kBarDone + 2;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tensor memory, abort flag
   static constexpr int kOffItems = (kOffMisc + 8 + 15) / 16 * 16;
   static constexpr int kBytes = 1024 + kOffItems + kItems * 64;
@@ -373,49 +373,53 @@ __device__ void producer(const CUtensorMap* tq, const CUtensorMap* tk, const Par
   }
 }
 
+// The MMAs of outer tile w.  (A lane each: with one for both, its own instructions, 1,950
+// cycles of them for the 1,090 that the MMAs of an inner tile take, were the bound.)
 template <int D, bool kBf16>
-__device__ void mma_lane(const Params& p, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
+__device__ void mma_lane(const Params& p, int w, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
   using G = Geo<D>;
   constexpr uint32_t id = tc05::idesc_f16(kTile, kTile, kBf16, false, false);
   const uint64_t dO = tc05::sw128_desc(smem_u32(sm + G::kOffOuter), 16, 1024);
   const uint64_t dI = tc05::sw128_desc(smem_u32(sm + G::kOffInner), 16, 1024);
-  uint32_t items = 0, slot = 0, parity = 0, cnt[2] = {0, 0};
+  const uint32_t tS = tmem + 2 * w * kTile;
+  uint32_t items = 0, slot = 0, parity = 0, cnt = 0;
   bool ok = true;
   for (uint32_t n = 0; ok; ++n, ++items) {
     if (!wait_or_abort(&bars[G::kBarWFull + n % kItems], (n / kItems) & 1, abort_flag, p.err_word)) break;
-    const Item it = *reinterpret_cast<const Item*>(sm + G::kOffItems + (n % kItems) * 64);
+    const Item& it = *reinterpret_cast<const Item*>(sm + G::kOffItems + (n % kItems) * 64);
+    const int b = it.b, first = it.t0, end = it.t1, from = it.from[w], to = it.to[w];
     mbar_arrive(&bars[G::kBarWEmpty + n % kItems]);
-    if (it.b < 0) break;
+    if (b < 0) break;
     const uint32_t ob = items & 1;
     ok = wait_or_abort(&bars[G::kBarOFull + ob], (items >> 1) & 1, abort_flag, p.err_word);
-    const uint64_t a0 = dO + ((ob * 2 * G::kTileBytes) >> 4);
-    for (int t = it.t0; ok && t < it.t1; ++t) {
+    const uint64_t a0 = dO + (((ob * 2 + w) * G::kTileBytes) >> 4);
+    for (int t = first; ok && t < end; ++t) {
       ok = wait_or_abort(&bars[G::kBarIFull + slot], parity, abort_flag, p.err_word);
       if (!ok) break;
-      const uint64_t b0 = dI + ((slot * G::kTileBytes) >> 4);
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (t < it.from[w] || t >= it.to[w]) continue;
-        const uint32_t buf = cnt[w] & 1, use = cnt[w] >> 1;
-        ok = ok && (use == 0 || wait_or_abort(&bars[G::kBarSEmpty + 2 * w + buf], (use - 1) & 1, abort_flag, p.err_word));
+      if (t >= from && t < to) {
+        const uint64_t b0 = dI + ((slot * G::kTileBytes) >> 4);
+        const uint32_t buf = cnt & 1, use = cnt >> 1;
+        ok = use == 0 || wait_or_abort(&bars[G::kBarSEmpty + 2 * w + buf], (use - 1) & 1, abort_flag, p.err_word);
         if (!ok) break;
         tc05::fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t o = ((kk / 4) * kSlabBytes + (kk % 4) * 32) >> 4;
-          tc05::mma_ss(tmem + (2 * w + buf) * kTile, a0 + ((w * G::kTileBytes) >> 4) + o, b0 + o, id, kk > 0 ? 1u : 0u);
+          tc05::mma_ss(tS + buf * kTile, a0 + o, b0 + o, id, kk > 0 ? 1u : 0u);
         }
         tc05::commit(&bars[G::kBarSFull + 2 * w + buf]);
-        ++cnt[w];
+        tc05::commit(&bars[G::kBarIEmpty + slot]);
+        ++cnt;
+      } else {
+        mbar_arrive(&bars[G::kBarIEmpty + slot]);
       }
-      tc05::commit(&bars[G::kBarIEmpty + slot]);
       if (++slot == G::kStages) slot = 0, parity ^= 1;
     }
     tc05::commit(&bars[G::kBarOEmpty + ob]);
   }
   // Every MMA this lane issued completes before the tensor memory is released.
-  tc05::commit(&bars[G::kBarDone]);
-  mbar_wait(&bars[G::kBarDone], 0);
+  tc05::commit(&bars[G::kBarDone + w]);
+  mbar_wait(&bars[G::kBarDone + w], 0);
 }
 
 __device__ __forceinline__ void lds_f2x2(uint32_t addr, uint64_t& a, uint64_t& b) {
@@ -609,13 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[G::kBarOFull + i], 1);
-      mbar_init(&bars[G::kBarOEmpty + i], 9);  // the MMAs, and the warps that read the halves
+      mbar_init(&bars[G::kBarOEmpty + i], 10);  // both lanes' MMAs, and the warps that read the halves
       mbar_init(&bars[G::kBarXFull + i], 4);
       mbar_init(&bars[G::kBarXEmpty + i], 4);
     }
     for (int s = 0; s < G::kStages; ++s) {
       mbar_init(&bars[G::kBarIFull + s], 1);
-      mbar_init(&bars[G::kBarIEmpty + s], 1);
+      mbar_init(&bars[G::kBarIEmpty + s], 2);  // both lanes
     }
     for (int s = 0; s < kLStages; ++s) {
       mbar_init(&bars[G::kBarLFull + s], 1);
@@ -627,9 +631,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars[G::kBarWFull + i], 1);
-      mbar_init(&bars[G::kBarWEmpty + i], 18);  // the producer, the MMA lane, 16 warps
+      mbar_init(&bars[G::kBarWEmpty + i], 19);  // the producer, the MMA lanes, 16 warps
     }
     mbar_init(&bars[G::kBarDone], 1);
+    mbar_init(&bars[G::kBarDone + 1], 1);
     *abort_flag = 0;
     fence_mbar_init();
     tc05::prefetch_tmap(&tq);
@@ -713,7 +718,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) producer<D, kSums>(&tq, &tk, p, sm, bars, abort_flag);
   } else if (warp == 1) {
-    if (lane == 0) mma_lane<D, kBf16>(p, sm, bars, tmem, abort_flag);
+    if (lane == 0) mma_lane<D, kBf16>(p, 0, sm, bars, tmem, abort_flag);
+  } else if (warp == 3) {
+    if (lane == 0) mma_lane<D, kBf16>(p, 1, sm, bars, tmem, abort_flag);
   } else if (warp == 2) {
     if (lane == 0) walker<D, kSums>(p, wk, rg, sm, bars, abort_flag);
   } else if (warp >= 4) {
