@@ -48,6 +48,7 @@ constexpr int kThreads = 640;           // 4 service warps, 4 warpgroups
 constexpr int kTile = 128;               // rows of a tile
 constexpr int kSlabBytes = kTile * 128;  // 128 rows x 64 sixteen-bit columns
 constexpr int kMaxSeqs = 1024;           // sequences per launch
+constexpr int kItemCost = 1;             // (8 prompts of 2,048 tokens: 0 385 us, 1 and 2 349, 5 360)
 constexpr int kItems = 3;                // items worked out ahead
 constexpr int kLStages = 3;              // slots of the ring of row statistics
 constexpr float kRaiseLog2 = 8.0f;       // the offset of a row's sum is raised beyond 2^8
@@ -87,6 +88,7 @@ struct Params {
   int b0;             // sequences before these
   int accumulate;
   int64_t page_tokens, max_pages, num_pages;
+  int shift;          // log2(page_tokens), or -1
   float c_log2;       // scale * log2(e)
 };
 
@@ -150,20 +152,20 @@ struct Items {
     const int lim = min(nk - 1, min((o + 1) * span, nq) - 1 + off);
     return lim < 0 ? 0 : lim / kTile + 1;
   }
-  // Pairs of the items before o.
+  // Places of the items before o: their pairs, and kItemCost for each that has any.
   __device__ int64_t before(int o) const {
     if (o == 0) return 0;
     if (kSums) {  // size(x) = all query tiles less floor(max(0, x span - off) / tpt)
       const int x0 = off > 0 ? (off + span - 1) / span : 0;
-      int64_t s = static_cast<int64_t>(o) * ((nq + tpt - 1) / tpt);
+      int64_t s = static_cast<int64_t>(o) * ((nq + tpt - 1) / tpt + kItemCost);
       if (o > x0) s -= floor_sum(o - x0, tpt, span, x0 * span - off);
       return s;
     }
     // all but the last item: max(0, floor((x span + c) / 128)) with c = span - 1 + off + 128
     const int n = min(o, count - 1), c = span - 1 + off + kTile;
-    const int x0 = c < 0 ? (-c + span - 1) / span : 0;
-    int64_t s = n > x0 ? floor_sum(n - x0, kTile, span, x0 * span + c) : 0;
-    if (o == count) s += size(count - 1);
+    const int x0 = c < kTile ? (kTile - c + span - 1) / span : 0;  // the first that has any
+    int64_t s = n > x0 ? floor_sum(n - x0, kTile, span, x0 * span + c) + static_cast<int64_t>(n - x0) * kItemCost : 0;
+    if (o == count) s += size(count - 1) + kItemCost;
     return s;
   }
 };
@@ -172,7 +174,7 @@ struct Items {
 template <bool kSums>
 struct Walk {
   int b, h, o;
-  int64_t off;   // place of the item's first pair
+  int64_t off;   // the item's first place; its pairs begin kItemCost further
   int size, first;
   Seq s;
 
@@ -183,7 +185,7 @@ struct Walk {
   }
   // The next item with a pair (there is one, unless b reaches p.B).
   __device__ __forceinline__ void next(const Params& p) {
-    off += size;
+    off += size + kItemCost;
     Items<kSums> it(p, s);
     ++o;
     for (;;) {
@@ -233,8 +235,9 @@ __device__ __forceinline__ Item item_of(const Params& p, const Walk<kSums>& wk, 
   it.nq = wk.s.nq;
   it.k0 = wk.s.k0;
   it.nk = wk.s.nk;
-  const int lo = static_cast<int>(max(begin - wk.off, int64_t(0)));
-  const int hi = static_cast<int>(min(end - wk.off, static_cast<int64_t>(wk.size)));
+  const int64_t first = wk.off + kItemCost, size = wk.size;
+  const int lo = static_cast<int>(min(max(begin - first, int64_t(0)), size));
+  const int hi = static_cast<int>(min(max(end - first, int64_t(0)), size));
   it.t0 = wk.first + lo;
   it.t1 = wk.first + hi;
   it.cut = lo > 0 ? 1 : hi < wk.size ? 2 : 0;
@@ -269,11 +272,15 @@ __device__ __forceinline__ void put_row(const Params& p, const Item& it, int w, 
   p.nlse[tile_id(p, it, tile) * kTile + row] = !live || m == SA_NEG_INF ? SA_NEG_INF : -(m + log2f(l));
 }
 
+__device__ __forceinline__ uint32_t page_index(const Params& p, int j) {
+  return p.shift >= 0 ? static_cast<uint32_t>(j) >> p.shift : static_cast<uint32_t>(j) / static_cast<uint32_t>(p.page_tokens);
+}
+
 // kSums 1: the weight of the item's key `row` of tile w.
 __device__ __forceinline__ void put_key(const Params& p, const Item& it, int w, int row, float sum) {
   const int j = it.o * 2 * kTile + w * kTile + row;
   if (j >= it.nk) return;
-  const uint32_t pi = static_cast<uint32_t>(j) / static_cast<uint32_t>(p.page_tokens);
+  const uint32_t pi = page_index(p, j);
   int32_t page = -1;
   if (pi < p.max_pages) page = __ldg(p.block_table + it.b * p.max_pages + pi);
   if (page < 0 || page >= p.num_pages) {
@@ -287,7 +294,7 @@ __device__ __forceinline__ void put_key(const Params& p, const Item& it, int w, 
 
 // ---- roles -----------------------------------------------------------------------------------
 
-// This CTA's range of pairs.
+// This CTA's range of places.
 struct Range {
   int64_t begin, end;
 };
@@ -298,19 +305,24 @@ template <int D, bool kSums>
 __device__ void walker(const Params& p, Walk<kSums> wk, Range rg, uint8_t* sm, uint64_t* bars, volatile int* abort_flag) {
   using G = Geo<D>;
   int4 cut = make_int4(-1, 0, 0, 0);  // the item that this range begins and does not end, for merge_kernel
-  for (uint32_t n = 0;; ++n) {
-    const uint32_t slot = n % kItems, use = n / kItems;
+  for (uint32_t n = 0;;) {
     const bool more = wk.b < p.B && wk.off < rg.end;
     Item it;
     if (more) it = item_of(p, wk, rg.begin, rg.end);
     else it.b = -1;
+    if (more && it.t0 == it.t1) {  // (of this item the range has what its change costs, no pair)
+      wk.next(p);
+      continue;
+    }
     if (more && it.cut == 2)
-      cut = make_int4(it.b, it.h, it.o, static_cast<int>((wk.off + wk.size - 1) / (rg.end - rg.begin)));
+      cut = make_int4(it.b, it.h, it.o, static_cast<int>((wk.off + kItemCost + wk.size - 1) / (rg.end - rg.begin)));
+    const uint32_t slot = n % kItems, use = n / kItems;
     if (use > 0 && !wait_or_abort(&bars[G::kBarWEmpty + slot], (use - 1) & 1, abort_flag, p.err_word)) break;
     *reinterpret_cast<Item*>(sm + G::kOffItems + slot * 64) = it;
     mbar_arrive(&bars[G::kBarWFull + slot]);
     if (!more) break;
     wk.next(p);
+    ++n;
   }
   p.cut[blockIdx.x] = cut;
 }
@@ -646,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc05::fence_before_sync();
 
-  // ---- the sequences' pairs, and this CTA's range (the ring is scratch until then)
+  // ---- the sequences' places, and this CTA's range (the ring is scratch until then)
   int64_t* pref = reinterpret_cast<int64_t*>(sm + G::kOffInner);
   bool bad = false;
   for (int b = tid; b < p.B; b += kThreads) {
@@ -671,10 +683,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  const int64_t pairs = bad ? 0 : pref[p.B];
-  const int64_t R = (pairs + gridDim.x - 1) / gridDim.x;
+  const int64_t places = bad ? 0 : pref[p.B];
+  const int64_t R = (places + gridDim.x - 1) / gridDim.x;
   Range rg{static_cast<int64_t>(blockIdx.x) * R, 0};
-  rg.end = min(rg.begin + R, pairs);
+  rg.end = min(rg.begin + R, places);
   Walk<kSums> wk{};
   wk.b = p.B;
   if (warp == 2 && rg.begin < rg.end) {  // (the walker's)
@@ -839,6 +851,9 @@ int launch_t(const WeightsArgs& a, cudaStream_t st) {
   p.max_pages = a.max_pages;
   p.num_pages = a.num_pages;
   p.c_log2 = a.scale * 1.4426950408889634f;
+  p.shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_tokens == int64_t(1) << i) p.shift = i;
   auto stats = weights_kernel<D, T, false>;
   auto sums = weights_kernel<D, T, true>;
   if (!allow_smem(reinterpret_cast<const void*>(stats)) || !allow_smem(reinterpret_cast<const void*>(sums))) return -1;
