@@ -15,54 +15,104 @@
 // E the equal keys before it, so one scan over the marks places every token in
 // ascending order.
 //
-// Bound by issue slots: some 30 instructions a token, and what a warp does once per
-// row.  So a row has one CTA where there are enough rows (keys kept in registers by
-// clusters of four CTAs a row, 64 warps instead of 16: 178 us for 2.16 M tokens in 8
-// heads), and a cluster of up to 8, which share their histograms, lists and counts
-// through distributed shared memory, where there are few.
+// Bound by issue slots, and by the way of a row's loads.  A row has one CTA where there
+// are enough rows, of 256 threads, so that few warps do what is done once per row (2.16 M
+// tokens in 8 heads: 68 us; 512 threads, 72; rows that clusters of four CTAs keep in
+// registers, 178), the longest contexts first (in the order given, 5 us more).  Where there
+// are few rows a cluster of up to 8 CTAs takes one, its histograms, lists and counts
+// shared through distributed shared memory (2 contexts of 131,072 tokens, 4 heads: 29 us).
+// The list holds tokens, not keys: the few keys come once more from L1 (keys written by the
+// second pass itself, each token's place from an atomic of its own: 83 us).
 #include "cluster.cuh"
 #include "weights.h"
+
+#include <type_traits>
 
 namespace sa {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kQuads = 4;                          // of four tokens, that a thread has in flight
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048;                        // of the first two digits (the third: 1,024)
+constexpr int kFirst = 2048, kSecond = 2048, kThird = 1024;  // bins of the key's three digits
+constexpr int kShift1 = 21, kShift2 = 10;          // the first digit's place, the second's
 constexpr int kList = 2048;                        // tokens that share the first digit found
 constexpr uint32_t kLowest = 0x007fffffu;          // the key of -inf
-constexpr uint32_t kNone = 0u, kAlways = 0xffffffffu;  // no token; one kept whatever its weight
+constexpr uint32_t kNoKey = 0xffffffffu;           // above every weight's
 
+// A larger key for a larger weight.  (fmaxf: NaN becomes -inf; the sum: -0 becomes 0.)
 __device__ __forceinline__ uint32_t key_of(float w) {
-  const uint32_t u = __float_as_uint(w + 0.0f);  // -0 becomes 0
-  if (w != w) return kLowest;
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  const int32_t u = __float_as_int(fmaxf(w, SA_NEG_INF) + 0.0f);
+  return static_cast<uint32_t>(u ^ ((u >> 31) | static_cast<int32_t>(0x80000000)));
+}
+// The weight of which w >= it says that w's key is at least k (NaN, so never, above +inf's).
+__device__ __forceinline__ float weight_of(uint32_t k) {
+  k = max(k, kLowest);
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
+// A row's CTA, or a cluster's.
+template <bool kCluster>
+struct Cfg {
+  static constexpr int kThreads = kCluster ? 512 : 256;
+  static constexpr int kCtas = kCluster ? 2 : 5;  // to a multiprocessor, at least
+};
+
+template <bool kCluster>
 struct Shared {
-  uint32_t hist[3][kBins];
-  uint32_t list[kList], token[kList];
+  static constexpr int kWarps = Cfg<kCluster>::kThreads / 32;
+  uint32_t hist[kFirst + kSecond + kThird];
+  uint32_t list[kList], token[kList];  // (the keys are filled in when the list is complete)
   uint32_t listed;                  // tokens in the list
   uint32_t sum[kWarps];             // of a block-wide scan
   uint32_t bin, above, inside;      // the digit found, the keys above it, its own
+  uint2 marked[kWarps];             // greater and equal keys of a warp's words
+  int seq;                          // the sequence of this CTA's row
   uint2 total;                      // greater and equal keys of the CTA
 };
+
+// Sum of the lanes up to and with this one.
+__device__ __forceinline__ uint32_t scan_warp(uint32_t v, int lane, int width = 32) {
+  for (int sh = 1; sh < width; sh <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, v, sh);
+    if (lane >= sh) v += x;
+  }
+  return v;
+}
 
 // Dynamic shared memory: Shared, then a byte per four tokens of the CTA: greater in the
 // low half, equal in the high one.
 template <bool kCluster>
-__global__ void __launch_bounds__(kThreads, 3)
-    kv_select_kernel(const __grid_constant__ SelectArgs a, int ctas) {
+__global__ void __launch_bounds__(Cfg<kCluster>::kThreads, Cfg<kCluster>::kCtas)
+    kv_select_kernel(const __grid_constant__ SelectArgs a, int ctas, int order) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
-  uint8_t* map = smem_raw + sizeof(Shared);
+  using S = Shared<kCluster>;
+  constexpr int kThreads = Cfg<kCluster>::kThreads, kWarps = S::kWarps;
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  uint8_t* map = smem_raw + sizeof(S);
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  const int row = static_cast<int>(blockIdx.x / static_cast<uint32_t>(ctas));
+  int row = static_cast<int>(blockIdx.x / static_cast<uint32_t>(ctas));
   const int rank = kCluster ? static_cast<int>(cluster_rank()) : 0;
-  const int b = row / a.Hkv, h = row - b * a.Hkv;
+  int b = row / a.Hkv;
+  const int h = row - b * a.Hkv;
+  if (!kCluster && order) {  // the b-th longest context (as many threads as sequences, at least)
+    int32_t* len = reinterpret_cast<int32_t*>(sm.list);
+    const int own = tid < a.B ? max(__ldg(a.ctx_len + tid), 0) : -1;
+    len[tid] = own;
+    __syncthreads();
+    int longer = 0;
+    if (tid < a.B) {
+      for (int i = 0; i < a.B; i += 4) {  // (places behind the last sequence hold -1)
+        const int4 v = *reinterpret_cast<const int4*>(len + i);
+        longer += (v.x > own || (v.x == own && i < tid)) + (v.y > own || (v.y == own && i + 1 < tid)) +
+                  (v.z > own || (v.z == own && i + 2 < tid)) + (v.w > own || (v.w == own && i + 3 < tid));
+      }
+      if (longer == b) sm.seq = tid;
+    }
+    __syncthreads();
+    b = sm.seq;
+    row = b * a.Hkv + h;
+  }
   const int64_t n64 = __ldg(a.ctx_len + b);
   const bool ok = n64 >= 0 && n64 <= a.max_pages * a.page_tokens;
   const int n = ok ? static_cast<int>(n64) : 0;
@@ -80,22 +130,28 @@ __global__ void __launch_bounds__(kThreads, 3)
   uint32_t need = static_cast<uint32_t>(a.budget - a.sink - a.recent);  // of the middle
   const int seg = ((n + ctas - 1) / ctas + 15) & ~15;
   const int begin = min(rank * seg, n), end = min(begin + seg, n), end16 = begin + ((end - begin + 15) & ~15);
+  const int sink = a.sink, stop = min(n - a.recent, end);  // the middle: [sink, stop)
   bool bad = false;
   const int32_t* table = a.block_table + static_cast<int64_t>(b) * a.max_pages;
   const uint32_t pt = static_cast<uint32_t>(a.page_tokens);
+  const float* pool = a.weights + static_cast<int64_t>(h) * pt;
+  const int64_t page_stride = static_cast<int64_t>(a.Hkv) * pt;
+  const uint32_t pages = static_cast<uint32_t>(a.num_pages);  // (below 2^31)
   auto weight_at = [&](uint32_t t) -> const float* {
     const uint32_t pi = a.shift >= 0 ? t >> a.shift : t / pt;
-    const int32_t p = __ldg(table + pi);
-    if (p < 0 || p >= a.num_pages) {
+    const uint32_t p = static_cast<uint32_t>(__ldg(table + pi));
+    if (p >= pages) {
       bad = true;
       return nullptr;
     }
-    return a.weights + (p * static_cast<int64_t>(a.Hkv) + h) * pt + (t - pi * pt);
+    return pool + p * page_stride + (t - pi * pt);
   };
-  // f(t, keys of t .. t + 3) for all quads of this CTA, those of a thread 4 * kThreads apart.
+  // f(t0, weights): this thread's quads at t0 + 4 * kThreads * r, for all tokens of the CTA;
+  // whole warps, so also quads behind the last.
   auto quads = [&](auto&& f) {
 #pragma unroll 1
-    for (int t0 = begin + 4 * tid; t0 < end16; t0 += 4 * kThreads * kQuads) {
+    for (int t1 = begin + 128 * warp; t1 < end16; t1 += 4 * kThreads * kQuads) {
+      const int t0 = t1 + 4 * lane;
       float w[kQuads][4];
 #pragma unroll
       for (int r = 0; r < kQuads; ++r) {
@@ -119,134 +175,182 @@ __global__ void __launch_bounds__(kThreads, 3)
           }
         }
       }
-#pragma unroll
-      for (int r = 0; r < kQuads; ++r) {
-        const int t = t0 + 4 * kThreads * r;
-        if (t >= end16) break;
-        uint32_t key[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) key[e] = key_of(w[r][e]);
-        if (t < a.sink || t + 3 >= n - a.recent || t + 3 >= end) {  // (few: the row's ends)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (t + e < a.sink || t + e >= n - a.recent) key[e] = kAlways;
-            if (t + e >= end) key[e] = kNone;
-          }
-        }
-        f(t, key);
-      }
+      f(t0, w);
     }
   };
-  auto middle = [](uint32_t k) { return k - 1u < kAlways - 1u; };
+  // of four tokens: a bit for each of the middle
+  auto middle = [&](int t) {
+    uint32_t m = 15u;
+    if (t < sink || t + 4 > stop) {  // (few: the row's ends)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t + e < sink || t + e >= stop) m &= ~(1u << e);
+    }
+    return m;
+  };
+  // and for each that is kept whatever its weight
+  auto always = [&](int t, uint32_t mid) {
+    uint32_t m = 0u;
+    if (mid != 15u) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t + e < end && !(mid >> e & 1u)) m |= 1u << e;
+    }
+    return m;
+  };
 
-  for (int i = tid; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
+  for (int i = tid; i < static_cast<int>(sizeof(sm.hist) / 4); i += kThreads) sm.hist[i] = 0;
   if (tid == 0) {
     sm.listed = 0;
     sm.total = make_uint2(0u, 0u);
   }
   __syncthreads();
 
-  // The digit whose keys hold the last one kept: `c` the counts of the bins at .. at + 3, all
-  // threads' together (the largest bins with the first threads).
-  const int at = kBins - 4 - 4 * tid;
-  auto find_digit = [&](uint4 c) {
-    const uint32_t sum = c.x + c.y + c.z + c.w;
-    uint32_t before = sum;
+  // The digit whose keys hold the last one kept: c the counts of this thread's bins (the
+  // largest bins with the first threads).
+  auto find_digit = [&](const auto& c, int bins) {
+    constexpr int kPer = sizeof(c) / sizeof(c[0]);
+    uint32_t sum = 0;
 #pragma unroll
-    for (int sh = 1; sh < 32; sh <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, before, sh);
-      if (lane >= sh) before += x;
-    }
+    for (int i = 0; i < kPer; ++i) sum += c[i];
+    uint32_t before = scan_warp(sum, lane);
     if (lane == 31) sm.sum[warp] = before;
     __syncthreads();
+    const uint32_t of = scan_warp(sm.sum[lane & (kWarps - 1)], lane, kWarps);
     before -= sum;
-    for (int w = 0; w < warp; ++w) before += sm.sum[w];
+    const uint32_t up0 = __shfl_sync(0xffffffffu, of, max(warp - 1, 0));
+    if (warp > 0) before += up0;
     if (before < need && need <= before + sum) {  // one thread
       uint32_t up = before;
-      int i = 3;
-      uint32_t v = c.w;
-      if (up + v < need) up += v, v = c.z, i = 2;
-      if (i == 2 && up + v < need) up += v, v = c.y, i = 1;
-      if (i == 1 && up + v < need) up += v, v = c.x, i = 0;
-      sm.bin = static_cast<uint32_t>(at + i);
-      sm.above = up;
-      sm.inside = v;
+      bool found = false;
+#pragma unroll
+      for (int i = kPer - 1; i >= 0; --i) {
+        if (found) continue;
+        if (up + c[i] >= need) {
+          found = true;
+          sm.bin = static_cast<uint32_t>(bins - kPer * (tid + 1) + i);
+          sm.above = up;
+          sm.inside = c[i];
+        }
+        up += c[i];
+      }
     }
     __syncthreads();
     need -= sm.above;
   };
-  auto counts = [&](int p) {  // over the cluster
-    uint32_t* h4 = sm.hist[p] + at;
-    if (!kCluster) {
+  // this thread's bins, over the CTAs `of` the cluster (or of its own alone)
+  auto counts = [&](const uint32_t* hist, auto& c, int bins, int of) {
+    constexpr int kPer = sizeof(c) / sizeof(c[0]);
+    const uint32_t* from = hist + bins - kPer * (tid + 1);
+    if (!kCluster || of == 1) {
       __syncthreads();
-      return *reinterpret_cast<const uint4*>(h4);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) c[i] = from[i];
+      return;
     }
     cluster_sync();
-    uint4 c = make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t addr = smem_u32(h4);
-    for (int q = 0; q < ctas; ++q) {
-      const uint4 v = ld_cluster4(cluster_addr(addr, static_cast<uint32_t>(q)));
-      c.x += v.x;
-      c.y += v.y;
-      c.z += v.z;
-      c.w += v.w;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) c[i] = 0;
+#pragma unroll
+    for (int q = 0; q < kMaxCluster; ++q) {
+      if (q >= of) break;
+      const uint32_t at = cluster_addr(smem_u32(from), static_cast<uint32_t>(q));
+      if constexpr (kPer % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < kPer; i += 4) {
+          const uint4 v = ld_cluster4(at + i * 4);
+          c[i] += v.x;
+          c[i + 1] += v.y;
+          c[i + 2] += v.z;
+          c[i + 3] += v.w;
+        }
+      } else {
+        const uint2 v = ld_cluster2(at);
+        c[0] += v.x;
+        c[1] += v.y;
+      }
     }
-    return c;
-  };
-  auto sync = [&]() {
-    if (kCluster) cluster_sync();
-    else __syncthreads();
   };
 
   // ---- the key of the last one kept, and the marks -------------------------------------------
   uint32_t ties = 0;
   // tokens of at least `from` are greater; those of `to` .. from - 1 go to the list
   auto mark = [&](uint32_t from, uint32_t to) {
-    quads([&](int t, const uint32_t(&key)[4]) {
-      uint32_t m = 0;
+    const float lo = weight_of(to), hi = weight_of(from);
+    quads([&](int t0, const float(&w)[kQuads][4]) {
+      uint32_t found = 0;
+      uint8_t* to = map + ((t0 - begin) >> 2);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (key[e] >= from) m |= 1u << e;
-        else if (key[e] >= to) {
-          const uint32_t i = atomicAdd(&sm.listed, 1u);
-          sm.list[i] = key[e];
-          sm.token[i] = static_cast<uint32_t>(t + e - begin);
+      for (int r = 0; r < kQuads; ++r) {
+        const int t = t0 + 4 * kThreads * r;
+        const uint32_t mid = middle(t);
+        uint32_t m = 0, l = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = fmaxf(w[r][e], SA_NEG_INF);
+          if (x >= hi) m |= 1u << e;
+          if (x >= lo) l |= 1u << e;
         }
+        found |= (l & ~m & mid) << (4 * r);
+        if (t < end16) to[kThreads * r] = static_cast<uint8_t>((m & mid) | always(t, mid));
       }
-      map[(t - begin) >> 2] = static_cast<uint8_t>(m);
+      if (!__any_sync(0xffffffffu, found != 0u)) return;
+      const uint32_t own = __popc(found);
+      uint32_t at = scan_warp(own, lane);
+      uint32_t base = 0;
+      if (lane == 31) base = atomicAdd(&sm.listed, at);
+      at += __shfl_sync(0xffffffffu, base, 31) - own;
+      for (; found != 0u; found &= found - 1u) {
+        const int bit = __ffs(found) - 1;
+        sm.token[at++] = static_cast<uint32_t>(t0 + 4 * kThreads * (bit >> 2) + (bit & 3) - begin);
+      }
     });
   };
   if (need == 0) {
-    mark(kAlways, kAlways);
+    mark(kNoKey, kNoKey);
   } else {
-    quads([&](int, const uint32_t(&key)[4]) {
-      const uint32_t d = key[0] >> 21;
-      if ((key[1] >> 21) == d && (key[2] >> 21) == d && (key[3] >> 21) == d && middle(key[0]) && d != kBins - 1) {
-        atomicAdd(sm.hist[0] + d, 4u);  // (a pool of zeros: fewer to queue for one word)
-      } else {
+    quads([&](int t0, const float(&w)[kQuads][4]) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (middle(key[e])) atomicAdd(sm.hist[0] + (key[e] >> 21), 1u);
+      for (int r = 0; r < kQuads; ++r) {
+        const uint32_t mid = middle(t0 + 4 * kThreads * r);
+        uint32_t d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = key_of(w[r][e]) >> kShift1;
+        if (mid == 15u && d[1] == d[0] && d[2] == d[0] && d[3] == d[0]) {
+          atomicAdd(sm.hist + d[0], 4u);  // (a pool of zeros: fewer to queue for one word)
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (mid >> e & 1u) atomicAdd(sm.hist + d[e], 1u);
+        }
       }
     });
-    find_digit(counts(0));
+    {
+      uint32_t c[kFirst / kThreads];
+      counts(sm.hist, c, kFirst, ctas);
+      find_digit(c, kFirst);
+    }
     uint32_t prefix = sm.bin;
     const uint32_t inside = sm.inside;
     if (inside == need) {  // the whole digit is kept
-      mark(prefix << 21, kAlways);
+      mark(prefix << kShift1, kNoKey);
     } else {
       const bool listed = inside <= kList;  // (the same for the whole cluster)
       if (listed) {
-        mark((prefix + 1) << 21, prefix << 21);
-        sync();
+        mark((prefix + 1) << kShift1, prefix << kShift1);
+        __syncthreads();
+        for (uint32_t i = tid; i < sm.listed; i += kThreads) {
+          const float* x = weight_at(static_cast<uint32_t>(begin) + sm.token[i]);
+          sm.list[i] = x ? key_of(__ldg(x)) : kLowest;
+        }
+        if (kCluster) cluster_sync();
       }
-      uint32_t last = 0;
-#pragma unroll 1
-      for (int p = 1; p < 3; ++p) {
-        const int shift = p == 1 ? 10 : 0, above_shift = p == 1 ? 21 : 10;
-        const uint32_t mask = p == 1 ? 2047u : 1023u;
+      auto later = [&](auto digit) {  // the next digit, from the list or from all tokens
+        constexpr bool kLast = decltype(digit)::value;
+        constexpr int kShift = kLast ? 0 : kShift2, kAbove = kLast ? kShift2 : kShift1, kBins = kLast ? kThird : kSecond;
+        uint32_t* hist = sm.hist + kFirst + (kLast ? kSecond : 0);
         auto count = [&](uint32_t k) {
-          if ((k >> above_shift) == prefix) atomicAdd(sm.hist[p] + ((k >> shift) & mask), 1u);
+          if ((k >> kAbove) == prefix) atomicAdd(hist + ((k >> kShift) & (kBins - 1)), 1u);
         };
         if (listed) {  // every CTA counts the whole list
           for (int q = 0; q < ctas; ++q) {
@@ -254,19 +358,25 @@ __global__ void __launch_bounds__(kThreads, 3)
             for (uint32_t i = tid; i < len; i += kThreads)
               count(kCluster ? ld_cluster(cluster_addr(smem_u32(sm.list + i), static_cast<uint32_t>(q))) : sm.list[i]);
           }
-          __syncthreads();
-          find_digit(*reinterpret_cast<const uint4*>(sm.hist[p] + at));
         } else {
-          quads([&](int, const uint32_t(&key)[4]) {
+          quads([&](int t0, const float(&w)[kQuads][4]) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (middle(key[e])) count(key[e]);
+            for (int r = 0; r < kQuads; ++r) {
+              const uint32_t mid = middle(t0 + 4 * kThreads * r);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (mid >> e & 1u) count(key_of(w[r][e]));
+            }
           });
-          find_digit(counts(p));
         }
-        prefix = (prefix << (p == 1 ? 11 : 10)) | sm.bin;
-        last = prefix;
-      }
+        uint32_t c[kBins / kThreads];
+        counts(hist, c, kBins, listed ? 1 : ctas);
+        find_digit(c, kBins);
+        prefix = prefix * kBins + sm.bin;
+      };
+      later(std::false_type{});
+      later(std::true_type{});
+      const uint32_t last = prefix;
       ties = need;
       if (listed) {
         for (uint32_t i = tid; i < sm.listed; i += kThreads) {
@@ -276,14 +386,22 @@ __global__ void __launch_bounds__(kThreads, 3)
           atomicOr(reinterpret_cast<uint32_t*>(map) + (t >> 4), 1u << bit);
         }
       } else {
-        quads([&](int t, const uint32_t(&key)[4]) {
-          uint32_t m = 0;
+        const float lo = weight_of(last);
+        quads([&](int t0, const float(&w)[kQuads][4]) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (key[e] > last) m |= 1u << e;
-            if (key[e] == last) m |= 16u << e;
+          for (int r = 0; r < kQuads; ++r) {
+            const int t = t0 + 4 * kThreads * r;
+            if (t >= end16) break;
+            const uint32_t mid = middle(t);
+            uint32_t m = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = fmaxf(w[r][e], SA_NEG_INF);
+              if (x > lo) m |= 1u << e;
+              if (x == lo) m |= 16u << e;
+            }
+            map[(t - begin) >> 2] = static_cast<uint8_t>((m & mid * 17u) | always(t, mid));
           }
-          map[(t - begin) >> 2] = static_cast<uint8_t>(m);
         });
       }
     }
@@ -294,50 +412,43 @@ __global__ void __launch_bounds__(kThreads, 3)
   const uint32_t* words = reinterpret_cast<const uint32_t*>(map);  // of 16 tokens
   const int nwords = (end16 - begin) / 16;
   auto both = [](uint32_t x) { return __popc(x & 0x0f0f0f0fu) | __popc(x & 0xf0f0f0f0u) << 16; };
-  uint32_t greater = 0, equal = 0;  // before this CTA's tokens, later before the round's
-  if (kCluster) {
-    uint32_t g = 0, q = 0;
-    for (int i = tid; i < nwords; i += kThreads) {
-      const uint32_t x = both(words[i]);
-      g += x & 0xffffu;
-      q += x >> 16;
-    }
-    g = __reduce_add_sync(0xffffffffu, g);
-    q = __reduce_add_sync(0xffffffffu, q);
-    if (lane == 0) {
-      atomicAdd(&sm.total.x, g);
-      atomicAdd(&sm.total.y, q);
-    }
-    cluster_sync();
-    for (int c = 0; c < rank; ++c) {
-      const uint2 t = ld_cluster2(cluster_addr(smem_u32(&sm.total), static_cast<uint32_t>(c)));
-      greater += t.x;
-      equal += t.y;
+  auto sync = [&]() {
+    if (kCluster) cluster_sync();
+    else __syncthreads();
+  };
+  // a warp's words: [first, last), and what is marked before them
+  const int per = (nwords + kWarps - 1) / kWarps, first = min(warp * per, nwords), last = min(first + per, nwords);
+  uint32_t greater = 0, equal = 0;
+  for (int i = first + lane; i < last; i += 32) {
+    const uint32_t x = both(words[i]);
+    greater += x & 0xffffu;
+    equal += x >> 16;
+  }
+  greater = __reduce_add_sync(0xffffffffu, greater);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) {
+    sm.marked[warp] = make_uint2(greater, equal);
+    if (kCluster) {
+      atomicAdd(&sm.total.x, greater);
+      atomicAdd(&sm.total.y, equal);
     }
   }
+  sync();
+  const uint2 w0 = lane < warp ? sm.marked[lane] : make_uint2(0u, 0u);
+  greater = __reduce_add_sync(0xffffffffu, w0.x);
+  equal = __reduce_add_sync(0xffffffffu, w0.y);
+  for (int c = 0; kCluster && c < rank; ++c) {
+    const uint2 t = ld_cluster2(cluster_addr(smem_u32(&sm.total), static_cast<uint32_t>(c)));
+    greater += t.x;
+    equal += t.y;
+  }
 #pragma unroll 1
-  for (int i0 = 0; i0 < nwords; i0 += kThreads) {
-    const uint32_t x = i0 + tid < nwords ? words[i0 + tid] : 0u;
-    const uint32_t own = both(x);  // (a round: at most 8,192 of either)
-    uint32_t before = own;
-#pragma unroll
-    for (int sh = 1; sh < 32; sh <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, before, sh);
-      if (lane >= sh) before += y;
-    }
-    __syncthreads();  // (the sums of the round before, or of a digit, have been read)
-    if (lane == 31) sm.sum[warp] = before;
-    __syncthreads();
-    before -= own;
-    uint32_t all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t c = sm.sum[w];
-      if (w < warp) before += c;
-      all += c;
-    }
+  for (int i0 = first; i0 < last; i0 += 32) {
+    const uint32_t x = i0 + lane < last ? words[i0 + lane] : 0u;
+    const uint32_t own = both(x), with = scan_warp(own, lane), all = __shfl_sync(0xffffffffu, with, 31);
+    const uint32_t before = with - own;
     uint32_t g = greater + (before & 0xffffu), q = equal + (before >> 16);
-    const int t0 = begin + (i0 + tid) * 16;
+    const int t0 = begin + (i0 + lane) * 16;
     for (uint32_t todo = (x | x >> 4) & 0x0f0f0f0fu; todo != 0u; todo &= todo - 1u) {
       const int bit = __ffs(todo) - 1;
       const bool tie = !(x >> bit & 1u);
@@ -363,13 +474,16 @@ int launch_kv_select(const SelectArgs& a, cudaStream_t st) {
   while (ctas < kMaxCluster && ((rows * ctas < 2 * sm_count() && ctas * 1024 < most) || most > ctas * kSelectTokens)) ctas *= 2;
   if (rows * ctas > INT32_MAX || most > ctas * kSelectTokens) return -1;
   const int64_t tokens = (most + ctas - 1) / ctas + 15;
-  const size_t smem = sizeof(Shared) + static_cast<size_t>(tokens / 16 + 1) * 4;
+  const int threads = ctas > 1 ? Cfg<true>::kThreads : Cfg<false>::kThreads;
+  const size_t smem = (ctas > 1 ? sizeof(Shared<true>) : sizeof(Shared<false>)) + static_cast<size_t>(tokens / 16 + 1) * 4;
+  // Where they come one after the other, the longest contexts go first.
+  const int order = ctas == 1 && a.B <= threads && rows > Cfg<false>::kCtas * sm_count() ? 1 : 0;
   const void* kernel = ctas > 1 ? reinterpret_cast<const void*>(kv_select_kernel<true>)
                                 : reinterpret_cast<const void*>(kv_select_kernel<false>);
   if (!allow_smem(kernel)) return -1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -378,8 +492,8 @@ int launch_kv_select(const SelectArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return (ctas > 1 ? cudaLaunchKernelEx(&cfg, kv_select_kernel<true>, a, static_cast<int>(ctas))
-                   : cudaLaunchKernelEx(&cfg, kv_select_kernel<false>, a, static_cast<int>(ctas))) == cudaSuccess
+  return (ctas > 1 ? cudaLaunchKernelEx(&cfg, kv_select_kernel<true>, a, static_cast<int>(ctas), order)
+                   : cudaLaunchKernelEx(&cfg, kv_select_kernel<false>, a, static_cast<int>(ctas), order)) == cudaSuccess
              ? 0 : -1;
 }
 
