@@ -466,7 +466,7 @@ const char* sa_status_string(int status) {
   }
 }
 
-int sa_version(void) { return 200; }
+int sa_version(void) { return 300; }
 
 int validate_indices(const void* idx, int idx_is_i64, int64_t B, int64_t I, int64_t Sq,
                      int64_t K, const int64_t* bound_per_batch, int64_t bound,
