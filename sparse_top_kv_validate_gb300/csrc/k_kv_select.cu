@@ -13,7 +13,8 @@
 // all.)  Token t is kept when key > T, or key == T and fewer than `ties` equal keys lie
 // before it: the number kept before a token is G + min(E, ties), with G the greater and
 // E the equal keys before it, so one scan over the marks places every token in
-// ascending order.
+// ascending order.  (Weights that change meanwhile give some list of tokens: no count of
+// one pass is an index of another unchecked.)
 //
 // Bound by issue slots, and by the way of a row's loads.  A row has one CTA where there
 // are enough rows, of 256 threads, so that few warps do what is done once per row (2.16 M
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(Cfg<kCluster>::kThreads, Cfg<kCluster>::kCtas)
       at += __shfl_sync(0xffffffffu, base, 31) - own;
       for (; found != 0u; found &= found - 1u) {
         const int bit = __ffs(found) - 1;
-        sm.token[at++] = static_cast<uint32_t>(t0 + 4 * kThreads * (bit >> 2) + (bit & 3) - begin);
+        if (at < kList) sm.token[at++] = static_cast<uint32_t>(t0 + 4 * kThreads * (bit >> 2) + (bit & 3) - begin);
       }
     });
   };
@@ -338,6 +339,8 @@ __global__ void __launch_bounds__(Cfg<kCluster>::kThreads, Cfg<kCluster>::kCtas)
       const bool listed = inside <= kList;  // (the same for the whole cluster)
       if (listed) {
         mark((prefix + 1) << kShift1, prefix << kShift1);
+        __syncthreads();
+        if (tid == 0) sm.listed = min(sm.listed, static_cast<uint32_t>(kList));
         __syncthreads();
         for (uint32_t i = tid; i < sm.listed; i += kThreads) {
           const float* x = weight_at(static_cast<uint32_t>(begin) + sm.token[i]);
@@ -452,7 +455,8 @@ __global__ void __launch_bounds__(Cfg<kCluster>::kThreads, Cfg<kCluster>::kCtas)
     for (uint32_t todo = (x | x >> 4) & 0x0f0f0f0fu; todo != 0u; todo &= todo - 1u) {
       const int bit = __ffs(todo) - 1;
       const bool tie = !(x >> bit & 1u);
-      if (!tie || q < ties) keep[g + min(q, ties)] = t0 + (bit >> 3) * 4 + (bit & 3);
+      const uint32_t at = g + min(q, ties);
+      if ((!tie || q < ties) && at < static_cast<uint32_t>(a.budget)) keep[at] = t0 + (bit >> 3) * 4 + (bit & 3);
       g += !tie;
       q += tie;
     }

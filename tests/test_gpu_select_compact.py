@@ -77,6 +77,33 @@ def test_selection_over_part_of_a_pool_off_16_bytes(cuda_lib):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("B,Hkv", [(256, 3), (257, 3), (100, 8), (96, 9)])
+def test_selection_of_many_contexts_whose_longest_go_first(cuda_lib, B, Hkv):
+    rng = random.Random(B)
+    ctx = [rng.choice([0, 1, 30, 31, 200, 200, rng.randint(32, 700)]) for _ in range(B)]
+    ctx[0], ctx[-1] = 0, 700
+    lay = Layout(ctx, [0] * B, 16, seed=B)
+    selected(cuda_lib, lay, weights_like(lay, Hkv, "spread", B), 30, 2, 5, Hkv)
+
+
+def test_selection_of_many_contexts_with_lengths_that_are_none(cuda_lib):
+    sa, B, Hkv = cuda_lib, 200, 4
+    lay = Layout([50] * B, [0] * B, 16, seed=6)
+    w = weights_like(lay, Hkv, "spread", 6)
+    ctx = lay.ctx_t.clone()
+    bad = torch.arange(0, B, 3)
+    ctx[bad] = torch.tensor([-1, -2147483648, 2147483647, 4096])[torch.arange(len(bad)) % 4].to(torch.int32)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    keep, n = sa.paged_kv_select(w.to(DEV), lay.table.to(DEV), ctx.to(DEV), 20, recent=4, err_word=err)
+    keep = keep.cpu()
+    assert int(err) == sa.ERRBIT_PAGE and n.tolist() == [0 if b % 3 == 0 else 20 for b in range(B)]
+    for b in range(B):
+        page, slot = ev.token_places(lay.table[b], 50, 16)
+        for h in range(Hkv):
+            want = [-1] * 20 if b % 3 == 0 else ev.select_row(w[page, h, slot].tolist(), 20, 0, 4)
+            assert keep[b, h].tolist() == want, (b, h)
+
+
 def test_selection_reports_bad_contexts_and_pages(cuda_lib):
     sa, lay = cuda_lib, Layout([100, 100, 100], [0] * 3, 16, seed=4)
     w = weights_like(lay, 1, "spread", 4) + 1
