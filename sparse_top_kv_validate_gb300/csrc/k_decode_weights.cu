@@ -6,7 +6,8 @@
 // The scores are 4 bytes per query head and token against 2 (D + 1) per KV head of the
 // FP8 pages, written once and read once here: with groups of 4 and heads of 128, 12% of
 // the decode's traffic where a second pass over K would be 50%.  Bound by that
-// traffic: every warp takes a contiguous range of 16-token tiles of all (sequence, KV
+// traffic (64 contexts, 1.08 M tokens, 32 / 8 heads of 128: 460 us for the decode with
+// weights, 372 without; 262,144 tokens: this kernel 14.5 us): every warp takes a contiguous range of 16-token tiles of all (sequence, KV
 // head)s laid end to end, 128 tokens at a time, four to a lane.
 #include "gather_common.cuh"
 #include "pool_add.cuh"

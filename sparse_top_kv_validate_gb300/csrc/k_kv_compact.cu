@@ -14,7 +14,7 @@
 // next), and their places put into shared memory; the rows themselves pass through a ring there,
 // each thread storing the pieces of 16 bytes that it has loaded.  (With the places worked
 // out for every piece, 160 instructions of it, that was the bound: 128 contexts to 2,048
-// tokens, FP8 pages, 289 us.)  Scale bytes and weights are moved by the threads that find the
+// tokens, 8 heads of 128, FP8 pages, 289 us; now 245, 66% of the copy bandwidth.)  Scale bytes and weights are moved by the threads that find the
 // rows, as soon as they have.  Where there are too few (sequence, KV head)s for the device, a
 // cluster of up to 8 larger CTAs shares one, each chunk cut in as many pieces.
 #include "cluster.cuh"
