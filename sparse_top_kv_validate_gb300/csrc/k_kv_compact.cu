@@ -16,7 +16,8 @@
 // out for every piece, 160 instructions of it, that was the bound: 128 contexts to 2,048
 // tokens, 8 heads of 128, FP8 pages, 289 us; now 245, 66% of the copy bandwidth.)  Scale bytes and weights are moved by the threads that find the
 // rows, as soon as they have.  Where there are too few (sequence, KV head)s for the device, a
-// cluster of up to 8 larger CTAs shares one, each chunk cut in as many pieces.
+// cluster of up to 8 larger CTAs shares one, each chunk cut in as many pieces (2 contexts of
+// 65,536 tokens to 16,384, 4 heads of 128, 16-bit elements: 54 us; a cluster of 16, 68).
 #include "cluster.cuh"
 #include "weights.h"
 
@@ -34,13 +35,15 @@ struct __align__(16) Place {
 
 // A thread moves up to kRows rows of a chunk, two pieces of each at a time; chunks in the ring; the
 // chunks whose places are kept: those in the ring and the one behind them.  A cluster's chunks
-// are larger, as its barrier costs more.
+// are larger, as its barrier costs more; its ring has two, for clusters whose CTAs fill their
+// multiprocessors wait for one another (the long contexts with 256 threads of 4 rows and
+// three chunks, 67 us; 512 threads of 2, 55; with four chunks, 80).
 constexpr int kPieces = 2;
 template <bool kCluster>
 struct Shape {
-  static constexpr int kThreads = kCluster ? 256 : 128;
-  static constexpr int kRows = kCluster ? 4 : 2;
-  static constexpr int kStages = kCluster ? 3 : 4;
+  static constexpr int kThreads = kCluster ? 512 : 128;
+  static constexpr int kRows = 2;
+  static constexpr int kStages = kCluster ? 2 : 4;
   static constexpr int kPlaces = kStages + 1;
   static constexpr int kRing = kStages * kRows * kPieces * kThreads * 16;
 
