@@ -160,6 +160,20 @@ def test_strided_views(cuda_lib):
     check(d, pool_of(lay, 1), lay, ev.weights_packed(odd.cpu(), odd[:, :1].cpu(), [0, n], [0, n]), [n], D, [2 * n])
 
 
+@pytest.mark.parametrize("D,gap", [(36, 0), (36, 1), (128, 3), (20, 4)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_rows_that_four_elements_do_not_divide(cuda_lib, dt, D, gap):
+    """On the fp32 pipes: q's tokens `gap` elements apart, k's rows whole, and the other way round."""
+    sa, n = cuda_lib, 140
+    g = torch.Generator().manual_seed(D + gap)
+    wide = torch.randn(n, 4 * D + gap, generator=g).to(DT[dt]).to(DEV)[:, :4 * D].unflatten(1, (4, D))
+    whole = torch.randn(n, 4, D, generator=g).to(DT[dt]).to(DEV)
+    lay = Layout([n], [n], 16, seed=D)
+    for q, k in ((wide, whole[:, :2]), (whole, wide[:, 1:3])):
+        got = sa.attn_weights_packed(q, k, pool_of(lay, 2).to(DEV), lay.table.to(DEV), packed.starts([0, n]), scale=-0.2)
+        check(got, pool_of(lay, 2), lay, ev.weights_packed(q.cpu(), k.cpu(), [0, n], [0, n], -0.2), [n], D, [2 * n])
+
+
 @pytest.mark.parametrize("nq,nk,Hq,Hkv", [([4000], [4000], 2, 1), ([3000, 10], [3000, 9000], 16, 1), ([1], [30000], 8, 1)])
 def test_items_cut_between_multiprocessors_and_the_same_every_time(cuda_lib, nq, nk, Hq, Hkv):
     a = run(cuda_lib, "bf16", nq, nk, Hq, Hkv, 64, pad=0)
