@@ -758,7 +758,7 @@ template <bool kSums>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Params p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int4 c = p.cut[blockIdx.x];
+  const int4 c = __ldcg(p.cut + blockIdx.x);
   if (c.x < 0) return;
   const Seq q = seq_of(p, c.x);
   Item it;
@@ -769,7 +769,9 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Para
   it.nk = q.nk;
   it.id = q.q0 / p.tpt + p.b0 + c.x;
   const int x = static_cast<int>(threadIdx.x);
-  auto part = [&](int cta) { return __ldg(p.part + (static_cast<int64_t>(cta) * 2 + (cta == static_cast<int>(blockIdx.x) ? 1 : 0)) * 256 + x); };
+  // (from L2: the read-only path promises nothing for what is written while this kernel is
+  // already resident, as it may be while the kernel before it still works)
+  auto part = [&](int cta) { return __ldcg(p.part + (static_cast<int64_t>(cta) * 2 + (cta == static_cast<int>(blockIdx.x) ? 1 : 0)) * 256 + x); };
   if constexpr (kSums) {
     float sum = 0.f;
     for (int i = blockIdx.x; i <= c.w; ++i) sum += part(i).x;
