@@ -515,12 +515,13 @@ __device__ void rows(const Params& p, uint8_t* sm, uint64_t* bars, uint32_t tmem
           const int end = min(p.tpt, nq - tok) * p.g - col0;
           const int key = tile * kTile + row;
           const int from = max(key - off - tok, 0) * p.g - col0;
-          // (rows that no query fills hold zeros, and -inf for -L)
-          const bool plain = tok + p.tpt <= nq && __all_sync(0xffffffffu, from <= 0);
+          // (the columns that no head of the group fills, where 128 is no multiple of it, lie behind
+          // `end` in every tile: what their rows hold is anything's)
+          const bool all = __all_sync(0xffffffffu, from <= 0);
           const uint32_t nl = nl0 + ls * kTile * 4;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            if (plain) add_columns<false>(r[q], c2, nl + q * 128, 0, 0, s2);
+            if (all && 32 * q + 32 <= end) add_columns<false>(r[q], c2, nl + q * 128, 0, 0, s2);
             else if (32 * q < end) add_columns<true>(r[q], c2, nl + q * 128, from - 32 * q, end - 32 * q, s2);
           }
         } else {
@@ -716,14 +717,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     wk.o = find(it.count, rest, [&](int o) { return it.before(o); });
     wk.off = pref[wk.b] + wk.h * head + it.before(wk.o);
     wk.fill(p);
-  }
-  if (kSums && p.g * p.tpt < kTile) {
-    // rows of a query tile that no head fills: nothing is loaded there, and nothing that
-    // is not finite may lie there
-    __syncthreads();  // the prefix has been read
-    constexpr int kWords = G::kTileBytes / 16;
-    for (int i = tid; i < G::kStages * kWords; i += kThreads)
-      reinterpret_cast<uint4*>(sm + G::kOffInner)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   fence_proxy_async_smem();  // the scratch becomes a target of TMA
   __syncthreads();

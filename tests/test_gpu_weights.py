@@ -142,6 +142,23 @@ def test_a_nan_query_and_keys_that_are_not_finite(cuda_lib, dt):
     assert torch.isfinite(w).all() and w[20] == 0 and (w[:20] > 0).all()
 
 
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("f16", 128), ("f32", 64)])
+@pytest.mark.parametrize("g", [1, 3, 4, 5, 6, 7, 10, 12, 33, 65, 127])
+def test_keys_of_infinite_scores_in_groups_of_any_size(cuda_lib, dt, D, g):
+    """Keys whose score is -inf for every query receive 0, the others what the definition gives:
+    also where the heads of a group leave rows of a query tile unfilled."""
+    sa, nq, nk = cuda_lib, [260, 40], [260, 500]
+    q, k, _, qs, ks = packed.make(dt, nq, nk, 2 * g, 2, D, seed=g, pad=3)
+    q[:, :, 5] = q[:, :, 5].abs() + 0.1
+    for b in range(2):
+        k[ks[b] + 20, 0, 5] = -math.inf
+        k[ks[b] + 77, :, 5] = -math.inf
+    lay = Layout(nk, nq, 16, seed=g)
+    before = pool_of(lay, 2, g)
+    got = sa.attn_weights_packed(q.to(DEV), k.to(DEV), before.to(DEV), lay.table.to(DEV), packed.starts(qs), packed.starts(ks))
+    check(got, before, lay, ev.weights_packed(q, k, qs, ks), nq, D, [n * g for n in nq])
+
+
 def test_strided_views(cuda_lib):
     sa, D, n = cuda_lib, 128, 150
     g = torch.Generator().manual_seed(7)
