@@ -88,6 +88,7 @@ struct Params {
   float* nlse;        // [query tiles][128]: -L of the rows
   float2* part;       // [CTAs][2][256]: (m, l), or (w, -), of items cut at the range's begin, end
   int4* cut;          // [CTAs]: the item cut at the range's end that begins in it, last CTA
+  int* bad;           // nullable [CTAs]: whether any start of the call, beyond this launch's too, is malformed
   int B, Tq, Tk, Hkv, g;
   int tpt;            // tokens per query tile: 128 / g
   int b0;             // sequences before these
@@ -672,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pref[b + 1] = p.Hkv * it.before(it.count);
     bad = bad || bad_span(p.q_start, b, p.Tq) || bad_span(p.k_start, b, p.Tk);
   }
+  for (int i = tid; p.bad && i < static_cast<int>(gridDim.x); i += kThreads) bad = bad || p.bad[i] != 0;
   if (bad && blockIdx.x == 0 && p.err_word) atomicOr(p.err_word, static_cast<uint32_t>(SA_ERRBIT_SEQ));
   bad = __syncthreads_or(bad);
   if (warp == 0) {
@@ -743,6 +745,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc05::fence_after_sync();
     tc05::tmem_dealloc(tmem, 512);
   }
+}
+
+// Calls of more sequences than a launch takes: every start is looked at before any weight
+// is written.  B: of the whole call.
+__global__ void __launch_bounds__(256) starts_kernel(const __grid_constant__ Params p, int B) {
+  bool bad = false;
+  for (int b = blockIdx.x * 256 + static_cast<int>(threadIdx.x); b < B; b += static_cast<int>(gridDim.x) * 256)
+    bad = bad || bad_span(p.q_start, b, p.Tq) || bad_span(p.k_start, b, p.Tk);
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x != 0) return;
+  p.bad[blockIdx.x] = bad;
+  if (bad && p.err_word) atomicOr(p.err_word, static_cast<uint32_t>(SA_ERRBIT_SEQ));
 }
 
 // Items cut between CTAs: a block for each CTA, which does something where an item
@@ -838,6 +852,8 @@ int launch_t(const WeightsArgs& a, cudaStream_t st) {
   ws += up256(static_cast<size_t>(sms) * 2 * 256 * sizeof(float2));
   p.cut = reinterpret_cast<int4*>(ws);
   ws += up256(static_cast<size_t>(sms) * sizeof(int4));
+  int* bad = reinterpret_cast<int*>(ws);
+  ws += up256(static_cast<size_t>(sms) * sizeof(int));
   p.nlse = reinterpret_cast<float*>(ws);
   p.weights = a.weights;
   p.err_word = a.err_word;
@@ -857,6 +873,12 @@ int launch_t(const WeightsArgs& a, cudaStream_t st) {
   auto stats = weights_kernel<D, T, false>;
   auto sums = weights_kernel<D, T, true>;
   if (!allow_smem(reinterpret_cast<const void*>(stats)) || !allow_smem(reinterpret_cast<const void*>(sums))) return -1;
+  if (a.B > kMaxSeqs) {
+    p.q_start = a.q_start;
+    p.k_start = a.k_start;
+    p.bad = bad;
+    if (launch_after(starts_kernel, sms, 256, 0, st, false, p, static_cast<int>(a.B)) != 0) return -1;
+  }
   for (int64_t b0 = 0; b0 < a.B; b0 += kMaxSeqs) {
     p.q_start = a.q_start + b0;
     p.k_start = a.k_start + b0;
@@ -883,7 +905,7 @@ bool weights_tc_supported(const WeightsArgs& a) {
 size_t weights_tc_workspace(const WeightsArgs& a) {
   const size_t sms = static_cast<size_t>(sm_count());
   const int64_t tpt = kTile / (a.Hq / a.Hkv);
-  return up256(sms * 2 * 256 * sizeof(float2)) + up256(sms * sizeof(int4)) +
+  return up256(sms * 2 * 256 * sizeof(float2)) + up256(sms * sizeof(int4)) + up256(sms * sizeof(int)) +
          static_cast<size_t>(a.Tq / tpt + a.B + 1) * static_cast<size_t>(a.Hkv) * kTile * sizeof(float);
 }
 

@@ -244,6 +244,32 @@ def test_malformed_starts_write_nothing(cuda_lib, dt):
         assert int(err) == sa.ERRBIT_SEQ and torch.equal(got, before)
 
 
+@pytest.mark.parametrize("accumulate", [True, False])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_malformed_starts_of_many_sequences_write_nothing(cuda_lib, dt, accumulate):
+    """A bad start anywhere among more sequences than a launch takes: none of them is written."""
+    sa, B = cuda_lib, 2600
+    nq, nk = [1, 2] * (B // 2), [3, 2] * (B // 2)
+    q, k, _, qs, ks = packed.make(dt, nq, nk, 4, 2, 64, seed=13, pad=0)
+    lay = Layout(nk, nq, 16, seed=13)
+    t, before = lay.table.to(DEV), pool_of(lay, 2).to(DEV)
+    q, k, ws = q.to(DEV), k.to(DEV), ev.weights_packed(q, k, qs, ks)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for at, by in ((B, 1), (1500, 50), (3, -40), (2047, 20)):
+        for which in (0, 1):
+            bad = [list(qs), list(ks)]
+            bad[which][at] += by
+            got = before.clone()
+            err.zero_()
+            sa.attn_weights_packed(q, k, got, t, packed.starts(bad[0]), packed.starts(bad[1]), accumulate=accumulate, err_word=err)
+            assert int(err) == sa.ERRBIT_SEQ and torch.equal(got, before), (at, by, which)
+    got = before.clone()
+    err.zero_()
+    sa.attn_weights_packed(q, k, got, t, packed.starts(qs), packed.starts(ks), accumulate=accumulate, err_word=err)
+    assert int(err) == 0
+    check(got, before.cpu(), lay, ws, nq if accumulate else nk, 64, [2 * n for n in nq])
+
+
 def test_captured_and_on_two_streams(cuda_lib):
     sa, nq, nk = cuda_lib, [300, 64], [500, 640]
     q, k, _, qs, ks = packed.make("bf16", nq, nk, 8, 2, 128, seed=10)
