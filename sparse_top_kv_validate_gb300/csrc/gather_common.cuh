@@ -63,11 +63,13 @@ __device__ __forceinline__ bool dense_visible(const GatherArgs& a, int64_t b, in
   return !(a.causal && c > off + i);
 }
 
-// What the weights of a decode row need of it: its maximum and the inverse of its
-// sum (0 where it saw nothing; NaN where it saw a NaN).
-__device__ __forceinline__ float2 row_stat(float m, float l) {
-  return make_float2(m, l != l ? l : (m == SA_NEG_INF || l == 0.f) ? 0.f : 1.0f / l);
+// The inverse of a row's sum: 0 where it saw nothing, NaN where it saw a NaN (a row of
+// nothing but NaN scores has no maximum either).
+__device__ __forceinline__ float row_inverse(float m, float l) {
+  return l != l ? l : (m == SA_NEG_INF || l == 0.f) ? 0.f : 1.0f / l;
 }
+// What the weights of a decode row need of it: its maximum and the inverse of its sum.
+__device__ __forceinline__ float2 row_stat(float m, float l) { return make_float2(m, row_inverse(m, l)); }
 
 // Per-batch write position of the fused current-token append.
 __device__ __forceinline__ int64_t write_pos_of(const GatherArgs& a, int64_t b) {

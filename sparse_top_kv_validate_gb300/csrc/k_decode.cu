@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(128) gather_simt_kernel(GatherArgs a) {
     if (a.splits == 1) {
       float LL = L;
       if (a.sink && M != SA_NEG_INF) LL += exp2f(a.sink[h] * kLog2e - M);
-      const float out = (M == SA_NEG_INF || LL == 0.f) ? 0.f : acc / LL;
+      const float out = LL == LL && (M == SA_NEG_INF || LL == 0.f) ? 0.f : acc / LL;
       static_cast<T*>(a.y)[((u.b * a.Hq + h) * a.Sq + u.i) * D + d] = from_f32<T>(out);
     } else {
       const int64_t pidx = (unit * a.splits + split) * a.hpu + hh;
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(128) combine_kernel(GatherArgs a) {
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (lane == 0) {
       if (a.sink && M != SA_NEG_INF) L += ex2(a.sink[h] * kLog2e - M);
-      inv_s = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
+      inv_s = row_inverse(M, L);
     }
   }
   __syncthreads();
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(256) combine_flat_kernel(GatherArgs a) {
     acc.w = fmaf(o[s].w, w, acc.w);
   }
   if (a.sink && M != SA_NEG_INF) L += ex2(a.sink[h] * kLog2e - M);
-  const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
+  const float inv = row_inverse(M, L);
   T* yp = static_cast<T*>(a.y) + ((u.b * a.Hq + h) * a.Sq + u.i) * a.Dv + d;
   store4<T>(yp, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }

@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(128) stream_combine_kernel(GatherArgs a) {
       for (int wi = 0; wi < kRegW; ++wi)
         if (wi < nw) M = fmaxf(M, ml[wi].x);
       const float Mu = (M == SA_NEG_INF) ? 0.f : M;
-      float L = 0.f, lost = 0.f;  // lost: NaN when a partial of nothing but NaN scores is left out
+      float L = 0.f, lost = 0.f;  // lost: NaN when a partial of nothing but NaN scores is left out, else 0
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int wi = 0; wi < kRegW; ++wi) {
@@ -645,9 +645,10 @@ __global__ void __launch_bounds__(128) stream_combine_kernel(GatherArgs a) {
           acc.w = fmaf(v[wi].w, f, acc.w);
         }
       }
-      if (a.stats && d == 0) a.stats[ui.b * a.Hq + ui.h0 + hh] = row_stat(M, L + lost);
+      L += lost;
+      if (a.stats && d == 0) a.stats[ui.b * a.Hq + ui.h0 + hh] = row_stat(M, L);
       if (a.sink && M != SA_NEG_INF) L += ex2(a.sink[ui.h0 + hh] * kLog2e - M);
-      const float inv = (M == SA_NEG_INF || L == 0.f) ? 0.f : 1.0f / L;
+      const float inv = row_inverse(M, L);
       T* yp = static_cast<T*>(a.y) + ((ui.b * a.Hq + ui.h0 + hh) * a.Sq + ui.i) * D + d;
       yp[0] = from_f32<T>(acc.x * inv);
       yp[1] = from_f32<T>(acc.y * inv);

@@ -583,3 +583,17 @@ def test_full_size_fp8_sampled_rows(cuda_lib):
                                       records=inp["kv_records"][b:b + 1].cpu(), n_rope=c.n_rope,
                                       scale=c.eff_scale(), window=c.window, rows=heads)
         assert_close(to64(y[b, heads]), ref, y.dtype, f"fp8 full b={b}")
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("f16", 128), ("f32", 64), ("f32", 72)])
+@pytest.mark.parametrize("K", [9, 40, 128, 700])
+def test_a_nan_query_comes_out_as_nan_however_its_row_is_split(cuda_lib, dt, D, K):
+    """A head whose scores are all NaN gives NaN, and only it; a row that selects nothing gives 0."""
+    q, k, v = synth.normal((2, 4, 1, D), dt, 1), synth.normal((2, 2, 900, D), dt, 2), synth.normal((2, 2, 900, D), dt, 3)
+    idx = synth.sorted_sample_rows(2, 0, 900, K, 4).reshape(2, 1, 1, K)
+    idx[1] = -1
+    q[0, 1, 0, 3] = float("nan")
+    q[1, 2, 0, 3] = float("nan")
+    y = cuda_lib.sparse_attn_decode(q.to(DEV), k.to(DEV), v.to(DEV), idx.to(DEV)).cpu()
+    assert torch.isnan(y[0, 1]).all() and torch.isfinite(y[0, [0, 2, 3]]).all()
+    assert (y[1] == 0).all()

@@ -479,6 +479,45 @@ def test_decode_nan_and_shared_pages(cuda_lib):
         assert torch.isnan(w.cpu()[page, 0, slot]).all()
 
 
+# contexts of one partial, of a few and of many (16 tokens to a warp where there are few)
+@pytest.mark.parametrize("n", [9, 20, 100, 127, 150, 1200, 9000])
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("f16", 128), ("f32", 64), ("f32", 72)])
+def test_a_nan_reaches_y_and_the_weights_alike(cuda_lib, dt, D, n):
+    """A query with a NaN, and a key with one: the output and the weights of what sees it are
+    NaN and the others' are not, however many parts a context was split into."""
+    sa, Hkv, g = cuda_lib, 2, 3
+    lay = Layout([n, 40], [1, 1], 16, seed=n)
+    kp, vp = elements(lay, Hkv, D, dt, n)
+    q = torch.randn(2, Hkv * g, D, generator=torch.Generator().manual_seed(n)).to(DT[dt])
+    table, ctx, _ = lay.gpu()
+    page, slot = ev.token_places(lay.table[0], n, 16)
+    before = pool_of(lay, Hkv, n)
+
+    def both(q, kp):
+        w = before.to(DEV)
+        y = sa.paged_attn_decode(q.to(DEV), kp.to(DEV), vp.to(DEV), table, ctx, weights=w)
+        plain = sa.paged_attn_decode(q.to(DEV), kp.to(DEV), vp.to(DEV), table, ctx)
+        assert torch.equal(torch.isnan(y), torch.isnan(plain)) and torch.equal(torch.nan_to_num(y), torch.nan_to_num(plain))
+        return torch.isnan(y.cpu()), torch.isnan(w.cpu())
+
+    bad = q.clone()
+    bad[0, 1, 7] = math.nan                                 # a head of KV head 0
+    ny, nw = both(bad, kp)
+    assert ny[0, 1].all() and ny.sum() == D
+    assert nw[page, 0, slot].all() and nw.sum() == n
+    for t in sorted({0, n // 2, n - 1}):                    # a key of KV head 1
+        kb = kp.clone()
+        kb[page[t], 1, slot[t], 3] = math.nan
+        ny, nw = both(q, kb)
+        assert ny[0, g:].all() and ny.sum() == g * D, t
+        assert nw[page, 1, slot].all() and nw.sum() == n, t
+    kb = kp.clone()                                         # a run of keys
+    kb[page[n // 3:2 * n // 3 + 1], 1, slot[n // 3:2 * n // 3 + 1], 3] = math.nan
+    ny, nw = both(q, kb)
+    assert ny[0, g:].all() and ny.sum() == g * D
+    assert nw[page, 1, slot].all() and nw.sum() == n
+
+
 def test_decode_refusals(cuda_lib):
     sa, D = cuda_lib, 64
     kp, vp = sa.new_fp8_pool(4, 2, 16, D), sa.new_fp8_pool(4, 2, 16, D)
