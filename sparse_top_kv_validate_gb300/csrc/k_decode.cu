@@ -30,6 +30,8 @@
 //  * paged_append_kernel: writes the new token into its page before a paged
 //    decode.
 // Results are deterministic run to run (fixed warp and split order).
+#include <cfloat>
+
 #include "gather_common.cuh"
 
 namespace sa {
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(128) gather_simt_kernel(GatherArgs a) {
     q[k] = d < D ? to_f32<T>(qp[d]) : 0.f;
     o[k] = 0.f;
   }
-  float m = SA_NEG_INF, l = 0.f;
+  float m = -FLT_MAX, l = 0.f;  // (finite: a score of -inf before any other has no -inf less -inf)
   const T* kp = static_cast<const T*>(a.k);
   const T* vp = static_cast<const T*>(a.v);
   const float sl2 = a.scale_log2;
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(128) gather_simt_kernel(GatherArgs a) {
       }
       if (score && lane == 0) *score = x;
       const float mn = fmaxf(m, x);
-      const float al = exp2f(m - mn);  // m == -inf -> 0
+      const float al = exp2f(m - mn);  // nothing before -> 0
       const float p = exp2f(x - mn);
       l = l * al + p;
 #pragma unroll
@@ -182,6 +184,7 @@ __global__ void __launch_bounds__(128) gather_simt_kernel(GatherArgs a) {
       m = mn;
     }
   }
+  if (m == -FLT_MAX && !(l > 0.f)) m = SA_NEG_INF;  // saw nothing, or nothing but -inf or NaN
 #pragma unroll
   for (int k = 0; k < DPL; ++k) sm_o[warp][lane + 32 * k] = o[k];
   if (lane == 0) {

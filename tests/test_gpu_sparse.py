@@ -597,3 +597,17 @@ def test_a_nan_query_comes_out_as_nan_however_its_row_is_split(cuda_lib, dt, D, 
     y = cuda_lib.sparse_attn_decode(q.to(DEV), k.to(DEV), v.to(DEV), idx.to(DEV)).cpu()
     assert torch.isnan(y[0, 1]).all() and torch.isfinite(y[0, [0, 2, 3]]).all()
     assert (y[1] == 0).all()
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("f32", 64), ("f32", 72)])
+def test_selected_keys_of_infinite_scores_have_no_part(cuda_lib, dt, D):
+    """Keys whose score is -inf, the first of every thread's among them: as if not selected."""
+    q, k, v = synth.normal((1, 4, 1, D), dt, 1), synth.normal((1, 2, 300, D), dt, 2), synth.normal((1, 2, 300, D), dt, 3)
+    q[..., 3] = q[..., 3].abs() + 0.1
+    idx = torch.arange(0, 300, 2, dtype=torch.int32)
+    low = idx[[0, 1, 2, 3, 4, 5, 64, 65, 66, 67, 128, 149]]
+    k[:, :, low.long(), 3] = -float("inf")
+    rest = torch.tensor([i for i in idx.tolist() if i not in low.tolist()], dtype=torch.int32)
+    y = cuda_lib.sparse_attn_decode(q.to(DEV), k.to(DEV), v.to(DEV), idx.reshape(1, 1, 1, -1).to(DEV))
+    want = oracle.sparse_attention(q, rest.reshape(1, 1, 1, -1), k, v, scale=D ** -0.5)
+    assert_close(to64(y), want, y.dtype, f"-inf scores {dt}")

@@ -518,6 +518,43 @@ def test_a_nan_reaches_y_and_the_weights_alike(cuda_lib, dt, D, n):
     assert nw[page, 1, slot].all() and nw.sum() == n
 
 
+def y_of(q, k, v, scale):
+    """A decode's y [Hq, D] of one sequence in 64 bits, and sum p |v|: q [Hq, D], k and v [Hkv, n, D]."""
+    qq = q.double().view(k.shape[0], -1, q.shape[-1])
+    p = ev._softmax(qq @ k.double().transpose(1, 2) * scale)
+    return (p @ v.double()).view(q.shape), (p @ v.double().abs()).view(q.shape)
+
+
+@pytest.mark.parametrize("n", [9, 100, 1200])
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("f16", 80), ("f32", 64), ("f32", 256)])
+def test_a_decode_of_keys_with_infinite_scores(cuda_lib, dt, D, n):
+    """Keys whose score is -inf, the first of every thread's among them, have no part in y and
+    receive 0.  Off by a probability's bound (its rounding to 16 bits added) times sum p |v|,
+    and half a step of y."""
+    sa, Hkv, g = cuda_lib, 2, 2
+    lay = Layout([n, 5], [1, 1], 16, seed=n)
+    kp, vp = elements(lay, Hkv, D, dt, n)
+    q = torch.randn(2, Hkv * g, D, generator=torch.Generator().manual_seed(n)).to(DT[dt])
+    q[:, :, 2] = q[:, :, 2].abs() + 0.1
+    page, slot = ev.token_places(lay.table[0], n, 16)
+    for t in (0, 1, 2, 3, 5, n // 2, n - 1):
+        kp[page[t], :, slot[t], 2] = -math.inf
+    before = pool_of(lay, Hkv, n)
+    w = before.to(DEV)
+    table, ctx, _ = lay.gpu()
+    y = sa.paged_attn_decode(q.to(DEV), kp.to(DEV), vp.to(DEV), table, ctx, weights=w).cpu()
+    ws, s = [], 1 / math.sqrt(D)
+    for b in range(2):
+        k, v = keys_of(lay, kp, b, D), keys_of(lay, vp, b, D)
+        low = torch.nan_to_num(k, neginf=0.0)               # (of finite magnitudes, the bound's)
+        ws.append((ev.weights_decode(q[b], k, s)[0], ev.weights_decode(q[b], low, s)[1]))
+        want, mag = y_of(q[b], k, v, s)
+        fi = torch.finfo(y.dtype)
+        rel = rel_bound(D, ws[b][1], 1) + lay.ctx[b] * 2.0 ** -22 + (0 if dt == "f32" else fi.eps / 2)
+        assert ((y[b].double() - want).abs() <= rel * mag + (want.abs() + rel * mag) * fi.eps / 2 + 1e-30).all()
+    check(w, before, lay, ws, [1, 1], D, [g, g])
+
+
 def test_decode_refusals(cuda_lib):
     sa, D = cuda_lib, 64
     kp, vp = sa.new_fp8_pool(4, 2, 16, D), sa.new_fp8_pool(4, 2, 16, D)
