@@ -92,8 +92,11 @@ __device__ __forceinline__ int32_t resolve_candidate(const GatherArgs& a, const 
 // ---------------------------------------------------------------------------
 // One CTA per (unit, head, split); warps stride over candidates; lanes hold
 // DPL dims each (d = lane + 32 * k).  fp32 FMA throughout.
+// kScores: a paged request whose scores are kept for the tokens' weights (an instance of
+// its own: tested for in every one, 16 contexts of 8,192 tokens in fp32 took 1,376 us
+// against 1,067).
 
-template <typename T, int DPL>
+template <typename T, int DPL, bool kScores>
 __global__ void __launch_bounds__(128) gather_simt_kernel(GatherArgs a) {
   __shared__ float sm_o[4][DPL * 32];
   __shared__ float sm_ml[4][2];
@@ -149,10 +152,10 @@ __global__ void __launch_bounds__(128) gather_simt_kernel(GatherArgs a) {
 #pragma unroll
     for (int t = 0; t < kU; ++t) {
       const int32_t row = rows[t];
-      // (paged: the scores that the tokens' weights are formed from, -inf for a bad page)
-      float* score = a.scores && cb + 4 * t < c1 ? a.scores + (u.b * a.Hq + h) * a.score_stride + cb + 4 * t : nullptr;
+      float* score = nullptr;  // -inf for a bad page
+      if (kScores && cb + 4 * t < c1) score = a.scores + (u.b * a.Hq + h) * a.score_stride + cb + 4 * t;
       if (row < 0) {
-        if (score && lane == 0) *score = SA_NEG_INF;
+        if (kScores && score && lane == 0) *score = SA_NEG_INF;
         continue;
       }
       float dot = 0.f;
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(128) gather_simt_kernel(GatherArgs a) {
         x += kLog2e * bias_term(a, u.b, h, u.i, j);
         if (x == SA_NEG_INF) continue;  // a -inf term masks the key
       }
-      if (score && lane == 0) *score = x;
+      if (kScores && lane == 0) *score = x;
       const float mn = fmaxf(m, x);
       const float al = exp2f(m - mn);  // nothing before -> 0
       const float p = exp2f(x - mn);
@@ -347,8 +350,9 @@ int launch_paged_append(const PagedAppendArgs& a, cudaStream_t st) {
 
 template <typename T, int DPL>
 static int launch_simt(const GatherArgs& a, cudaStream_t st) {
-  const int64_t grid = a.units * a.hpu * a.splits;
-  gather_simt_kernel<T, DPL><<<static_cast<unsigned>(grid), 128, 0, st>>>(a);
+  const unsigned grid = static_cast<unsigned>(a.units * a.hpu * a.splits);
+  if (a.scores) gather_simt_kernel<T, DPL, true><<<grid, 128, 0, st>>>(a);
+  else gather_simt_kernel<T, DPL, false><<<grid, 128, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
