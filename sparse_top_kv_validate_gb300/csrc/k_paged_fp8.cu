@@ -794,14 +794,14 @@ __global__ void __launch_bounds__(128) fp8_combine_kernel(const GatherArgs a) {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int64_t c = c0; c <= c1; c += 8) {
     float2 e[8];
-    float4 v[8];
+    float4 v[8];  // (not through the read-only path: written while this kernel may be resident)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       e[i] = make_float2(SA_NEG_INF, 0.f);
       v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c + i <= c1) {
-        e[i] = __ldg(ml + part(c + i));
-        v[i] = __ldg(reinterpret_cast<const float4*>(a.part_o + part(c + i) * a.D + d));
+        e[i] = ml[part(c + i)];
+        v[i] = *reinterpret_cast<const float4*>(a.part_o + part(c + i) * a.D + d);
       }
     }
     float mn = M;

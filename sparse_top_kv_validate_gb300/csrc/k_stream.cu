@@ -608,7 +608,9 @@ __global__ void __launch_bounds__(128) stream_combine_kernel(GatherArgs a) {
   if (nw <= kRegW) {
     // Few partials: every thread loads all it needs at once -- its float4 of
     // each partial and its head's (m, l) of each -- then merges in registers:
-    // one round trip to L2 after the stream kernel ends.
+    // one round trip to L2 after the stream kernel ends.  (Plain loads: the read-only path
+    // promises nothing for what is written while this kernel is resident, and loads that
+    // must come from L2 are issued one after the other, 8 us more.)
     constexpr int kG2 = (16 * D / 4 + 127) / 128;
 #pragma unroll
     for (int g = 0; g < kG2; ++g) {
@@ -622,8 +624,8 @@ __global__ void __launch_bounds__(128) stream_combine_kernel(GatherArgs a) {
         if (wi < nw) {
           const int64_t w = w_lo + wi;
           const int64_t sb = (w * 2 + ((w * R >= off) ? 0 : 1)) * a.hpu + hh;
-          v[wi] = __ldg(reinterpret_cast<const float4*>(a.part_o + sb * D + d));
-          ml[wi] = __ldg(reinterpret_cast<const float2*>(a.part_ml) + sb);
+          v[wi] = *reinterpret_cast<const float4*>(a.part_o + sb * D + d);
+          ml[wi] = reinterpret_cast<const float2*>(a.part_ml)[sb];
         }
       }
       float M = SA_NEG_INF;
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(128) stream_combine_kernel(GatherArgs a) {
       const int64_t w = w_lo + w0 + wi;
       const int sl = (w * R >= off) ? 0 : 1;  // the unit begins inside w's range
       const float2 ml =
-          __ldg(reinterpret_cast<const float2*>(a.part_ml) + (w * 2 + sl) * a.hpu + hh);
+          reinterpret_cast<const float2*>(a.part_ml)[(w * 2 + sl) * a.hpu + hh];
       sm_m[wi][hh] = ml.x;
       sm_l[wi][hh] = ml.y;
     }
@@ -717,8 +719,8 @@ __global__ void __launch_bounds__(128) stream_combine_kernel(GatherArgs a) {
         const int64_t w = w_lo + w0 + wi;
         const int sl = (w * R >= off) ? 0 : 1;
         const float f = sm_m[wi][hh];
-        const float4 v = __ldg(reinterpret_cast<const float4*>(
-            a.part_o + ((w * 2 + sl) * a.hpu + hh) * D + d));
+        const float4 v = *reinterpret_cast<const float4*>(
+            a.part_o + ((w * 2 + sl) * a.hpu + hh) * D + d);
         s4.x += v.x * f;
         s4.y += v.y * f;
         s4.z += v.z * f;
