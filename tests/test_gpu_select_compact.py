@@ -370,3 +370,47 @@ def test_a_cache_kept_within_its_budget(cuda_lib, quantised):
         fp8.check(y[:, :, None], q1[:, :, None], lay, [p.cpu() for p in pools])
     cut()
     assert ctx.tolist() == [64, 60, 64] and int(err) == 0
+
+
+@pytest.mark.parametrize("quantised", [True, False])
+def test_a_captured_step_that_keeps_its_budget(cuda_lib, quantised):
+    """A token written and attended to, the tokens to keep selected, their rows moved, the
+    lengths set back: one graph, replayed with new tokens, against the calls one by one."""
+    sa, Hq, Hkv, D, pt, budget, sink, recent = cuda_lib, 8, 2, 64, 16, 40, 2, 8
+    n = [39, 40, 7]
+    lay = Layout([budget + 1] * 3, [1] * 3, pt, seed=15)
+    table = lay.table.to(DEV)
+    pools = [p.to(DEV) for p in (fp8.fill(lay, Hkv, D, 15) if quantised else wt.elements(lay, Hkv, D, "bf16", 15))]
+    w, ctx = wt.pool_of(lay, Hkv, 15).to(DEV), torch.tensor(n, dtype=torch.int32, device=DEV)
+    q, k, v = (torch.zeros(3, H, D, dtype=torch.bfloat16, device=DEV) for H in (Hq, Hkv, Hkv))
+    err, gen = torch.zeros(1, dtype=torch.int32, device=DEV), torch.Generator().manual_seed(15)
+
+    def step(pools, w, ctx):
+        ctx += 1
+        y = sa.paged_attn_decode(q, *pools, table, ctx, k_new=k, v_new=v, weights=w, err_word=err)
+        seen = w.clone()
+        keep, left = sa.paged_kv_select(w, table, ctx, budget, sink=sink, recent=recent, err_word=err)
+        sa.paged_kv_compact(*pools, table, ctx, keep, weights=w, head_dim=D, err_word=err)
+        ctx.copy_(left)
+        return y, seen, keep
+
+    step([p.clone() for p in pools], w.clone(), ctx.clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(pools, w, ctx)
+    for _ in range(6):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, generator=gen).bfloat16())
+        lens = [c + 1 for c in ctx.tolist()]
+        own = [p.clone() for p in pools], w.clone(), ctx.clone()
+        graph.replay()
+        want = step(*own)
+        for a, b in zip((*out, *pools, w, ctx), (*want, *own[0], own[1], own[2])):
+            assert torch.equal(a, b)
+        for b, c in enumerate(lens):
+            page, slot = ev.token_places(lay.table[b], c, pt)
+            for h in range(Hkv):
+                rows = ev.select_row(out[1].cpu()[page, h, slot].tolist(), budget, sink, recent)
+                assert out[2][b, h].tolist() == rows + [-1] * (budget - len(rows))
+    assert ctx.tolist() == [40, 40, 13] and int(err) == 0
