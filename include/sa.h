@@ -796,8 +796,10 @@ int attn_prefill_packed(const sa_packed_params* p, void* stream);
  * weight is the sum of the softmax probabilities that the queries of the KV head's
  * group give it.  Two calls accumulate it.  Both SET the weights of the tokens that
  * are new with them (so that a page that changes hands needs no clearing) and ADD to
- * the others'.  A page that two sequences of one call share receives the weights of
- * both, in no order.  Sums and softmax statistics are fp32.
+ * the others'.  Of a page that two sequences of one call share, a token to which both
+ * add receives the weights of both, in no order; one that either sets holds the weights
+ * of either, added to or not (let one sequence alone set such tokens).
+ * Sums and softmax statistics are fp32.
  *
  * After a compaction a token's place in its pages is no longer its position: rotate
  * with rotary_embed and the true positions, and write with paged_kv_write without a rope.
@@ -813,7 +815,8 @@ int attn_prefill_packed(const sa_packed_params* p, void* stream);
  * and the weight of token j is set to w_j where j >= nk - nq (the queries' own tokens) or
  * accumulate is 0, else w_j is added to it.  All queries of a prompt, a chunk's, or
  * the last few of a context may be given.  Sequences without queries or keys, and
- * slots that hold no token, are left as they are.
+ * slots that hold no token, are left as they are.  The scores have no softcap: the weights
+ * are not those that attn_prefill_packed gives with one.
  * scale 0 means 1/sqrt(D).  dtype SA_F16 / SA_BF16 with D 64 or 128, a positive scale,
  * Hq / Hkv <= 128 and 16-byte aligned pointers and strides run on the tcgen05 tensor
  * cores; other shapes (SA_F32, D a multiple of 4 up to 256) take a kernel on the fp32

@@ -1373,7 +1373,8 @@ def attn_weights_packed(q, k, weights, block_table, q_start, k_start=None, *, sc
     ``weights`` (float32 ``[num_pages, Hkv, page_tokens]``, through ``block_table`` int32
     ``[B, max_pages]``) becomes the sum of the probabilities that the queries of the head's group
     give it: set for the queries' own tokens, added to the others', or set for all with
-    ``accumulate=False``.  Returns ``weights``."""
+    ``accumulate=False`` (of a page that two sequences share, to those of either).  The scores
+    have no softcap.  Returns ``weights``."""
     L = load()
     qs, qst = _rows(q, "q")
     ks, kst = _rows(k, "k", q.dtype)

@@ -232,6 +232,41 @@ def test_bad_pages_are_reported_and_skipped(cuda_lib):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_prefix_that_sequences_share(cuda_lib, dt):
+    """Weights added to the tokens of a page of two sequences come from both; weights that are
+    set there are those of either."""
+    sa, D, Hkv, g, pt = cuda_lib, 64, 2, 3, 16
+    nq, nk, common = [20, 130], [52, 162], 32
+    q, k, _, qs, ks = packed.make(dt, nq, nk, Hkv * g, Hkv, D, seed=14, pad=0)
+    k[ks[1]:ks[1] + common] = k[:common]
+    lay = Layout(nk, nq, pt, seed=14)
+    lay.table[1, :common // pt] = lay.table[0, :common // pt]
+    ws = ev.weights_packed(q, k, qs, ks)
+    before = pool_of(lay, Hkv, 14)
+    page, slot = ev.token_places(lay.table[0], common, pt)
+    for accumulate in (True, False):
+        got = sa.attn_weights_packed(q.to(DEV), k.to(DEV), before.to(DEV), lay.table.to(DEV), packed.starts(qs),
+                                     packed.starts(ks), accumulate=accumulate).cpu()
+        have = got[page, :, slot].double()
+        parts = [w[:, :common].T for w, _ in ws]
+        rel = [rel_bound(D, m, n * g) for (_, m), n in zip(ws, nq)]
+        if accumulate:                                      # (two additions, in either order)
+            want = before[page, :, slot].double() + parts[0] + parts[1]
+            tol = parts[0] * rel[0] + parts[1] * rel[1] + want.abs() * 2.0 ** -23
+            assert ((have - want).abs() <= tol).all()
+        else:
+            near = [(have - w).abs() <= w * (r + 2.0 ** -24) + 1e-30 for w, r in zip(parts, rel)]
+            assert (near[0] | near[1]).all()
+        for b in range(2):                                  # their own tokens
+            p, s = ev.token_places(lay.table[b], nk[b], pt)
+            w = ws[b][0][:, common:].T
+            have = got[p, :, s][common:].double()
+            old = before[p, :, s][common:].double() if accumulate else torch.zeros_like(w)
+            old[len(old) - nq[b]:] = 0
+            assert ((have - old - w).abs() <= w * rel[b] + (old + w) * 2.0 ** -24 + 1e-30).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_malformed_starts_write_nothing(cuda_lib, dt):
     sa = cuda_lib
     q, k, _, qs, ks = packed.make(dt, [40, 9], [64, 30], 4, 2, 64, seed=9, pad=0)
