@@ -27,6 +27,9 @@
 //  * Per tile: S^T = K . Q^T and O^T += V^T . P^T on the m16n8k16 tensor-core
 //    MMA with keys as M and the GQA group as N (P^T from the S^T accumulator
 //    by an in-register 8x8 transpose), online softmax in the log2 domain.
+//    A probability is rounded once to the storage type for its product with V
+//    (half a step, 2^-8 of it in bf16 and 2^-11 in f16: the MMA takes both operands in one
+//    type); scores, sums and outputs are fp32.
 //  * A unit inside one warp's range is written directly; a unit split across
 //    warps leaves one partial per warp, merged by stream_combine_kernel in
 //    warp order (deterministic).

@@ -100,8 +100,10 @@ struct Params {
 
 // ---- items and their places ------------------------------------------------------------
 
-// sum_{i < n} floor((a i + b) / m), the Euclidean recurrence.  (Tokens stay below 2^30, so
-// that a n + b, with a and b reduced, fits 32 bits.)
+// sum_{i < n} floor((a i + b) / m) by Euclid's algorithm on (a, m): the quotients leave the sum,
+// and the points under the line that is left are counted along the other axis (Graham, Knuth,
+// Patashnik, Concrete Mathematics, 3.5).  (Tokens stay below 2^30, so that a n + b, with a
+// and b reduced, fits 32 bits.)
 __device__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t s = 0;
   while (n > 0) {
