@@ -810,34 +810,34 @@ KERNEL_SOURCES = {
 TRAFFIC: dict = {
     # workload: (kernel, bytes per launch, source hash at capture, how)
     "csa_fp8_b16_h128_d576_t65536_k2048_w128": (
-        "fp8_tc05_kernel", 42_666_496, "4d5499920cc78155",
+        "fp8_tc05_kernel", 42_667_008, "4ef6193e246c06b9",
         "ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum, one launch of the bench's own "
         "workload (42.67 MB read, 0 written; ncu starts each kernel with cold caches, so the "
         "decoded rows are read from DRAM here and from L2 in a live call)"),
     "index_select_b16_ih64_id128_r16384_k2048": (
-        "index_score_kernel", 18_047_232, "7b8479ac54a89ab1",
-        "ncu --set full, one launch of the bench's own workload (18.05 MB read, 0 written: the "
-        "index records once)"),
+        "index_score_kernel", 18_047_232, "e8fc125601c23329",
+        "ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum, one launch of the bench's own "
+        "workload (18.05 MB read, 0 written: the index records once)"),
     "csa_ref_b16_h128_d512_l128_t65536_k2048": (
-        "fp8_tc05_kernel", 37_858_048, "4d5499920cc78155",
+        "fp8_tc05_kernel", 37_857_024, "4ef6193e246c06b9",
         "ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum, one launch of the bench's own "
-        "workload (37.86 MB read, 1,280 B written; cold caches under ncu, as above)"),
-    "compress_r4": ("compress_r4_kernel", 546_426_624, "89fe5929934292d9",
+        "workload (37.86 MB read, 0 written; cold caches under ncu, as above)"),
+    "compress_r4": ("compress_r4_kernel", 546_680_576, "fa1e5e4487b2e6b8",
                     "ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum, one launch of the "
-                    "bench's own workload (536.98 MB read, 9.45 MB written)"),
+                    "bench's own workload (536.98 MB read, 9.70 MB written)"),
     "sparse_bf16_b32_h64_kv8_d128_t8192_k2048": (
-        "gather_stream_kernel", 274_255_872, "96f01ec1f92b7531",
+        "gather_stream_kernel", 274_385_152, "7618eb679aa8c278",
         "ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum, one launch of the bench's own "
-        "workload (270.69 MB read, 3.57 MB written)"),
+        "workload (270.69 MB read, 3.70 MB written)"),
     "paged_fp16_b128_h32_kv8_d128_ctx1k-32k_p16": (
-        "gather_stream_kernel", 8_926_250_739, "96f01ec1f92b7531",
+        "gather_stream_kernel", 8_925_423_141, "7618eb679aa8c278",
         "ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum, one launch of the same "
-        "sequences' distribution at 16 sequences (workload paged_fp16_b16: 1,159.68 MB, 1.0034 x "
+        "sequences' distribution at 16 sequences (workload paged_fp16_b16: 1,159.58 MB, 1.0033 x "
         "its algorithmic bytes), scaled by the algorithmic bytes to the 128-sequence batch"),
     "prefill_bf16_b4_s4096_h32_kv8_d128_causal_softcap50": (
-        "prefill_tc05_kernel", 427_458_048, "b003441e58206e07",
+        "prefill_tc05_kernel", 436_415_488, "742e374ad7f928a8",
         "ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum, one launch of the bench's own "
-        "workload (272.07 MB read, 155.39 MB written: part of Y and the present K/V is still in "
+        "workload (280.81 MB read, 155.60 MB written: part of Y and the present K/V is still in "
         "L2 when the kernel ends)"),
 }
 
