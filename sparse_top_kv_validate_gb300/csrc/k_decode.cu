@@ -93,8 +93,8 @@ __device__ __forceinline__ int32_t resolve_candidate(const GatherArgs& a, const 
 // One CTA per (unit, head, split); warps stride over candidates; lanes hold
 // DPL dims each (d = lane + 32 * k).  fp32 FMA throughout.
 // kScores: a paged request whose scores are kept for the tokens' weights (an instance of
-// its own: tested for in every one, 16 contexts of 8,192 tokens in fp32 took 1,376 us
-// against 1,067).
+// its own: 16 contexts of 8,192 tokens, 32 / 8 heads of 128 in fp32, 1,055 us; with the test
+// in every one 1,370, as those that keep scores still take).
 
 template <typename T, int DPL, bool kScores>
 __global__ void __launch_bounds__(128) gather_simt_kernel(GatherArgs a) {

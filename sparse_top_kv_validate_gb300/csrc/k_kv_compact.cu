@@ -17,7 +17,7 @@
 // tokens, 8 heads of 128, FP8 pages, 289 us; now 245, 66% of the copy bandwidth.)  Scale bytes and weights are moved by the threads that find the
 // rows, as soon as they have.  Where there are too few (sequence, KV head)s for the device, a
 // cluster of up to 8 larger CTAs shares one, each chunk cut in as many pieces (2 contexts of
-// 65,536 tokens to 16,384, 4 heads of 128, 16-bit elements: 54 us; a cluster of 16, 68).
+// 66,000 and 69,000 tokens to 16,384, 4 heads of 128, 16-bit elements: 54 us; a cluster of 16, 68).
 #include "cluster.cuh"
 #include "weights.h"
 

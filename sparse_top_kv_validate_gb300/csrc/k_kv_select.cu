@@ -21,7 +21,7 @@
 // tokens in 8 heads: 68 us; 512 threads, 72; rows that clusters of four CTAs keep in
 // registers, 178), the longest contexts first (in the order given, 5 us more).  Where there
 // are few rows a cluster of up to 8 CTAs takes one, its histograms, lists and counts
-// shared through distributed shared memory (2 contexts of 131,072 tokens, 4 heads: 29 us).
+// shared through distributed shared memory (2 contexts of 118,000 and 144,000 tokens, 4 heads: 29 us).
 // The list holds tokens, not keys: the few keys come once more from L1 (keys written by the
 // second pass itself, each token's place from an atomic of its own: 83 us).
 #include "cluster.cuh"

@@ -9,11 +9,14 @@
 //   kSums 1  outer tiles of keys, inner tiles of query rows: w of every key.
 // Both times a thread owns an outer row, so that its sum runs along the columns of the
 // score tile that it reads from tensor memory: no reduction between threads, no
-// second operand, no probabilities to be passed on.  8 prompts of 2,048 tokens, 32 / 8 heads
-// of 128: 348 us, 55% of the bf16 peak for both products; an inner tile takes 1,450 to
+// second operand, no probabilities to be passed on.  8 prompts of 299 to 3,338 tokens, 16,384
+// in all, 32 / 8 heads of 128: 348 us, 55% of the bf16 peak for both products (of 2,048
+// tokens each, 267 us in f16, 54%); an inner tile takes 1,450 to
 // 1,750 cycles, of which its MMAs take 1,090 and its exponentials (one per visible pair,
 // query head and form) 1,024: bound by what the lanes that issue the MMAs do besides.
-// The last 32 queries of 8 contexts, 131,072 keys: 112 us, 43 for the statistics (K at 80% of
+// Groups that leave rows of a query tile unfilled mask their columns in every tile: 5 heads to
+// the group, 361 us (masked at a sequence's end alone, 349).
+// The last 32 queries of 8 contexts, 112,700 keys: 111 us, 43 for the statistics (K at 80% of
 // the copy bandwidth) and 65 for the sums, whose items have one inner tile each.
 //
 // A query row is a (token, head of the group): a tile is 128 / g tokens times the g
@@ -53,7 +56,7 @@ constexpr int kThreads = 640;           // 4 service warps, 4 warpgroups
 constexpr int kTile = 128;               // rows of a tile
 constexpr int kSlabBytes = kTile * 128;  // 128 rows x 64 sixteen-bit columns
 constexpr int kMaxSeqs = 1024;           // sequences per launch
-constexpr int kItemCost = 1;             // (8 prompts of 2,048 tokens: 0 385 us, 1 and 2 349, 5 360)
+constexpr int kItemCost = 1;             // (the prompts: 0 385 us, 1 and 2 349, 5 360)
 constexpr int kItems = 3;                // items worked out ahead
 constexpr int kLStages = 3;              // slots of the ring of row statistics
 constexpr float kRaiseLog2 = 8.0f;       // the offset of a row's sum is raised beyond 2^8
@@ -750,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Calls of more sequences than a launch takes: every start is looked at before any weight
-// is written.  B: of the whole call.
+// is written (4 us of 209 for 3,000 sequences).  B: of the whole call.
 __global__ void __launch_bounds__(256) starts_kernel(const __grid_constant__ Params p, int B) {
   bool bad = false;
   for (int b = blockIdx.x * 256 + static_cast<int>(threadIdx.x); b < B; b += static_cast<int>(gridDim.x) * 256)
